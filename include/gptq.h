@@ -411,6 +411,164 @@ int gptq_w4a16_matmul(const uint16_t* x, int64_t batch, const uint32_t* qweight,
                       size_t ws_bytes, void* stream);
 
 /*
+ * W4A16 product with low-rank adapters of many requests -- the product of
+ * gptq_w4a16_matmul ("INT4/INT8 量化推理" sec. 六) plus, for each activation
+ * row, the low-rank update its request was tuned with (no counterpart on the
+ * pages: one packed base layer serves every request):
+ *   y[b] = x[b] Q^T + scaling[a] (x[b] A_a^T) B_a^T,    a = adapter[b]
+ * x: batch x d_in fp16 (original column order; A_a's columns are in that order
+ *    too); y: batch x d_out fp32 out.  qweight, scales, qzeros, perm,
+ *    group_size, d_out, d_in: as gptq_w4a16_gemm (group_size a multiple of 32
+ *    dividing d_in, or -1).
+ * lora_a: n_adapters x rank x d_in fp16; lora_b: n_adapters x d_out x rank fp16
+ *    (the layouts of two torch Linear weights).  Adapters of smaller rank are
+ *    padded with zeros.  lora_scaling: n_adapters fp32.
+ * adapter: batch int32 on the device, 0 .. n_adapters - 1, or -1 (no adapter:
+ *    the packed product alone).  Any other value is recorded in the device
+ *    status (0x201) and handled as -1.  Rows of one request need not be
+ *    adjacent; adjacent rows share the adapter's loads.
+ * rank: a multiple of 8, 8 .. 256.  0 <= batch <= 65535 (0: no-op);
+ *    0 <= n_adapters <= 65536 (0: lora_* may be NULL).
+ * ws: gptq_w4a16_lora_workspace_bytes(batch, d_out, d_in, rank) bytes, not
+ *    shared with a call that may run at the same time.
+ * All sums are fp32; the result does not depend on timing (no atomics on y).
+ */
+size_t gptq_w4a16_lora_workspace_bytes(int64_t batch, int64_t d_out, int64_t d_in, int rank);
+int gptq_w4a16_lora(const uint16_t* x, int64_t batch, const uint32_t* qweight,
+                    const uint16_t* scales, const uint8_t* qzeros, const int32_t* perm,
+                    int64_t d_out, int64_t d_in, int group_size, const uint16_t* lora_a,
+                    const uint16_t* lora_b, const float* lora_scaling, const int32_t* adapter,
+                    int64_t n_adapters, int rank, float* y, void* ws, size_t ws_bytes,
+                    void* stream);
+
+/*
+ * A whole mixture-of-experts layer of packed experts for a few tokens -- the
+ * consumer of what gptq_quantize_layer_batched and gptq_pack_int4 make of an
+ * expert stack ("INT4/INT8 量化推理" sec. 五: top-k routed experts; sec. 六:
+ * weights in 4 bits, activations in fp16):
+ *   p = softmax(logits[t]) over the experts, S = the top_k largest logits
+ *       (equal ones: the lower index), w_e = p_e, or p_e / sum_S p when
+ *       renormalize != 0;
+ *   h_e = silu(G_e x[t]) * (U_e x[t]),   y[t] = sum_{e in S} w_e D_e h_e.
+ * An expert whose logit is -inf or NaN is masked: it takes no part in the
+ * softmax and is never chosen, so a token may use fewer than top_k experts; a
+ * token with none gets y = 0.  A logit of +inf counts as the largest finite
+ * value.
+ * x: tokens x d_model fp16; logits: tokens x n_experts fp32; y: tokens x
+ *    d_model fp32 out.
+ * qweight_in / scales_in / qzeros_in: n_experts packed layers of 2 d_ff x
+ *    d_model, rows 0 .. d_ff - 1 the gate G_e and d_ff .. 2 d_ff - 1 the up
+ *    projection U_e; perm_in: n_experts x d_model int32 or NULL.
+ * qweight_out / scales_out / qzeros_out: n_experts packed layers D_e of d_model
+ *    x d_ff; perm_out: n_experts x d_ff int32 or NULL.
+ * group_size: a multiple of 32 dividing d_model and d_ff, or -1 (one group per
+ *    row).  d_model, d_ff: multiples of 128, 128 .. 32768.
+ * 0 <= tokens <= 64 (0: no-op), 1 <= n_experts <= 256, 1 <= top_k <=
+ * min(8, n_experts).
+ * ws: gptq_w4a16_moe_workspace_bytes(...) bytes, not shared with a call that
+ *    may run at the same time.
+ * h stays in fp32 between the products; all sums are fp32 and the result does
+ * not depend on timing (no atomics on y).
+ */
+size_t gptq_w4a16_moe_workspace_bytes(int64_t tokens, int64_t n_experts, int top_k,
+                                      int64_t d_model, int64_t d_ff);
+int gptq_w4a16_moe(const uint16_t* x, int64_t tokens, const float* logits, int64_t n_experts,
+                   int top_k, int renormalize, const uint32_t* qweight_in,
+                   const uint16_t* scales_in, const uint8_t* qzeros_in, const int32_t* perm_in,
+                   const uint32_t* qweight_out, const uint16_t* scales_out,
+                   const uint8_t* qzeros_out, const int32_t* perm_out, int64_t d_model,
+                   int64_t d_ff, int group_size, float* y, void* ws, size_t ws_bytes,
+                   void* stream);
+
+/*
+ * Appending to a paged 4-bit key / value cache -- "大模型量化实战（上）" (the
+ * KV cache in INT4) with the group quantizer of rtn_quantize ("校准艺术" sec.
+ * 2.1), applied to each new key and value row as it arrives, and the rotary
+ * position rotation on the way.  For token t with slots[t] >= 0:
+ *   q_out[t] = fp16(rot(q[t])),  K slot <- quantize(rot(k[t])),
+ *   V slot <- quantize(v[t]),    slot = page * page_size + row of the page.
+ * rot, on the first rot_dim of the head_dim elements, with c_i, s_i =
+ * cos_sin[p][i], cos_sin[p][rot_dim / 2 + i] at p = positions[t]:
+ *   (a, b) -> (a c_i - b s_i, b c_i + a s_i),
+ *   a, b = elements i and rot_dim / 2 + i (interleaved == 0) or 2 i and 2 i + 1
+ *   (interleaved != 0); every product and sum rounded to fp32.
+ * quantize: for each group of group_size elements of a head the fp16 scale s
+ *   and zero point z of rtn_quantize with bits = 4, codes c = clamp(rne(x / s)
+ *   + z, 0, 15).  An infinite element counts as the largest finite value of
+ *   its sign, a NaN as the smallest.
+ *
+ * The cache (k_codes / v_codes: pages x kv_heads x page_size x head_dim / 8
+ * words; k_params / v_params: pages x kv_heads x page_size x (head_dim /
+ * group_size) x 2 fp16, the pair (s, z)) holds the elements of a row in the
+ * order in which a warp's vector loads hand them to its matrix operands; with
+ * NB = head_dim / 32:
+ *   keys:   word t NB + i (t < 4, i < NB) holds elements 32 i + 8 t .. + 7;
+ *   values: half word h NB + i (h < 8) holds elements 32 i + 4 h .. + 3;
+ * the lowest element in the lowest nibble.
+ *
+ * q: tokens x q_heads x head_dim or NULL (then q_out NULL); k, v: tokens x
+ *    kv_heads x head_dim; all of `dtype` (GPTQ_DTYPE_F32 or GPTQ_DTYPE_F16), a
+ *    token's rows dense, tokens q_stride / k_stride / v_stride elements apart
+ *    (views into one fused projection output; a multiple of 16 bytes).
+ * positions: tokens int32, slots: tokens int64.  slots[t] < 0: the cache is not
+ *    written for that token (padding).  A slot or (with rot_dim > 0) a position
+ *    out of range is recorded in the device status (0x201) and nothing is
+ *    written for that token.  The slots >= 0 of one call must be distinct: a
+ *    slot given twice holds a mix of its tokens (no other slot is affected).
+ * cos_sin: n_positions x rot_dim fp32 (NULL when rot_dim == 0).
+ * k_values, v_values: tokens x kv_heads x head_dim fp16 or NULL (both): the
+ *    values fp16(s (c - z)) that the cache now holds, for attention over the
+ *    new tokens themselves; written for padding tokens too.
+ * head_dim: 64, 128 or 256; group_size: 32, 64, 128 or 256 dividing it, or -1;
+ * rot_dim: a multiple of 16, 0 .. head_dim; 1 <= kv_heads, q_heads <= 1024;
+ * page_size: a power of two, 16 .. 4096.  tokens == 0: no-op.
+ */
+int gptq_kv4_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                    const void* v, int64_t v_stride, int dtype, int64_t tokens, int q_heads,
+                    int kv_heads, int head_dim, const int32_t* positions, const int64_t* slots,
+                    const float* cos_sin, int64_t n_positions, int rot_dim, int interleaved,
+                    int group_size, int64_t pages, int page_size, uint32_t* k_codes,
+                    uint16_t* k_params, uint32_t* v_codes, uint16_t* v_params, uint16_t* q_out,
+                    uint16_t* k_values, uint16_t* v_values, void* stream);
+
+/*
+ * Attention of the last tokens of each sequence over the cache that
+ * gptq_kv4_append fills.  Sequence b has seq_lens[b] keys, the new tokens'
+ * among them, and n = q_start[b + 1] - q_start[b] queries, its last n tokens;
+ * query i sees the keys j <= seq_lens[b] - n + i and, with window > 0, j >
+ * seq_lens[b] - n + i - window:
+ *   out[t][h] = sum_j softmax_j(scale q[t][h] . K[j][h']) V[j][h'],
+ *   h' = h / (q_heads / kv_heads).  A query that sees no key gets 0.
+ * q, out: tokens x q_heads x head_dim fp16.  Rows of out behind q_start[seqs]
+ *    are left as they are.
+ * block_table: seqs x table_width int32, the page of each page_size keys of a
+ *    sequence (entries that no key needs are not read); seq_lens: seqs int32;
+ *    q_start: seqs + 1 int32, non-decreasing, within 0 .. tokens.
+ * max_q_len, max_seq_len: host bounds of n and seq_lens (max_seq_len <=
+ *    table_width * page_size): they size the launch and the workspace.
+ * A sequence whose length or query range breaks these bounds is recorded in
+ * the device status (0x201) and its rows are left as they are; a page outside
+ * 0 .. pages - 1 is recorded and its keys are not seen.
+ * Keys and values enter the products as exact codes; scores, softmax
+ * statistics and sums are fp32, probabilities two fp16 parts (22 bits), out is
+ * rounded once.
+ * head_dim, group_size, page_size and the cache: as gptq_kv4_append; q_heads a
+ * multiple of kv_heads.  seqs == 0 or tokens == 0: no-op.
+ * ws: gptq_kv4_attention_workspace_bytes(...) bytes, not shared with a call
+ *    that may run at the same time.
+ */
+size_t gptq_kv4_attention_workspace_bytes(int64_t seqs, int q_heads, int kv_heads, int head_dim,
+                                          int64_t max_q_len, int64_t max_seq_len);
+int gptq_kv4_attention(const uint16_t* q, int64_t tokens, int64_t seqs, int q_heads,
+                       int kv_heads, int head_dim, const uint32_t* k_codes,
+                       const uint16_t* k_params, const uint32_t* v_codes,
+                       const uint16_t* v_params, int64_t pages, int page_size, int group_size,
+                       const int32_t* block_table, int64_t table_width, const int32_t* seq_lens,
+                       const int32_t* q_start, float scale, int64_t window, int64_t max_q_len,
+                       int64_t max_seq_len, uint16_t* out, void* ws, size_t ws_bytes,
+                       void* stream);
+
+/*
  * Round-to-nearest baseline -- "大模型量化实战（上）" (RTN: every weight
  * rounded on its own) with the min-max group quantizer of "校准艺术" sec. 2.1:
  * the same group parameters and codes as gptq_quantize_layer, taken on the
@@ -487,9 +645,11 @@ int gptq_debug_gemm_nt(const float* A, int64_t lda, const float* B, int64_t ldb,
  * bracket itself with two CUDA events on its stream; gptq_debug_kernel_times
  * waits for the recorded events, returns per kind the summed milliseconds
  * (ms[k]) and the number of timed launch sites (spans[k]), and forgets the
- * records.  Kinds, in order (n_kinds >= 16): hessian, gather, finalize,
+ * records.  Kinds, in order (n_kinds >= 16; those beyond n_kinds are left
+ * out): hessian, gather, finalize,
  * factorization, init_work, split_u, static_params, sweep, update_near,
- * update_far, pack, unpack, rtn, w4a16, probe, awq (names from
+ * update_far, pack, unpack, rtn, w4a16, probe, awq, w4a16_lora, w4a16_moe,
+ * kv4_append, kv4_attention (names from
  * gptq_debug_kernel_kind_name).  Use it on eager launches only, never while
  * a stream is being captured; it creates two CUDA events per launch site
  * while enabled.  Disabled (the default) it costs one flag test per launch.

@@ -108,7 +108,7 @@ extern "C" int gptq_debug_kernel_timing(int enable)
 extern "C" int gptq_debug_kernel_times(double* ms, int64_t* spans, int n_kinds)
 {
     using namespace gptq;
-    if (!ms || !spans || n_kinds < kKKinds) return GPTQ_ERR_INVALID_ARG;
+    if (!ms || !spans || n_kinds < 16) return GPTQ_ERR_INVALID_ARG;
     for (int k = 0; k < n_kinds; ++k) { ms[k] = 0.0; spans[k] = 0; }
     std::vector<TimedSpan> take;
     {
@@ -136,7 +136,7 @@ extern "C" const char* gptq_debug_kernel_kind_name(int kind)
     static const char* names[gptq::kKKinds] = {
         "hessian", "gather", "finalize", "factorization", "init_work", "split_u",
         "static_params", "sweep", "update_near", "update_far", "pack", "unpack", "rtn",
-        "w4a16", "probe", "awq"};
+        "w4a16", "probe", "awq", "w4a16_lora", "w4a16_moe", "kv4_append", "kv4_attention"};
     return (kind >= 0 && kind < gptq::kKKinds) ? names[kind] : "unknown";
 }
 

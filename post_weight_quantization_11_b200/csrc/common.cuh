@@ -18,6 +18,8 @@ inline cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+inline bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
 // Process-wide count of kernel launches issued by the library (diagnostics).
 void count_launches(int n = 1);
 
@@ -41,7 +43,7 @@ int persistent_ctas(int kind);
 enum KernelKind : int {
     kKHessian = 0, kKGather, kKFinalize, kKFactor, kKInitWork, kKSplitU, kKStaticParams,
     kKSweep, kKUpdateNear, kKUpdateFar, kKPack, kKUnpack, kKRtn, kKW4A16, kKProbe, kKAwq,
-    kKKinds
+    kKLora, kKMoe, kKKvAppend, kKKvAttention, kKKinds
 };
 
 // While timing is enabled, the launches issued in this object's lifetime are

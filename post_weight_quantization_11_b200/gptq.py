@@ -37,7 +37,9 @@ EXPORTED = ("gptq_status_string", "gptq_abi_version", "gptq_debug_launch_count",
             "gptq_pack_int4", "gptq_pack_bits", "gptq_unpack_bits",
             "gptq_channel_abs_sum", "gptq_awq_workspace_bytes", "gptq_awq_search",
             "gptq_unpack_int4", "gptq_w4a16_gemm", "gptq_w4a16_matmul_workspace_bytes",
-            "gptq_w4a16_matmul", "rtn_quantize", "gptq_debug_gemm_nt",
+            "gptq_w4a16_matmul", "gptq_w4a16_lora_workspace_bytes", "gptq_w4a16_lora",
+            "gptq_w4a16_moe_workspace_bytes", "gptq_w4a16_moe", "gptq_kv4_append",
+            "gptq_kv4_attention_workspace_bytes", "gptq_kv4_attention", "rtn_quantize", "gptq_debug_gemm_nt",
             "gptq_debug_chol_task_order", "gptq_debug_div_rn", "gptq_debug_bounded_wait",
             "gptq_debug_kernel_timing", "gptq_debug_kernel_times", "gptq_debug_kernel_kind_name")
 
@@ -96,6 +98,17 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "gptq_w4a16_gemm": ([P, I64, P, P, P, P, I64, I64, I32, P, P], I32),
         "gptq_w4a16_matmul_workspace_bytes": ([I64, I64], SZ),
         "gptq_w4a16_matmul": ([P, I64, P, P, P, P, I64, I64, I32, P, P, SZ, P], I32),
+        "gptq_w4a16_lora_workspace_bytes": ([I64, I64, I64, I32], SZ),
+        "gptq_w4a16_lora": ([P, I64, P, P, P, P, I64, I64, I32, P, P, P, P, I64, I32, P, P, SZ, P],
+                            I32),
+        "gptq_w4a16_moe_workspace_bytes": ([I64, I64, I32, I64, I64], SZ),
+        "gptq_w4a16_moe": ([P, I64, P, I64, I32, I32, P, P, P, P, P, P, P, P, I64, I64, I32, P, P,
+                            SZ, P], I32),
+        "gptq_kv4_append": ([P, I64, P, I64, P, I64, I32, I64, I32, I32, I32, P, P, P, I64, I32,
+                             I32, I32, I64, I32, P, P, P, P, P, P, P, P], I32),
+        "gptq_kv4_attention_workspace_bytes": ([I64, I32, I32, I32, I64, I64], SZ),
+        "gptq_kv4_attention": ([P, I64, I64, I32, I32, I32, P, P, P, P, I64, I32, I32, P, I64, P,
+                                P, F32, I64, I64, I64, P, P, SZ, P], I32),
         "gptq_debug_gemm_nt": ([P, I64, P, I64, P, I64, I64, I64, I64, F32, F32, I32, P], I32),
         "gptq_debug_chol_task_order": ([I64, P, I64], I64),
         "gptq_debug_div_rn": ([P, P, I64, P], I32),
@@ -170,7 +183,7 @@ def gptq_set_max_ctas(kind: int, max_ctas: int) -> None:
     _check("gptq_set_max_ctas", load_library().gptq_set_max_ctas(int(kind), int(max_ctas)))
 
 
-N_KERNEL_KINDS = 16
+N_KERNEL_KINDS = 20
 
 
 def gptq_debug_kernel_timing(enable: bool) -> None:
@@ -562,6 +575,276 @@ def gptq_w4a16_matmul(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tens
                                             _ptr(perm), m, d, int(group_size), _ptr(y), _ptr(ws),
                                             ws.numel() * ws.element_size(), _stream(x)))
     return y
+
+
+def _same_device(dev, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} must be on {dev}, got {t.device}")
+
+
+def _call(fn: str, dev, *args):
+    """The entry point on the device's current stream (made current for the call)."""
+    f = getattr(load_library(), fn)
+    if dev.index == torch.cuda.current_device():
+        _check(fn, f(*args, torch.cuda.current_stream(dev).cuda_stream))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn, f(*args, torch.cuda.current_stream(dev).cuda_stream))
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _out(t, name: str, shape, dtype, dev):
+    """The caller's output, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _need(t, name, dtype)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def _workspace(ws, nbytes: int, dev):
+    if ws is None:
+        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+    _need(ws, "ws")
+    return ws
+
+
+def _packed_layer(qweight, scales, qzeros, perm, lead, m, d, group_size, tag=""):
+    """Checks a packed layer (or a stack of them, lead = (E,)) of m x d."""
+    _need(qweight, "qweight" + tag, torch.int32)
+    _need(scales, "scales" + tag, torch.float16)
+    _need(qzeros, "qzeros" + tag, torch.uint8)
+    G = 1 if group_size == -1 else d // max(1, group_size)
+    for t, name, shape in ((qweight, "qweight", (m, d // 8)), (scales, "scales", (m, G)),
+                           (qzeros, "qzeros", (m, (G + 1) // 2))):
+        if tuple(t.shape) != (*lead, *shape):
+            raise ValueError(f"{name}{tag} must be {(*lead, *shape)}, got {tuple(t.shape)}")
+    if perm is not None:
+        _need(perm, "perm" + tag, torch.int32)
+        if tuple(perm.shape) != (*lead, d):
+            raise ValueError(f"perm{tag} must be {(*lead, d)}, got {tuple(perm.shape)}")
+
+
+def gptq_w4a16_lora_workspace_bytes(batch: int, d_out: int, d_in: int, rank: int) -> int:
+    return int(load_library().gptq_w4a16_lora_workspace_bytes(int(batch), int(d_out), int(d_in),
+                                                              int(rank)))
+
+
+def gptq_w4a16_lora(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor,
+                    qzeros: torch.Tensor, lora_a: torch.Tensor, lora_b: torch.Tensor,
+                    adapter: torch.Tensor, lora_scaling: torch.Tensor, group_size: int = 128,
+                    perm=None, y=None, ws=None) -> torch.Tensor:
+    """y = x Q^T plus, for row b with a = adapter[b] >= 0, lora_scaling[a] (x[b]
+    A_a^T) B_a^T (batch x d_out fp32).  x: batch x d_in fp16; lora_a: adapters x
+    rank x d_in, lora_b: adapters x d_out x rank fp16; adapter: batch int32
+    (-1: none); lora_scaling: adapters fp32."""
+    _need(x, "x", torch.float16)
+    _need(lora_a, "lora_a", torch.float16)
+    _need(lora_b, "lora_b", torch.float16)
+    _need(adapter, "adapter", torch.int32)
+    _need(lora_scaling, "lora_scaling", torch.float32)
+    b, d = x.shape
+    m = qweight.shape[0]
+    n, r = lora_a.shape[0], lora_a.shape[1]
+    _packed_layer(qweight, scales, qzeros, perm, (), m, d, group_size)
+    if lora_a.shape != (n, r, d) or lora_b.shape != (n, m, r):
+        raise ValueError("lora_a must be adapters x rank x d_in, lora_b adapters x d_out x rank")
+    if adapter.shape != (b,) or lora_scaling.shape != (n,):
+        raise ValueError("adapter must have one entry per row of x, lora_scaling one per adapter")
+    dev = x.device
+    y = _out(y, "y", (b, m), torch.float32, dev)
+    ws = _workspace(ws, gptq_w4a16_lora_workspace_bytes(b, m, d, r), dev)
+    _same_device(dev, qweight=qweight, scales=scales, qzeros=qzeros, perm=perm, lora_a=lora_a,
+                 lora_b=lora_b, adapter=adapter, lora_scaling=lora_scaling, y=y, ws=ws)
+    _call("gptq_w4a16_lora", dev, _addr(x), b, _addr(qweight), _addr(scales), _addr(qzeros),
+          _addr(perm), m, d, int(group_size), _addr(lora_a), _addr(lora_b), _addr(lora_scaling),
+          _addr(adapter), n, r, _addr(y), _addr(ws), ws.numel() * ws.element_size())
+    return y
+
+
+def gptq_w4a16_moe_workspace_bytes(tokens: int, n_experts: int, top_k: int, d_model: int,
+                                   d_ff: int) -> int:
+    return int(load_library().gptq_w4a16_moe_workspace_bytes(int(tokens), int(n_experts),
+                                                             int(top_k), int(d_model), int(d_ff)))
+
+
+def gptq_w4a16_moe(x: torch.Tensor, logits: torch.Tensor, qweight_in: torch.Tensor,
+                   scales_in: torch.Tensor, qzeros_in: torch.Tensor, qweight_out: torch.Tensor,
+                   scales_out: torch.Tensor, qzeros_out: torch.Tensor, top_k: int,
+                   group_size: int = 128, renormalize: bool = True, perm_in=None, perm_out=None,
+                   y=None, ws=None) -> torch.Tensor:
+    """A mixture-of-experts layer of packed experts for up to 64 tokens: y =
+    sum over the top_k experts of w_e D_e (silu(G_e x) * (U_e x)) (tokens x
+    d_model fp32).  x: tokens x d_model fp16; logits: tokens x experts fp32
+    (-inf or NaN: masked); the packed stacks: E x 2 d_ff x d_model (gate rows,
+    then up rows) and E x d_model x d_ff, as quantize_moe_from_inputs packs
+    them; perm_in: E x d_model, perm_out: E x d_ff."""
+    _need(x, "x", torch.float16)
+    _need(logits, "logits", torch.float32)
+    T, d = x.shape
+    E = logits.shape[1]
+    f = qweight_out.shape[-1] * 8
+    if logits.shape != (T, E):
+        raise ValueError("logits must be tokens x experts")
+    _packed_layer(qweight_in, scales_in, qzeros_in, perm_in, (E,), 2 * f, d, group_size, "_in")
+    _packed_layer(qweight_out, scales_out, qzeros_out, perm_out, (E,), d, f, group_size, "_out")
+    dev = x.device
+    y = _out(y, "y", (T, d), torch.float32, dev)
+    ws = _workspace(ws, gptq_w4a16_moe_workspace_bytes(T, E, top_k, d, f), dev)
+    _same_device(dev, logits=logits, qweight_in=qweight_in, scales_in=scales_in,
+                 qzeros_in=qzeros_in, perm_in=perm_in, qweight_out=qweight_out,
+                 scales_out=scales_out, qzeros_out=qzeros_out, perm_out=perm_out, y=y, ws=ws)
+    _call("gptq_w4a16_moe", dev, _addr(x), T, _addr(logits), E, int(top_k), int(bool(renormalize)),
+          _addr(qweight_in), _addr(scales_in), _addr(qzeros_in), _addr(perm_in),
+          _addr(qweight_out), _addr(scales_out), _addr(qzeros_out), _addr(perm_out), d, f,
+          int(group_size), _addr(y), _addr(ws), ws.numel() * ws.element_size())
+    return y
+
+
+class KV4Cache:
+    """A paged 4-bit key / value cache: codes pages x kv_heads x page_size x
+    head_dim / 8 int32 and parameters pages x kv_heads x page_size x groups x 2
+    fp16 (scale, zero point) for keys and values.  The order of a row's
+    elements in its words is that of gptq_kv4_append in include/gptq.h."""
+
+    def __init__(self, k_codes, k_params, v_codes, v_params):
+        for t, name, dt in ((k_codes, "k_codes", torch.int32), (k_params, "k_params", torch.float16),
+                            (v_codes, "v_codes", torch.int32), (v_params, "v_params", torch.float16)):
+            _need(t, name, dt)
+        if k_codes.dim() != 4 or k_params.dim() != 5 or k_params.shape[4] != 2:
+            raise ValueError("codes must be pages x kv_heads x page_size x head_dim / 8, params "
+                             "pages x kv_heads x page_size x groups x 2")
+        if k_codes.shape[:3] != k_params.shape[:3]:
+            raise ValueError("codes and params must have the same pages, heads and page size")
+        if v_codes.shape != k_codes.shape or v_params.shape != k_params.shape:
+            raise ValueError("keys and values must have the same shapes")
+        self.k_codes, self.k_params = k_codes, k_params
+        self.v_codes, self.v_params = v_codes, v_params
+        self.pages, self.kv_heads, self.page_size = k_codes.shape[:3]
+        self.head_dim = k_codes.shape[3] * 8
+        groups = k_params.shape[3]
+        if groups < 1 or self.head_dim % groups != 0:
+            raise ValueError("the groups must divide head_dim")
+        self.group_size = self.head_dim // groups
+        self.device = k_codes.device
+        _same_device(self.device, k_params=k_params, v_codes=v_codes, v_params=v_params)
+
+    @classmethod
+    def empty(cls, pages: int, kv_heads: int, page_size: int, head_dim: int,
+              group_size: int = -1, device="cuda"):
+        """A cache of zeros."""
+        g = head_dim if group_size == -1 else group_size
+        codes = lambda: torch.zeros(pages, kv_heads, page_size, head_dim // 8,      # noqa: E731
+                                    dtype=torch.int32, device=device)
+        params = lambda: torch.zeros(pages, kv_heads, page_size, head_dim // g, 2,  # noqa: E731
+                                     dtype=torch.float16, device=device)
+        return cls(codes(), params(), codes(), params())
+
+
+def _rows(t, name: str, tokens: int, heads, head_dim: int, dtype):
+    """A tokens x heads x head_dim tensor or view with dense rows: its token stride."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[0] != tokens or t.shape[2] != head_dim or \
+            (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be tokens x heads x head_dim, got {tuple(t.shape)}")
+    if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != head_dim)):
+        raise ValueError(f"{name}: the heads of a token must be dense")
+    return t.stride(0) if tokens > 1 else t.shape[1] * head_dim
+
+
+def gptq_kv4_append(k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
+                    slots: torch.Tensor, cos_sin, cache: KV4Cache, q=None,
+                    interleaved: bool = False, values: bool = False, q_out=None):
+    """Rotates q and k (tokens x heads x head_dim, fp16 or fp32, views into one
+    projection output allowed) at positions (int32), quantizes k and v and
+    writes them to slots (int64, page * page_size + row; < 0: not written) of
+    the cache.  cos_sin: positions x rot_dim fp32 (cosines, then sines) or None.
+    Returns (q_out fp16 or None, k_values, v_values): with values=True the fp16
+    keys and values that the cache now holds, else None."""
+    dt = _wdtype(k)
+    if k.dim() != 3:
+        raise ValueError("k must be tokens x kv_heads x head_dim")
+    T, D, dev = k.shape[0], cache.head_dim, k.device
+    ks = _rows(k, "k", T, cache.kv_heads, D, k.dtype)
+    vs = _rows(v, "v", T, cache.kv_heads, D, k.dtype)
+    qs, hq = 0, 0
+    if q is not None:
+        qs = _rows(q, "q", T, None, D, k.dtype)
+        hq = q.shape[1]
+        q_out = _out(q_out, "q_out", (T, hq, D), torch.float16, dev)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _need(slots, "slots", torch.int64)
+    rot, n_pos = 0, 0
+    if cos_sin is not None:
+        _need(cos_sin, "cos_sin", torch.float32)
+        _need(positions, "positions", torch.int32)
+        n_pos, rot = cos_sin.shape
+        if positions.shape != (T,):
+            raise ValueError("positions must have one entry per token")
+    if slots.shape != (T,):
+        raise ValueError("slots must have one entry per token")
+    kv = torch.empty(2, T, cache.kv_heads, D, dtype=torch.float16, device=dev) if values else None
+    kval, vval = (kv[0], kv[1]) if values else (None, None)
+    _same_device(dev, v=v, q=q, slots=slots, positions=positions, cos_sin=cos_sin,
+                 cache=cache.k_codes, q_out=q_out)
+    _call("gptq_kv4_append", dev, _addr(q), qs, _addr(k), ks, _addr(v), vs, dt, T, hq,
+          cache.kv_heads, D, _addr(positions), _addr(slots), _addr(cos_sin), n_pos, rot,
+          int(bool(interleaved)), cache.group_size, cache.pages, cache.page_size,
+          _addr(cache.k_codes), _addr(cache.k_params), _addr(cache.v_codes),
+          _addr(cache.v_params), _addr(q_out), _addr(kval), _addr(vval))
+    return q_out, kval, vval
+
+
+def gptq_kv4_attention_workspace_bytes(seqs: int, q_heads: int, kv_heads: int, head_dim: int,
+                                       max_q_len: int, max_seq_len: int) -> int:
+    return int(load_library().gptq_kv4_attention_workspace_bytes(
+        int(seqs), int(q_heads), int(kv_heads), int(head_dim), int(max_q_len), int(max_seq_len)))
+
+
+def gptq_kv4_attention(q: torch.Tensor, cache: KV4Cache, block_table: torch.Tensor,
+                       seq_lens: torch.Tensor, q_start: torch.Tensor, scale: float,
+                       window: int = 0, max_q_len: int = 1, max_seq_len=None, out=None,
+                       ws=None) -> torch.Tensor:
+    """Attention of each sequence's last tokens (rows q_start[b] .. q_start[b+1]
+    of q, tokens x q_heads x head_dim fp16) over its seq_lens[b] cached keys,
+    causal, optionally within a window.  block_table: seqs x width int32 pages.
+    max_q_len, max_seq_len (default: the table's width in keys) bound the
+    queries and keys of a sequence.  Returns out (as q; rows behind the last
+    sequence are not written)."""
+    _need(q, "q", torch.float16)
+    _need(block_table, "block_table", torch.int32)
+    _need(seq_lens, "seq_lens", torch.int32)
+    _need(q_start, "q_start", torch.int32)
+    if q.dim() != 3 or q.shape[2] != cache.head_dim:
+        raise ValueError("q must be tokens x q_heads x head_dim")
+    T, hq, D = q.shape
+    B = seq_lens.shape[0]
+    if block_table.dim() != 2 or block_table.shape[0] != B or q_start.shape != (B + 1,):
+        raise ValueError("block_table must be seqs x width, q_start seqs + 1")
+    width = block_table.shape[1]
+    if max_seq_len is None:
+        max_seq_len = width * cache.page_size
+    dev = q.device
+    out = _out(out, "out", (T, hq, D), torch.float16, dev)
+    ws = _workspace(ws, gptq_kv4_attention_workspace_bytes(B, hq, cache.kv_heads, D, max_q_len,
+                                                           max_seq_len), dev)
+    _same_device(dev, cache=cache.k_codes, block_table=block_table, seq_lens=seq_lens,
+                 q_start=q_start, out=out, ws=ws)
+    _call("gptq_kv4_attention", dev, _addr(q), T, B, hq, cache.kv_heads, D, _addr(cache.k_codes),
+          _addr(cache.k_params), _addr(cache.v_codes), _addr(cache.v_params), cache.pages,
+          cache.page_size, cache.group_size, _addr(block_table), width, _addr(seq_lens),
+          _addr(q_start), float(scale), int(window), int(max_q_len), int(max_seq_len), _addr(out),
+          _addr(ws), ws.numel() * ws.element_size())
+    return out
 
 
 def gptq_unpack_int4(qweight: torch.Tensor, qzeros: torch.Tensor, d_in: int, n_groups: int):
