@@ -4,33 +4,35 @@
 //
 //   p = softmax(logits), S = top_k of it,  y = sum_S w_e D_e (silu(G_e x) * U_e x)
 //
-// Three kernels: the routes, h (one warp per row of an expert and token), y.
+// Three kernels: routes and h, the second product over slices of its columns,
+// and the joined y.
 #include <cfloat>
 #include <cmath>
 
 #include "common.cuh"
 #include "tc_common.cuh"
+#include "w4_rows.cuh"
 
 namespace gptq {
 
 constexpr int kMoeTokens = 64, kMoeExperts = 256, kMoeTopK = 8;
+constexpr int kMoePairs = kMoeTokens * kMoeTopK;
+
+struct MoeRoutes;
 
 struct MoeParams {
     const __half* x;
     const float* logits;
-    const uint32_t* qwi;
-    const __half* sci;
-    const uint8_t* qzi;
     const int32_t* pi;
-    const uint32_t* qwo;
-    const __half* sco;
-    const uint8_t* qzo;
     const int32_t* po;
-    int64_t d, f, gi, go;
+    int64_t d, f;
     int T, E, k, renorm;
-    int* ids;          // T x k, -1: none
-    float* w;          // T x k
-    float* h;          // T k x f
+    W4Layer in, out;
+    int chunk;                             // tokens of an expert that are staged together
+    int slice, slices;                     // steps of a slice of the second product
+    MoeRoutes* routes;
+    float* h;                              // T k x f
+    float* part;                           // slices x T k x d
     float* y;
 };
 
@@ -83,67 +85,229 @@ __device__ __forceinline__ void moe_route(const float* logits, int E, int k, int
     }
 }
 
-__global__ void __launch_bounds__(256) moe_route_kernel(const MoeParams p)
-{
-    for (int t = threadIdx.x >> 5; t < p.T; t += 8)
-        moe_route(p.logits + int64_t(t) * p.E, p.E, p.k, p.renorm, p.ids + t * p.k, p.w + t * p.k);
-}
+// What the second kernel reads of the routes: chunks of up to p.chunk pairs of
+// one expert, in expert order
+struct MoeRoutes {
+    int chunks;
+    int expert[kMoePairs];
+    int start[kMoePairs];                  // in list
+    int n[kMoePairs];
+    int list[kMoePairs];                   // pairs (t k + j), expert by expert
+    int id[kMoePairs];                     // expert of each pair, -1: none
+    float w[kMoePairs];
+};
 
-// One warp: the product of row r of a packed layer with x (through perm)
-template <typename T>
-__device__ __forceinline__ float row_dot(const uint32_t* qw, const __half* sc, const uint8_t* qz,
-                                         const int32_t* perm, int64_t r, int64_t d, int64_t g,
-                                         const T* x)
+// All threads: routes of all tokens and the chunks, in shared memory
+__device__ __forceinline__ void moe_routes(const MoeParams& p, MoeRoutes& r, int* cnt, int* off,
+                                           int* coff)
 {
-    const int lane = threadIdx.x & 31;
-    const int64_t G = d / g;
-    float s = 0.f;
-    for (int64_t k = lane; k < d; k += 32) {
-        const int64_t src = perm ? perm[k] : k;
-        if (src < 0 || src >= d) {
-            atomicCAS(&g_device_status, 0, kErrIndex);
-            continue;
+    const int tid = threadIdx.x, lane = tid & 31, pairs = p.T * p.k;
+    for (int e = tid; e < p.E; e += blockDim.x) cnt[e] = 0;
+    for (int t = tid >> 5; t < p.T; t += blockDim.x >> 5)
+        moe_route(p.logits + int64_t(t) * p.E, p.E, p.k, p.renorm, r.id + t * p.k, r.w + t * p.k);
+    __syncthreads();
+    int pos[kMoePairs / 32];                               // of the first warp: place in the expert's list
+    if (tid < 32) {                                        // in pair order: every CTA has the same lists
+#pragma unroll
+        for (int u = 0; u < kMoePairs / 32; ++u) {
+            const int i = u * 32 + lane;
+            const int id = i < pairs ? r.id[i] : -1;
+            if (u * 32 >= pairs) break;
+            const uint32_t same = __match_any_sync(0xffffffffu, id);
+            const int before = __popc(same & ((1u << lane) - 1u));
+            pos[u] = id >= 0 ? cnt[id] + before : -1;
+            __syncwarp();
+            if (id >= 0 && before == 0) cnt[id] += __popc(same);
+            __syncwarp();
         }
-        const int64_t gi = k / g;
-        const int c = (qw[r * (d / 8) + k / 8] >> (4 * (k % 8))) & 15;
-        const int z = (qz[r * ((G + 1) / 2) + gi / 2] >> (4 * (gi & 1))) & 15;
-        s += float(x[src]) * (__half2float(sc[r * G + gi]) * float(c - z));
     }
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    return s;
+    __syncthreads();
+    if (tid < 32) {                                        // prefix sums over the experts
+        const int per = (p.E + 31) / 32, e0 = lane * per, e1 = min(p.E, e0 + per);
+        int a = 0, c = 0;
+        for (int e = e0; e < e1; ++e) { a += cnt[e]; c += (cnt[e] + p.chunk - 1) / p.chunk; }
+        int pa = a, pc = c;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int va = __shfl_up_sync(0xffffffffu, pa, o), vc = __shfl_up_sync(0xffffffffu, pc, o);
+            if (lane >= o) { pa += va; pc += vc; }
+        }
+        if (lane == 31) r.chunks = pc;
+        pa -= a;
+        pc -= c;
+        for (int e = e0; e < e1; ++e) {
+            off[e] = pa;
+            coff[e] = pc;
+            pa += cnt[e];
+            pc += (cnt[e] + p.chunk - 1) / p.chunk;
+        }
+    }
+    __syncthreads();
+    if (tid < 32) {
+#pragma unroll
+        for (int u = 0; u < kMoePairs / 32; ++u) {
+            const int i = u * 32 + lane;
+            if (i < pairs && pos[u] >= 0) r.list[off[r.id[i]] + pos[u]] = i;
+        }
+    }
+    for (int e = tid; e < p.E; e += blockDim.x)
+        for (int c = 0, left = cnt[e]; left > 0; ++c, left -= p.chunk) {
+            r.expert[coff[e] + c] = e;
+            r.start[coff[e] + c] = off[e] + c * p.chunk;
+            r.n[coff[e] + c] = min(left, p.chunk);
+        }
+    __syncthreads();
 }
 
-__global__ void __launch_bounds__(256) moe_in_simple_kernel(const MoeParams p)
+// h = silu(G x) (U x) of every pair.  A row tile is 8 gate rows and the same 8
+// up rows, so that a lane holds both of an element of h.  The CTAs share the
+// row tiles of all chunks evenly; a CTA stages a chunk's tokens once.
+template <bool WIDE>
+__global__ void __launch_bounds__(W4_THREADS, 2) moe_in_kernel(const MoeParams p)
 {
-    const int64_t r = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    const int pair = blockIdx.y, e = p.ids[pair];
-    if (e < 0 || r >= p.f) return;
-    const int64_t m = 2 * p.f, G = p.d / p.gi;
-    const __half* x = p.x + int64_t(pair / p.k) * p.d;
-    const int32_t* perm = p.pi ? p.pi + e * p.d : nullptr;
-    const uint32_t* qw = p.qwi + e * m * (p.d / 8);
-    const __half* sc = p.sci + e * m * G;
-    const uint8_t* qz = p.qzi + e * m * ((G + 1) / 2);
-    const float gate = row_dot(qw, sc, qz, perm, r, p.d, p.gi, x);
-    const float up = row_dot(qw, sc, qz, perm, r + p.f, p.d, p.gi, x);
-    if ((threadIdx.x & 31) == 0) p.h[pair * p.f + r] = gate / (1.f + expf(-gate)) * up;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ MoeRoutes r;
+    __shared__ int cnt[kMoeExperts], off[kMoeExperts], coff[kMoeExperts];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int kw = warp % W4_KW, rw = warp / W4_KW, g = lane >> 2, t = lane & 3;
+    const int steps = int(p.d / W4_STEP), groups = int(p.f / (8 * W4_RW));
+    uint4* x = reinterpret_cast<uint4*>(smem);
+    float* xs = reinterpret_cast<float*>(smem + w4_x_bytes(steps, p.chunk, false));
+    float* red = xs + w4_xs_bytes(steps, 1, WIDE) / 4;
+    moe_routes(p, r, cnt, off, coff);
+    if (blockIdx.x == 0) {                                 // for the second kernel
+        const int* src = reinterpret_cast<const int*>(&r);
+        for (int i = threadIdx.x; i < int(sizeof(MoeRoutes) / 4); i += blockDim.x)
+            reinterpret_cast<int*>(p.routes)[i] = src[i];
+    }
+    const int64_t units = int64_t(r.chunks) * groups;
+    int64_t u = units * blockIdx.x / gridDim.x;
+    const int64_t u1 = units * (blockIdx.x + 1) / gridDim.x;
+    while (u < u1) {
+        const int c = int(u / groups), g0 = int(u - int64_t(c) * groups);
+        const int g1 = int(min(int64_t(groups), g0 + (u1 - u)));
+        const int e = r.expert[c], cols = r.n[c];
+        const int* list = r.list + r.start[c];
+        const int64_t row0 = int64_t(e) * 2 * p.f;
+        const W4Stage st{x, xs, cols, 0};
+        w4_sweep<1, WIDE, false, true>(
+            p.in, st, red, g0, g1, 0, steps,
+            [&](int grp, int w) {
+                const int64_t ra = row0 + (int64_t(grp) * W4_RW + w) * 8 + g;
+                return w4_rows(p.in, ra, ra + p.f);
+            },
+            [&]() {
+                w4_stage_half<1, WIDE>(
+                    x, xs, [&](int n) { return p.x + int64_t(list[n] / p.k) * p.d; },
+                    p.pi ? p.pi + e * p.d : nullptr, 0, steps, cols, int(p.d));
+                __syncthreads();
+            },
+            [&](int grp, float (&v)[1][2]) {
+                const int n = 2 * t + kw;
+                if (n < cols) {
+                    const float gate = v[0][0], up = v[0][1];
+                    p.h[int64_t(list[n]) * p.f + (int64_t(grp) * W4_RW + rw) * 8 + g] =
+                        gate / (1.f + expf(-gate)) * up;
+                }
+            });
+        u += g1 - g0;
+    }
 }
 
-__global__ void __launch_bounds__(256) moe_out_simple_kernel(const MoeParams p)
+// part[slice][pair] = D h over a slice of the columns
+template <bool WIDE>
+__global__ void __launch_bounds__(W4_THREADS, 2) moe_out_kernel(const MoeParams p)
 {
-    const int64_t r = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ MoeRoutes r;
+    __shared__ float undo[8];
+    __shared__ uint32_t top[8];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int kw = warp % W4_KW, rw = warp / W4_KW, g = lane >> 2, t = lane & 3;
+    const int groups = int(p.d / (16 * W4_RW)), nsteps = int(p.f / W4_STEP);
+    uint4* x = reinterpret_cast<uint4*>(smem);
+    float* xs = reinterpret_cast<float*>(smem + w4_x_bytes(p.slice, p.chunk, true));
+    float* red = xs + w4_xs_bytes(p.slice, 1, WIDE) / 4;
+    pdl_wait();
+    for (int i = threadIdx.x; i < int(sizeof(MoeRoutes) / 4); i += blockDim.x)
+        reinterpret_cast<int*>(&r)[i] = reinterpret_cast<const int*>(p.routes)[i];
+    __syncthreads();
+    const int64_t units = int64_t(r.chunks) * p.slices * groups;
+    int64_t u = units * blockIdx.x / gridDim.x;
+    const int64_t u1 = units * (blockIdx.x + 1) / gridDim.x;
+    while (u < u1) {
+        const int cs = int(u / groups), g0 = int(u - int64_t(cs) * groups);
+        const int g1 = int(min(int64_t(groups), g0 + (u1 - u)));
+        const int c = cs / p.slices, sl = cs - c * p.slices;
+        const int e = r.expert[c], cols = r.n[c];
+        const int k0 = sl * p.slice, steps = min(p.slice, nsteps - k0);
+        const int* list = r.list + r.start[c];
+        const int64_t row0 = int64_t(e) * p.d;
+        const W4Stage st{x, xs, cols, steps * 16 * cols};
+        w4_sweep<1, WIDE, true, false>(
+            p.out, st, red, g0, g1, k0, steps,
+            [&](int grp, int w) {
+                const int64_t ra = row0 + (int64_t(grp) * W4_RW + w) * 16 + g;
+                return w4_rows(p.out, ra, ra + 8);
+            },
+            [&]() {
+                w4_stage_split<1, WIDE>(
+                    x, xs, undo, top, [&](int n) { return p.h + int64_t(list[n]) * p.f; },
+                    p.po ? p.po + e * p.f : nullptr, k0 * W4_STEP, steps, cols, int(p.f));
+                __syncthreads();
+            },
+            [&](int grp, float (&v)[1]) {
+                const int n = 2 * t + (kw & 1);
+                if (n < cols)
+                    p.part[(int64_t(sl) * p.T * p.k + list[n]) * p.d +
+                           (int64_t(grp) * W4_RW + rw) * 16 + g + 8 * (kw >> 1)] = v[0] * undo[n];
+            });
+        u += g1 - g0;
+    }
+}
+
+// y[t] = sum over the token's experts of w (sum over the slices of part)
+__global__ void __launch_bounds__(256) moe_join_kernel(const MoeParams p)
+{
+    pdl_wait();
+    const int64_t r = int64_t(blockIdx.x) * 256 + threadIdx.x;
     const int t = blockIdx.y;
     if (r >= p.d) return;
-    const int64_t G = p.f / p.go;
-    float s = 0.f;
+    float y = 0.f;
     for (int j = 0; j < p.k; ++j) {
-        const int pair = t * p.k + j, e = p.ids[pair];
-        if (e < 0) continue;
-        s += p.w[pair] * row_dot(p.qwo + e * p.d * (p.f / 8), p.sco + e * p.d * G,
-                                 p.qzo + e * p.d * ((G + 1) / 2), p.po ? p.po + e * p.f : nullptr, r,
-                                 p.f, p.go, p.h + pair * p.f);
+        const int pair = t * p.k + j;
+        if (p.routes->id[pair] < 0) continue;
+        float s = 0.f;
+        for (int sl = 0; sl < p.slices; ++sl) s += p.part[(int64_t(sl) * p.T * p.k + pair) * p.d + r];
+        y = fmaf(p.routes->w[pair], s, y);
     }
-    if ((threadIdx.x & 31) == 0) p.y[t * p.d + r] = s;
+    p.y[t * p.d + r] = y;
+}
+
+struct MoePlan {
+    int chunk, slices, slice;
+    size_t smem_in, smem_out, at_h, at_part, bytes;
+};
+
+// Tokens of an expert that are staged together (up to 8, the columns of one
+// product; fewer where a row of x is so long that they would not fit) and slices
+// of the second product's columns: 64 KB of staged activations let three CTAs
+// share an SM.
+MoePlan moe_plan(int64_t T, int k, int64_t d, int64_t f)
+{
+    MoePlan m{};
+    const int si = int(d / W4_STEP), so = int(f / W4_STEP);
+    m.chunk = int(std::min<int64_t>(std::min<int64_t>(T, 8), 160 * 1024 / (256 * si)));
+    m.slice = std::min(so, std::max(1, 64 * 1024 / (512 * m.chunk)));
+    m.slices = (so + m.slice - 1) / m.slice;
+    m.slice = (so + m.slices - 1) / m.slices;
+    m.slices = (so + m.slice - 1) / m.slice;
+    m.smem_in = w4_x_bytes(si, m.chunk, false) + w4_xs_bytes(si, 1, false) + w4_red_bytes(1);
+    m.smem_out = w4_x_bytes(m.slice, m.chunk, true) + w4_xs_bytes(m.slice, 1, false) + w4_red_bytes(1);
+    const size_t pairs = size_t(T) * k;
+    m.at_h = align_up(sizeof(MoeRoutes), 256);
+    m.at_part = m.at_h + align_up(pairs * f * 4, 256);
+    m.bytes = m.at_part + align_up(size_t(m.slices) * pairs * d * 4, 256);
+    return m;
 }
 
 }  // namespace gptq
@@ -152,8 +316,10 @@ extern "C" size_t gptq_w4a16_moe_workspace_bytes(int64_t tokens, int64_t n_exper
                                                  int64_t d_model, int64_t d_ff)
 {
     if (tokens <= 0 || n_experts <= 0 || top_k <= 0 || d_model <= 0 || d_ff <= 0) return 0;
-    const size_t pairs = size_t(tokens) * size_t(top_k);
-    return gptq::align_up(pairs * 8, 256) + gptq::align_up(pairs * size_t(d_ff) * 4, 256);
+    if (tokens > gptq::kMoeTokens || top_k > gptq::kMoeTopK || d_model % 128 != 0 ||
+        d_ff % 128 != 0 || d_model > gptq::kMaxDim || d_ff > gptq::kMaxDim)
+        return 0;
+    return gptq::moe_plan(tokens, top_k, d_model, d_ff).bytes;
 }
 
 extern "C" int gptq_w4a16_moe(const uint16_t* x, int64_t tokens, const float* logits,
@@ -185,26 +351,43 @@ extern "C" int gptq_w4a16_moe(const uint16_t* x, int64_t tokens, const float* lo
         return GPTQ_ERR_INVALID_ARG;
     if (ws_bytes < gptq_w4a16_moe_workspace_bytes(tokens, n_experts, top_k, d_model, d_ff))
         return GPTQ_ERR_INVALID_ARG;
-    const int64_t pairs = tokens * top_k;
+    const MoePlan plan = moe_plan(tokens, top_k, d_model, d_ff);
     MoeParams p{};
     p.x = reinterpret_cast<const __half*>(x);
     p.logits = logits;
-    p.qwi = qweight_in; p.sci = reinterpret_cast<const __half*>(scales_in); p.qzi = qzeros_in;
     p.pi = perm_in;
-    p.qwo = qweight_out; p.sco = reinterpret_cast<const __half*>(scales_out); p.qzo = qzeros_out;
     p.po = perm_out;
-    p.d = d_model; p.f = d_ff; p.gi = gi; p.go = go;
+    p.d = d_model; p.f = d_ff;
     p.T = (int)tokens; p.E = (int)n_experts; p.k = top_k; p.renorm = renormalize != 0;
+    p.in = w4_layer(qweight_in, scales_in, qzeros_in, d_model, gi);
+    p.out = w4_layer(qweight_out, scales_out, qzeros_out, d_ff, go);
+    p.chunk = plan.chunk; p.slice = plan.slice; p.slices = plan.slices;
     uint8_t* w = static_cast<uint8_t*>(ws);
-    p.ids = reinterpret_cast<int*>(w);
-    p.w = reinterpret_cast<float*>(w + pairs * 4);
-    p.h = reinterpret_cast<float*>(w + align_up(size_t(pairs) * 8, 256));
+    p.routes = reinterpret_cast<MoeRoutes*>(w);
+    p.h = reinterpret_cast<float*>(w + plan.at_h);
+    p.part = reinterpret_cast<float*>(w + plan.at_part);
     p.y = y;
     cudaStream_t st = as_stream(stream);
     KernelTimer kt(kKMoe, st);
-    moe_route_kernel<<<1, 256, 0, st>>>(p);
-    moe_in_simple_kernel<<<dim3((unsigned)ceil_div(d_ff, 8), (unsigned)pairs), 256, 0, st>>>(p);
-    moe_out_simple_kernel<<<dim3((unsigned)ceil_div(d_model, 8), (unsigned)tokens), 256, 0, st>>>(p);
+    const int sms = device_sm_count();
+    auto ctas = [&](size_t smem, int64_t units) {
+        const int64_t per = std::max<int64_t>(1, std::min<int64_t>(2, 220 * 1024 / int64_t(smem + 12 * 1024)));
+        return (unsigned)std::min<int64_t>(per * sms, std::max<int64_t>(1, units));
+    };
+    auto in = gi % W4_STEP == 0 ? moe_in_kernel<true> : moe_in_kernel<false>;
+    auto out = go % W4_STEP == 0 ? moe_out_kernel<true> : moe_out_kernel<false>;
+    if (cudaFuncSetAttribute(in, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)plan.smem_in) !=
+            cudaSuccess ||
+        cudaFuncSetAttribute(out, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)plan.smem_out) != cudaSuccess)
+        return GPTQ_ERR_CUDA;
+    const int64_t pairs = tokens * top_k;
+    in<<<ctas(plan.smem_in, pairs * (d_ff / (8 * W4_RW))), W4_THREADS, plan.smem_in, st>>>(p);
+    if (launch_after(out, ctas(plan.smem_out, pairs * plan.slices * (d_model / (16 * W4_RW))),
+                     W4_THREADS, plan.smem_out, st, p) != cudaSuccess ||
+        launch_after(moe_join_kernel, dim3((unsigned)ceil_div(d_model, 256), (unsigned)tokens), 256,
+                     0, st, p) != cudaSuccess)
+        return GPTQ_ERR_CUDA;
     count_launches(3);
     return launch_status();
 }
