@@ -4,27 +4,28 @@
 //   y[r][n] = sum_k Q[r][k] x[n][k],  Q[r][k] = s (c - z) per group of g columns
 //           = sum over groups of  s (sum_k c x  -  z sum_k x)
 //
-// A CTA has 8 warps = KW shares of the columns x RW row tiles of 16 rows.  A
+// A CTA has 16 warps = KW shares of the columns x RW row tiles of 16 rows.  A
 // step is 128 columns of a row tile: 64 bytes a row, 1 KB a warp.
-//  * Products on m16n8k16 mma.sync, fp16 x fp16 -> fp32, rows as A.  A nibble
-//    alone in its half word is the fp16 subnormal c 2^-24, and four bits up it
-//    is c 2^-20: one AND makes an operand register of two codes (nibbles 0 and
-//    4, then 2 and 6, of the low positions; 1 and 5, 3 and 7 of the high ones),
-//    with no OR, subtraction or conversion.  The two positions have their own
-//    accumulators, joined when the group's scale is applied; the zero point is
-//    applied there too, through the group's sum of x.  1.25 ALU instructions an
-//    operand register, against 2.75 for codes in the mantissa of 1024.
-//    Products (11 by 4 bits) are exact, sums fp32.
-//  * Rows come straight from HBM into registers: the four 16-byte loads of a
-//    step's row are the four lanes that hold the row's operand, so nothing
-//    passes through shared memory.  Every lane keeps a ring of four steps in
-//    flight (4 KB a warp), across row tiles.
+//  * Products on m16n8k16 mma.sync, fp16 x fp16 -> fp32, rows as A, up to eight
+//    columns n.  A nibble alone in its half word is the fp16 subnormal c 2^-24,
+//    and four bits up it is c 2^-20: one AND makes an operand register of two
+//    codes (nibbles 0 and 4, then 2 and 6, of the low positions; 1 and 5, 3 and
+//    7 of the high ones), with no OR, subtraction or conversion.  The two
+//    positions have their own accumulators, joined when the group's scale is
+//    applied; the zero point is applied there too, through the group's sum of
+//    x.  1.25 ALU instructions an operand register, against 2.75 for codes in
+//    the mantissa of 1024.  Products (11 by 4 bits) are exact, sums fp32.
+//  * Every warp has its own ring of W4_RING steps in shared memory, filled by
+//    16-byte asynchronous copies that run ahead across row tiles: no barrier
+//    between warps, and no registers (a ring of four steps in registers was
+//    bound by waiting for loads at 0.33 of HBM: a wait on one load waits for
+//    the younger ones that share its scoreboard).
 //  * x is staged once per CTA in operand order: 16 bytes hold the eight columns
 //    of one packed word for one n, so one LDS.128 feeds two products; the order
 //    within the eight is the nibbles' pairing above.
 // Groups that are a multiple of 128 columns (WIDE) fold once a step; smaller
-// ones fold every 32 columns, for which a lane takes the words of a row that
-// are 16 bytes apart (32-bit loads) so that a product stays inside 32 columns.
+// ones fold every 32 columns, for which a lane takes words of a row that are 16
+// bytes apart, so that a product stays inside 32 columns.
 // SPLIT: x in two fp16 parts (22 bits) for fp32 activations, scaled by a power
 // of two per column.
 #pragma once
@@ -34,10 +35,10 @@
 
 namespace gptq {
 
-constexpr int W4_KW = 4, W4_RW = 2;               // column shares, row tiles of a CTA
-constexpr int W4_THREADS = 32 * W4_KW * W4_RW;
-constexpr int W4_RING = 4;                        // steps in flight per lane
+constexpr int W4_THREADS = 512;
+constexpr int W4_RING = 6;                        // steps in flight per warp
 constexpr int W4_STEP = 128;                      // columns per step
+constexpr int W4_COLS = 8;                        // columns n of a product
 
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch()
@@ -56,21 +57,27 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Streamed once: not kept in L1
-__device__ __forceinline__ uint4 ld_stream16(const void* p)
+// D = A B
+__device__ __forceinline__ void mma_16816_first(float (&c)[4], uint32_t a0, uint32_t a1,
+                                                uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
 {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-__device__ __forceinline__ uint32_t ld_nc4(const void* p)
+// 16 bytes global -> shared, asynchronous
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src)
 {
-    uint32_t v;
-    asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v) : "l"(p));
-    return v;
+    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(dst), "l"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // floor(block * 32 / g) for blocks of 32 columns: block * mul >> 22, exact for
@@ -107,112 +114,104 @@ inline W4Layer w4_layer(const uint32_t* qw, const uint16_t* sc, const uint8_t* q
     return l;
 }
 
-// The two rows (g, g + 8 of the row tile) of a lane
+// The rows of a group of row tiles: a uniform base for the first and the second
+// row of every lane, and the lane's own offsets from it (32 bits: an address is
+// a uniform register plus one lane register)
 struct W4Rows {
     const uint8_t* q[2];
     const __half* s[2];
     const uint8_t* z[2];
+    uint32_t oq[2], os[2], oz[2];
 };
 
-__device__ __forceinline__ W4Rows w4_rows(const W4Layer& l, int64_t ra, int64_t rb)
+// base[i]: uniform row; row[i]: the lane's row from there on
+__device__ __forceinline__ W4Rows w4_rows(const W4Layer& l, const int64_t (&base)[2],
+                                          const uint32_t (&row)[2])
 {
     W4Rows r;
-    const uint8_t* q = reinterpret_cast<const uint8_t*>(l.qw);
-    r.q[0] = q + ra * l.rowb;
-    r.q[1] = q + rb * l.rowb;
-    r.s[0] = l.sc + ra * l.G;
-    r.s[1] = l.sc + rb * l.G;
-    r.z[0] = l.qz + ra * l.Gb;
-    r.z[1] = l.qz + rb * l.Gb;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        r.q[i] = reinterpret_cast<const uint8_t*>(l.qw) + base[i] * l.rowb;
+        r.s[i] = l.sc + base[i] * l.G;
+        r.z[i] = l.qz + base[i] * l.Gb;
+        r.oq[i] = row[i] * uint32_t(l.rowb) + (threadIdx.x & 3) * 16;
+        r.os[i] = row[i] * uint32_t(l.G);
+        r.oz[i] = row[i] * uint32_t(l.Gb);
+    }
     return r;
 }
 
-// A step of a lane: 16 bytes of each row and the scale and zero point (bits 0 ..
-// 15 and 16 ..) of the step's group, or, where groups are smaller, of the 32
-// columns of the lane's own number in the quad
-struct W4Regs {
-    uint4 q[2];
-    uint32_t p[2];
-};
-
-template <bool WIDE>
-__device__ __forceinline__ void w4_load(W4Regs& v, const W4Rows& r, const W4Layer& l, int step)
+// Scale and zero point of a group, as two halves of a register: of the group of
+// column block 4 step + block (of 32 columns), for each of the lane's rows
+__device__ __forceinline__ void w4_load_params(uint32_t (&p)[2], const W4Rows& r, const W4Layer& l,
+                                               int block)
 {
-    const int t = threadIdx.x & 3;
-    const int grp = int((uint32_t(step * 4 + (WIDE ? 0 : t)) * l.grp.mul) >> 22);
+    const uint32_t grp = (uint32_t(block) * l.grp.mul) >> 22;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        if constexpr (WIDE) {
-            v.q[i] = ld_stream16(r.q[i] + step * 64 + t * 16);
-        } else {
-            const uint8_t* p = r.q[i] + step * 64 + t * 4;
-            v.q[i] = make_uint4(ld_nc4(p), ld_nc4(p + 16), ld_nc4(p + 32), ld_nc4(p + 48));
-        }
-        v.p[i] = uint32_t(__half_as_ushort(r.s[i][grp])) |
-                 (((uint32_t(r.z[i][grp >> 1]) >> (4 * (grp & 1))) & 15u) << 16);
+        const uint32_t z = (r.z[i][r.oz[i] + (grp >> 1)] >> (4 * (grp & 1))) & 15u;
+        p[i] = uint32_t(__half_as_ushort(r.s[i][r.os[i] + grp])) | (z << 16);
     }
 }
 
 // Staged activations: chunk ((step 4 + w) cols + n) 4 + t of 16 bytes holds, for
 // column n, the columns 128 step + 32 t + 8 w .. (WIDE) or 128 step + 32 w + 8 t ..
-// in the order 0 4 2 6 1 5 3 7; SPLIT: a second plane behind the first.  xs: the
-// sums of a step's 128 (WIDE) or 32 columns, 8 NT floats each, zero behind cols.
+// in the order 0 4 2 6 1 5 3 7; SPLIT: a second plane behind the first.  xs: 2^-24
+// times the sums of a step's 128 (WIDE) or 32 columns, 8 floats each.  Lanes of
+// columns behind cols read another column; their results are not used.
 struct W4Stage {
     const uint4* x;
     const float* xs;
-    int cols;              // columns that are staged (the others are zero)
+    int cols;              // columns that are staged
     int plane;             // chunks of one plane
 };
 
-template <int NT, bool WIDE, bool SPLIT>
-__device__ __forceinline__ void w4_step(float (&y)[NT][4], const W4Regs& v, const W4Stage& st,
-                                        int step)
+// A slot of the ring: row 8 i + g (the lane's row i) at 64 (8 i + g), its 16-byte
+// parts t exchanged by t ^ (g >> 1) so that the 32-bit reads of the narrow form
+// hit 32 banks
+__device__ __forceinline__ uint32_t w4_part(int g, int t) { return uint32_t(t ^ ((g >> 1) & 3)) * 16; }
+
+// y += 2^-24 times the step's product.  qa, qb: the lane's words of its rows.  p:
+// w4_load_params, held by lane t of the quad for (WIDE) step src of four or
+// (otherwise) block t of this step.
+template <bool WIDE, bool SPLIT>
+__device__ __forceinline__ void w4_step(float (&y)[4], const uint32_t (&qa)[4],
+                                        const uint32_t (&qb)[4], const uint32_t (&p)[2], int src,
+                                        const uint4* x, const float* xs, const W4Stage& st)
 {
     constexpr uint32_t LO = 0x000F000Fu, HI = 0x00F000F0u;
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const uint32_t qa[4] = {v.q[0].x, v.q[0].y, v.q[0].z, v.q[0].w};
-    const uint32_t qb[4] = {v.q[1].x, v.q[1].y, v.q[1].z, v.q[1].w};
-    float lo[NT][4], hi[NT][4];
+    const int lane = threadIdx.x & 31, t = lane & 3;
+    float lo[4], hi[4];
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-        if (!WIDE || w == 0) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) lo[n][i] = hi[n][i] = 0.f;
-        }
         const uint32_t a = qa[w], b = qb[w], a8 = a >> 8, b8 = b >> 8;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const bool on = n * 8 + g < st.cols;
-            const int at = ((step * 4 + w) * st.cols + n * 8 + g) * 4 + t;
-#pragma unroll
-            for (int p = 0; p < (SPLIT ? 2 : 1); ++p) {
-                const uint4 x = on ? st.x[at + p * st.plane] : make_uint4(0u, 0u, 0u, 0u);
-                mma_16816(lo[n], a & LO, b & LO, a8 & LO, b8 & LO, x.x, x.y);
-                mma_16816(hi[n], a & HI, b & HI, a8 & HI, b8 & HI, x.z, x.w);
+        for (int h = 0; h < (SPLIT ? 2 : 1); ++h) {
+            const uint4 f = x[h * st.plane];
+            if (h == 0 && (!WIDE || w == 0)) {
+                mma_16816_first(lo, a & LO, b & LO, a8 & LO, b8 & LO, f.x, f.y);
+                mma_16816_first(hi, a & HI, b & HI, a8 & HI, b8 & HI, f.z, f.w);
+            } else {
+                mma_16816(lo, a & LO, b & LO, a8 & LO, b8 & LO, f.x, f.y);
+                mma_16816(hi, a & HI, b & HI, a8 & HI, b8 & HI, f.z, f.w);
             }
         }
+        x += st.cols * 4;
         if (!WIDE || w == 3) {
-            uint32_t pa = v.p[0], pb = v.p[1];
-            if constexpr (!WIDE) {
-                pa = __shfl_sync(0xffffffffu, pa, (lane & ~3) | w);
-                pb = __shfl_sync(0xffffffffu, pb, (lane & ~3) | w);
-            }
-            const float s[2] = {__half2float(__ushort_as_half((unsigned short)(pa & 0xffffu))),
-                                __half2float(__ushort_as_half((unsigned short)(pb & 0xffffu)))};
-            const float z[2] = {s[0] * float(pa >> 16), s[1] * float(pb >> 16)};   // exact
+            float s[2], z[2];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const float2 xs = *reinterpret_cast<const float2*>(
-                    st.xs + (WIDE ? step : step * 4 + w) * (8 * NT) + n * 8 + 2 * t);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float c = fmaf(hi[n][i], 0.0625f, lo[n][i]);             // 2^-24 sum c x
-                    y[n][i] = fmaf(s[i >> 1] * 16777216.f, c, y[n][i]);
-                    y[n][i] = fmaf(-z[i >> 1], (i & 1) ? xs.y : xs.x, y[n][i]);
-                }
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t u = __shfl_sync(0xffffffffu, p[i], (lane & ~3) | (WIDE ? src : w));
+                s[i] = __half2float(__ushort_as_half((unsigned short)(u & 0xffffu)));
+                z[i] = -float(u >> 16);
             }
+            const float2 k = *reinterpret_cast<const float2*>(xs + 2 * t);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float c = fmaf(hi[i], 0.0625f, lo[i]);                 // 2^-24 sum c x
+                y[i] = fmaf(s[i >> 1], fmaf(z[i >> 1], (i & 1) ? k.y : k.x, c), y[i]);
+            }
+            xs += W4_COLS;
         }
     }
 }
@@ -250,13 +249,11 @@ template <bool WIDE> __device__ __forceinline__ float w4_join(float s)
 
 // Stages columns [k0, k0 + 128 steps) of `cols` fp16 rows (row(n): its first
 // element), through perm when given.  All threads; ends without a barrier.
-template <int NT, bool WIDE, class Row>
+template <bool WIDE, class Row>
 __device__ __forceinline__ void w4_stage_half(uint4* x, float* xs, Row row, const int32_t* perm,
                                               int k0, int steps, int cols, int d)
 {
-    constexpr int XS = 8 * NT;
-    for (int i = threadIdx.x; i < steps * (WIDE ? 1 : 4) * XS; i += blockDim.x)
-        if (i % XS >= cols) xs[i] = 0.f;
+    constexpr int XS = W4_COLS;
     const int nch = steps * 16, total = cols * nch;        // a multiple of 16
     for (int base = 0; base < total; base += blockDim.x) {
         const int i = base + threadIdx.x;
@@ -284,20 +281,20 @@ __device__ __forceinline__ void w4_stage_half(uint4* x, float* xs, Row row, cons
             x[w4_chunk<WIDE>(kc, n, cols)] = w4_order(h);
         }
         s = w4_join<WIDE>(s);
-        if (on && kc % (WIDE ? 16 : 4) == 0) xs[(kc / (WIDE ? 16 : 4)) * XS + n] = s;
+        if (on && kc % (WIDE ? 16 : 4) == 0) xs[(kc / (WIDE ? 16 : 4)) * XS + n] = s * 0x1p-24f;
     }
 }
 
 // Stages fp32 rows in two fp16 parts: column n scaled by the power of two that
 // brings its largest magnitude to 2^14 .. 2^15 (undo[n]: its inverse; a column
-// with an infinity or NaN is not scaled).  top: NT * 8 words of scratch.  Holds
+// with an infinity or NaN is not scaled).  top: W4_COLS words of scratch.  Holds
 // barriers; ends without one.
-template <int NT, bool WIDE, class Row>
+template <bool WIDE, class Row>
 __device__ __forceinline__ void w4_stage_split(uint4* x, float* xs, float* undo, uint32_t* top,
                                                Row row, const int32_t* perm, int k0, int steps,
                                                int cols, int d)
 {
-    constexpr int XS = 8 * NT;
+    constexpr int XS = W4_COLS;
     for (int i = threadIdx.x; i < XS; i += blockDim.x) top[i] = 0u;
     __syncthreads();
     const int nch = steps * 16, total = cols * nch;
@@ -334,8 +331,6 @@ __device__ __forceinline__ void w4_stage_split(uint4* x, float* xs, float* undo,
         if (on && (threadIdx.x & 15) == 0) atomicMax(&top[n], m);   // 16 lanes: one step of one n
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < steps * (WIDE ? 1 : 4) * XS; i += blockDim.x)
-        if (i % XS >= cols) xs[i] = 0.f;
     auto factor = [&](int n) {                             // 2^(14 - exponent of the maximum)
         const uint32_t m = top[n];
         if (m == 0u || m >= 0x7f800000u) return 1.f;
@@ -365,101 +360,139 @@ __device__ __forceinline__ void w4_stage_split(uint4* x, float* xs, float* undo,
             x[at + cols * nch] = w4_order(l);
         }
         s = w4_join<WIDE>(s);
-        if (on && kc % (WIDE ? 16 : 4) == 0) xs[(kc / (WIDE ? 16 : 4)) * XS + n] = s;
+        if (on && kc % (WIDE ? 16 : 4) == 0) xs[(kc / (WIDE ? 16 : 4)) * XS + n] = s * 0x1p-24f;
     }
 }
 
-// Shared memory of a staged slice
+// Dynamic shared memory of a sweep, in this order
 inline __host__ __device__ size_t w4_x_bytes(int steps, int cols, bool split)
 {
     return size_t(steps) * 256 * cols * (split ? 2 : 1);
 }
-inline __host__ __device__ size_t w4_xs_bytes(int steps, int nt, bool wide)
+inline __host__ __device__ size_t w4_xs_bytes(int steps, bool wide)
 {
-    return size_t(steps) * (wide ? 1 : 4) * 8 * nt * 4;
+    return size_t(steps) * (wide ? 1 : 4) * W4_COLS * 4;
 }
-constexpr size_t w4_red_bytes(int nt) { return size_t(2) * W4_THREADS * 4 * nt * 4; }
+constexpr size_t W4_RED_BYTES = size_t(2) * W4_THREADS * 16;
+constexpr size_t W4_RING_BYTES = size_t(W4_THREADS / 32) * W4_RING * 1024;
+inline __host__ __device__ size_t w4_smem(int steps, int cols, bool wide, bool split)
+{
+    return w4_x_bytes(steps, cols, split) + w4_xs_bytes(steps, wide) + W4_RED_BYTES + W4_RING_BYTES;
+}
 
 // Sweeps the row-tile groups [g0, g1) over a slice of `steps` steps that starts
-// at step k0 of the rows.
-//   rows(group, rw): the lane's two rows of row tile rw of the group;
-//   stage(): stages x (called after the first loads are issued; ends with a
+// at step k0 of the rows.  red: W4_RED_BYTES, then the ring.
+//   rows(group): the lane's rows of a group of RW row tiles;
+//   stage(): stages x (called after the first copies are issued; ends with a
 //            barrier);
-//   done(group, y): this thread's share of the joined result: y[n][j], element
-//            j = kw of the four of an m16n8 tile (row (lane >> 2) + 8 (j >> 1),
-//            column 8 n + 2 (lane & 3) + (j & 1)) of row tile rw.
-// PAIR: done gets elements kw and kw + 2 instead, in the warps kw < 2 only (rows
-// r and r + 8: gate and up).
-template <int NT, bool WIDE, bool SPLIT, bool PAIR, class RowsF, class StageF, class DoneF>
+//   done(group, j, v): v the joined element j of the four of an m16n8 tile (row
+//            (lane >> 2) + 8 (j >> 1), column 2 (lane & 3) + (j & 1)) of row tile
+//            rw = warp / KW, times 2^24.  The KW warps of a tile share its four
+//            elements.
+// PAIR: done(group, j, v, v2) gets elements j and j + 2 together (rows r and r +
+// 8: gate and up).
+template <int KW, bool WIDE, bool SPLIT, bool PAIR, class RowsF, class StageF, class DoneF>
 __device__ __forceinline__ void w4_sweep(const W4Layer& l, const W4Stage& st, float* red, int g0,
                                          int g1, int k0, int steps, RowsF rows, StageF stage,
                                          DoneF done)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int kw = warp % W4_KW, rw = warp / W4_KW;
-    const int s0 = steps * kw / W4_KW, n = steps * (kw + 1) / W4_KW - s0;
-    W4Regs ring[W4_RING];
-    W4Rows cur = rows(g0, rw);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = lane & 3, g = lane >> 2;
+    const int kw = warp % KW, rw = warp / KW;
+    const int s0 = steps * kw / KW, n = steps * (kw + 1) / KW - s0;
+    uint8_t* ring = reinterpret_cast<uint8_t*>(red) + W4_RED_BYTES + warp * (W4_RING * 1024);
+    const uint32_t put = smem_u32(ring) + g * 64 + w4_part(g, t);
+    // producer: step pj of group pg goes into slot ps
+    int pg = n ? g0 : g1, pj = 0, ps = 0;
+    W4Rows prod = rows(g0);
+    auto issue = [&]() {
+        if (pg < g1) {
 #pragma unroll
-    for (int r = 0; r < W4_RING; ++r)
-        if (r < n) w4_load<WIDE>(ring[r], cur, l, k0 + s0 + r);
-    stage();
-    int buf = 0;
-    for (int grp = g0; grp < g1; ++grp, buf ^= 1) {
-        const bool more = grp + 1 < g1;
-        const W4Rows next = more ? rows(grp + 1, rw) : cur;
-        float y[NT][4];
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) y[i][j] = 0.f;
-        for (int jb = 0; jb < n; jb += W4_RING) {
-#pragma unroll
-            for (int r = 0; r < W4_RING; ++r) {
-                if (jb + r < n) {
-                    w4_step<NT, WIDE, SPLIT>(y, ring[r], st, s0 + jb + r);
-                    if (jb + W4_RING + r < n)
-                        w4_load<WIDE>(ring[r], cur, l, k0 + s0 + jb + W4_RING + r);
-                    else if (more)
-                        w4_load<WIDE>(ring[r], next, l, k0 + s0 + r);
-                }
+            for (int i = 0; i < 2; ++i)
+                cp_async16(put + ps * 1024 + i * 512, prod.q[i] + (k0 + s0 + pj) * 64 + prod.oq[i]);
+            if (++pj == n) {
+                pj = 0;
+                if (++pg < g1) prod = rows(pg);
             }
         }
-        float* out = red + buf * (W4_THREADS * 4 * NT);
+        ps = ps + 1 == W4_RING ? 0 : ps + 1;
+        cp_async_commit();                                 // one (maybe empty) group per step
+    };
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
-            *reinterpret_cast<float4*>(out + ((i * 8 + warp) * 32 + lane) * 4) =
-                make_float4(y[i][0], y[i][1], y[i][2], y[i][3]);
-        __syncthreads();                                   // the buffer of two groups ago is free
-        if constexpr (PAIR) {
-            if (kw < 2) {
-                float v[NT][2];
+    for (int i = 0; i < W4_RING; ++i) issue();
+    // scales and zero points of four steps (WIDE: lane t those of step t; else
+    // block t of each), loaded four steps ahead
+    constexpr int PR = WIDE ? 1 : 4;
+    uint32_t par[PR][2] = {};
+    auto params = [&](uint32_t (&p)[PR][2], const W4Rows& r, int j) {
 #pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    v[i][0] = v[i][1] = 0.f;
+        for (int i = 0; i < PR; ++i)
+            w4_load_params(p[i], r, l, (k0 + s0 + min(j + (WIDE ? t : i), n - 1)) * 4 + (WIDE ? 0 : t));
+    };
+    W4Rows cur = prod;
+    if (n) params(par, rows(g0), 0);
+    stage();
+    const uint4* xw = st.x + (min(g, st.cols - 1) * 4 + t) + s0 * st.cols * 16;
+    const float* xsw = st.xs + s0 * (WIDE ? 1 : 4) * W4_COLS;
+    int slot = 0;
+    for (int grp = g0; grp < g1; ++grp) {
+        const W4Rows next = rows(min(grp + 1, g1 - 1));
+        float y[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint4* x = xw;
+        const float* xs = xsw;
+        for (int jb = 0; jb < n; jb += 4) {
+            uint32_t ahead[PR][2];
+            if (jb + 4 < n) params(ahead, cur, jb + 4);
+            else params(ahead, next, 0);
 #pragma unroll
-                    for (int k = 0; k < W4_KW; ++k) {
-                        const float* p = out + ((i * 8 + rw * W4_KW + k) * 32 + lane) * 4 + kw;
-                        v[i][0] += p[0];
-                        v[i][1] += p[2];
+            for (int r = 0; r < 4; ++r) {
+                if (jb + r < n) {
+                    cp_async_wait<W4_RING - 1>();
+                    if (!WIDE) __syncwarp();
+                    uint32_t q[2][4];
+                    const uint8_t* from = ring + slot * 1024 + g * 64;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        if constexpr (WIDE) {
+                            const uint4 v =
+                                *reinterpret_cast<const uint4*>(from + i * 512 + w4_part(g, t));
+                            q[i][0] = v.x; q[i][1] = v.y; q[i][2] = v.z; q[i][3] = v.w;
+                        } else {
+#pragma unroll
+                            for (int w = 0; w < 4; ++w)
+                                q[i][w] = *reinterpret_cast<const uint32_t*>(
+                                    from + i * 512 + w4_part(g, w) + t * 4);
+                        }
                     }
+                    if (!WIDE) __syncwarp();
+                    slot = slot + 1 == W4_RING ? 0 : slot + 1;
+                    issue();                               // into the slot just read
+                    w4_step<WIDE, SPLIT>(y, q[0], q[1], par[WIDE ? 0 : r], r, x, xs, st);
+                    x += st.cols * 16;
+                    xs += (WIDE ? 1 : 4) * W4_COLS;
                 }
-                done(grp, v);
             }
-        } else {
-            float v[NT];
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                v[i] = 0.f;
+            for (int i = 0; i < PR; ++i) { par[i][0] = ahead[i][0]; par[i][1] = ahead[i][1]; }
+        }
+        float* out = red + ((grp - g0) & 1) * (W4_THREADS * 4);
+        *reinterpret_cast<float4*>(out + threadIdx.x * 4) = make_float4(y[0], y[1], y[2], y[3]);
+        __syncthreads();                                   // the buffer of two groups ago is free
+        constexpr int OUT = PAIR ? 2 : 4;                  // results per lane of a tile
+        for (int j = kw; j < OUT; j += KW) {
+            float v = 0.f, v2 = 0.f;
 #pragma unroll
-                for (int k = 0; k < W4_KW; ++k)
-                    v[i] += out[((i * 8 + rw * W4_KW + k) * 32 + lane) * 4 + kw];
+            for (int k = 0; k < KW; ++k) {
+                const float* p = out + ((rw * KW + k) * 32 + lane) * 4 + j;
+                v += p[0];
+                if (PAIR) v2 += p[2];
             }
-            done(grp, v);
+            if constexpr (PAIR) done(grp, j, v * 0x1p24f, v2 * 0x1p24f);
+            else done(grp, j, v * 0x1p24f);
         }
         cur = next;
     }
-    __syncthreads();                                       // x and red free again
+    cp_async_wait<0>();
+    __syncthreads();                                       // x, red and the ring free again
 }
 
 // A kernel on the stream that may start before its predecessor on it has ended

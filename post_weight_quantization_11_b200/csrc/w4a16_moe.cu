@@ -16,6 +16,7 @@
 namespace gptq {
 
 constexpr int kMoeTokens = 64, kMoeExperts = 256, kMoeTopK = 8;
+constexpr int MOE_KW = 4, MOE_RW = 4;       // of w4_sweep
 constexpr int kMoePairs = kMoeTokens * kMoeTopK;
 
 struct MoeRoutes;
@@ -162,17 +163,17 @@ __device__ __forceinline__ void moe_routes(const MoeParams& p, MoeRoutes& r, int
 // up rows, so that a lane holds both of an element of h.  The CTAs share the
 // row tiles of all chunks evenly; a CTA stages a chunk's tokens once.
 template <bool WIDE>
-__global__ void __launch_bounds__(W4_THREADS, 2) moe_in_kernel(const MoeParams p)
+__global__ void __launch_bounds__(W4_THREADS, 1) moe_in_kernel(const MoeParams p)
 {
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ MoeRoutes r;
     __shared__ int cnt[kMoeExperts], off[kMoeExperts], coff[kMoeExperts];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int kw = warp % W4_KW, rw = warp / W4_KW, g = lane >> 2, t = lane & 3;
-    const int steps = int(p.d / W4_STEP), groups = int(p.f / (8 * W4_RW));
+    const int rw = warp / MOE_KW, g = lane >> 2, t = lane & 3;
+    const int steps = int(p.d / W4_STEP), groups = int(p.f / (8 * MOE_RW));
     uint4* x = reinterpret_cast<uint4*>(smem);
     float* xs = reinterpret_cast<float*>(smem + w4_x_bytes(steps, p.chunk, false));
-    float* red = xs + w4_xs_bytes(steps, 1, WIDE) / 4;
+    float* red = xs + w4_xs_bytes(steps, WIDE) / 4;
     moe_routes(p, r, cnt, off, coff);
     if (blockIdx.x == 0) {                                 // for the second kernel
         const int* src = reinterpret_cast<const int*>(&r);
@@ -189,23 +190,23 @@ __global__ void __launch_bounds__(W4_THREADS, 2) moe_in_kernel(const MoeParams p
         const int* list = r.list + r.start[c];
         const int64_t row0 = int64_t(e) * 2 * p.f;
         const W4Stage st{x, xs, cols, 0};
-        w4_sweep<1, WIDE, false, true>(
+        w4_sweep<MOE_KW, WIDE, false, true>(
             p.in, st, red, g0, g1, 0, steps,
-            [&](int grp, int w) {
-                const int64_t ra = row0 + (int64_t(grp) * W4_RW + w) * 8 + g;
-                return w4_rows(p.in, ra, ra + p.f);
+            [&](int grp) {
+                const int64_t ra = row0 + int64_t(grp) * (8 * MOE_RW);
+                const uint32_t lr = rw * 8 + g;
+                return w4_rows(p.in, {ra, ra + p.f}, {lr, lr});
             },
             [&]() {
-                w4_stage_half<1, WIDE>(
+                w4_stage_half<WIDE>(
                     x, xs, [&](int n) { return p.x + int64_t(list[n] / p.k) * p.d; },
                     p.pi ? p.pi + e * p.d : nullptr, 0, steps, cols, int(p.d));
                 __syncthreads();
             },
-            [&](int grp, float (&v)[1][2]) {
-                const int n = 2 * t + kw;
+            [&](int grp, int j, float gate, float up) {
+                const int n = 2 * t + j;
                 if (n < cols) {
-                    const float gate = v[0][0], up = v[0][1];
-                    p.h[int64_t(list[n]) * p.f + (int64_t(grp) * W4_RW + rw) * 8 + g] =
+                    p.h[int64_t(list[n]) * p.f + (int64_t(grp) * MOE_RW + rw) * 8 + g] =
                         gate / (1.f + expf(-gate)) * up;
                 }
             });
@@ -215,18 +216,18 @@ __global__ void __launch_bounds__(W4_THREADS, 2) moe_in_kernel(const MoeParams p
 
 // part[slice][pair] = D h over a slice of the columns
 template <bool WIDE>
-__global__ void __launch_bounds__(W4_THREADS, 2) moe_out_kernel(const MoeParams p)
+__global__ void __launch_bounds__(W4_THREADS, 1) moe_out_kernel(const MoeParams p)
 {
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ MoeRoutes r;
     __shared__ float undo[8];
     __shared__ uint32_t top[8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int kw = warp % W4_KW, rw = warp / W4_KW, g = lane >> 2, t = lane & 3;
-    const int groups = int(p.d / (16 * W4_RW)), nsteps = int(p.f / W4_STEP);
+    const int rw = warp / MOE_KW, g = lane >> 2, t = lane & 3;
+    const int groups = int(p.d / (16 * MOE_RW)), nsteps = int(p.f / W4_STEP);
     uint4* x = reinterpret_cast<uint4*>(smem);
     float* xs = reinterpret_cast<float*>(smem + w4_x_bytes(p.slice, p.chunk, true));
-    float* red = xs + w4_xs_bytes(p.slice, 1, WIDE) / 4;
+    float* red = xs + w4_xs_bytes(p.slice, WIDE) / 4;
     pdl_wait();
     for (int i = threadIdx.x; i < int(sizeof(MoeRoutes) / 4); i += blockDim.x)
         reinterpret_cast<int*>(&r)[i] = reinterpret_cast<const int*>(p.routes)[i];
@@ -243,23 +244,24 @@ __global__ void __launch_bounds__(W4_THREADS, 2) moe_out_kernel(const MoeParams 
         const int* list = r.list + r.start[c];
         const int64_t row0 = int64_t(e) * p.d;
         const W4Stage st{x, xs, cols, steps * 16 * cols};
-        w4_sweep<1, WIDE, true, false>(
+        w4_sweep<MOE_KW, WIDE, true, false>(
             p.out, st, red, g0, g1, k0, steps,
-            [&](int grp, int w) {
-                const int64_t ra = row0 + (int64_t(grp) * W4_RW + w) * 16 + g;
-                return w4_rows(p.out, ra, ra + 8);
+            [&](int grp) {
+                const int64_t ra = row0 + int64_t(grp) * (16 * MOE_RW);
+                const uint32_t lr = rw * 16 + g;
+                return w4_rows(p.out, {ra, ra}, {lr, lr + 8});
             },
             [&]() {
-                w4_stage_split<1, WIDE>(
+                w4_stage_split<WIDE>(
                     x, xs, undo, top, [&](int n) { return p.h + int64_t(list[n]) * p.f; },
                     p.po ? p.po + e * p.f : nullptr, k0 * W4_STEP, steps, cols, int(p.f));
                 __syncthreads();
             },
-            [&](int grp, float (&v)[1]) {
-                const int n = 2 * t + (kw & 1);
+            [&](int grp, int j, float v) {
+                const int n = 2 * t + (j & 1);
                 if (n < cols)
                     p.part[(int64_t(sl) * p.T * p.k + list[n]) * p.d +
-                           (int64_t(grp) * W4_RW + rw) * 16 + g + 8 * (kw >> 1)] = v[0] * undo[n];
+                           (int64_t(grp) * MOE_RW + rw) * 16 + g + 8 * (j >> 1)] = v * undo[n];
             });
         u += g1 - g0;
     }
@@ -289,20 +291,20 @@ struct MoePlan {
 };
 
 // Tokens of an expert that are staged together (up to 8, the columns of one
-// product; fewer where a row of x is so long that they would not fit) and slices
-// of the second product's columns: 64 KB of staged activations let three CTAs
-// share an SM.
+// product; fewer where a row of x is so long that they would not fit beside the
+// ring) and slices of the second product's columns.
 MoePlan moe_plan(int64_t T, int k, int64_t d, int64_t f)
 {
+    constexpr int MOST = 72 * 1024;                        // bytes of staged activations
     MoePlan m{};
     const int si = int(d / W4_STEP), so = int(f / W4_STEP);
-    m.chunk = int(std::min<int64_t>(std::min<int64_t>(T, 8), 160 * 1024 / (256 * si)));
-    m.slice = std::min(so, std::max(1, 64 * 1024 / (512 * m.chunk)));
+    m.chunk = int(std::min<int64_t>(std::min<int64_t>(T, W4_COLS), MOST / (256 * si)));
+    m.slice = std::min(so, std::max(1, MOST / (512 * m.chunk)));
     m.slices = (so + m.slice - 1) / m.slice;
     m.slice = (so + m.slices - 1) / m.slices;
     m.slices = (so + m.slice - 1) / m.slice;
-    m.smem_in = w4_x_bytes(si, m.chunk, false) + w4_xs_bytes(si, 1, false) + w4_red_bytes(1);
-    m.smem_out = w4_x_bytes(m.slice, m.chunk, true) + w4_xs_bytes(m.slice, 1, false) + w4_red_bytes(1);
+    m.smem_in = w4_smem(si, m.chunk, false, false);
+    m.smem_out = w4_smem(m.slice, m.chunk, false, true);
     const size_t pairs = size_t(T) * k;
     m.at_h = align_up(sizeof(MoeRoutes), 256);
     m.at_part = m.at_h + align_up(pairs * f * 4, 256);
@@ -370,10 +372,7 @@ extern "C" int gptq_w4a16_moe(const uint16_t* x, int64_t tokens, const float* lo
     cudaStream_t st = as_stream(stream);
     KernelTimer kt(kKMoe, st);
     const int sms = device_sm_count();
-    auto ctas = [&](size_t smem, int64_t units) {
-        const int64_t per = std::max<int64_t>(1, std::min<int64_t>(2, 220 * 1024 / int64_t(smem + 12 * 1024)));
-        return (unsigned)std::min<int64_t>(per * sms, std::max<int64_t>(1, units));
-    };
+    auto ctas = [&](int64_t units) { return (unsigned)std::min<int64_t>(sms, units); };
     auto in = gi % W4_STEP == 0 ? moe_in_kernel<true> : moe_in_kernel<false>;
     auto out = go % W4_STEP == 0 ? moe_out_kernel<true> : moe_out_kernel<false>;
     if (cudaFuncSetAttribute(in, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)plan.smem_in) !=
@@ -382,8 +381,8 @@ extern "C" int gptq_w4a16_moe(const uint16_t* x, int64_t tokens, const float* lo
                              (int)plan.smem_out) != cudaSuccess)
         return GPTQ_ERR_CUDA;
     const int64_t pairs = tokens * top_k;
-    in<<<ctas(plan.smem_in, pairs * (d_ff / (8 * W4_RW))), W4_THREADS, plan.smem_in, st>>>(p);
-    if (launch_after(out, ctas(plan.smem_out, pairs * plan.slices * (d_model / (16 * W4_RW))),
+    in<<<ctas(pairs * (d_ff / (8 * MOE_RW))), W4_THREADS, plan.smem_in, st>>>(p);
+    if (launch_after(out, ctas(pairs * plan.slices * (d_model / (16 * MOE_RW))),
                      W4_THREADS, plan.smem_out, st, p) != cudaSuccess ||
         launch_after(moe_join_kernel, dim3((unsigned)ceil_div(d_model, 256), (unsigned)tokens), 256,
                      0, st, p) != cudaSuccess)
