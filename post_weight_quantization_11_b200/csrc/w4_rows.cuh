@@ -4,8 +4,8 @@
 //   y[r][n] = sum_k Q[r][k] x[n][k],  Q[r][k] = s (c - z) per group of g columns
 //           = sum over groups of  s (sum_k c x  -  z sum_k x)
 //
-// A CTA has 16 warps = KW shares of the columns x RW row tiles of 16 rows.  A
-// step is 128 columns of a row tile: 64 bytes a row, 1 KB a warp.
+// A CTA has 16 warps = KW shares of the columns x RW row tiles of 32 rows.  A
+// step is 128 columns of a row tile: 64 bytes a row, 2 KB a warp.
 //  * Products on m16n8k16 mma.sync, fp16 x fp16 -> fp32, rows as A, up to eight
 //    columns n.  A nibble alone in its half word is the fp16 subnormal c 2^-24,
 //    and four bits up it is c 2^-20: one AND makes an operand register of two
@@ -15,11 +15,12 @@
 //    applied; the zero point is applied there too, through the group's sum of
 //    x.  1.25 ALU instructions an operand register, against 2.75 for codes in
 //    the mantissa of 1024.  Products (11 by 4 bits) are exact, sums fp32.
-//  * Every warp has its own ring of W4_RING steps in shared memory, filled by
-//    16-byte asynchronous copies that run ahead across row tiles: no barrier
-//    between warps, and no registers (a ring of four steps in registers was
-//    bound by waiting for loads at 0.33 of HBM: a wait on one load waits for
-//    the younger ones that share its scoreboard).
+//  * Every warp has its own ring of W4_RING steps in shared memory, filled by one
+//    TMA copy a step (32 rows x 64 bytes, 64-byte swizzle) that runs ahead across
+//    row tiles: no barrier between warps, no registers, two instructions a step.
+//    (A ring of four steps in registers was bound by waiting for loads: a wait
+//    on one load waits for the younger ones that share its scoreboard.)
+//  * 32 rows a warp share each read of x.
 //  * x is staged once per CTA in operand order: 16 bytes hold the eight columns
 //    of one packed word for one n, so one LDS.128 feeds two products; the order
 //    within the eight is the nibbles' pairing above.
@@ -36,7 +37,8 @@
 namespace gptq {
 
 constexpr int W4_THREADS = 512;
-constexpr int W4_RING = 6;                        // steps in flight per warp
+constexpr int W4_RING = 3;                        // steps in flight per warp
+constexpr int W4_SLOT = 2048;                     // bytes of one
 constexpr int W4_STEP = 128;                      // columns per step
 constexpr int W4_COLS = 8;                        // columns n of a product
 
@@ -68,16 +70,32 @@ __device__ __forceinline__ void mma_16816_first(float (&c)[4], uint32_t a0, uint
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-// 16 bytes global -> shared, asynchronous
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src)
+// Shared memory by its 32-bit address
+__device__ __forceinline__ uint4 lds16(uint32_t a)
 {
-    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(dst), "l"(src)
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(a)
                  : "memory");
+    return v;
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void cp_async_wait()
+__device__ __forceinline__ uint32_t lds4(uint32_t a)
 {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ float lds_f(uint32_t a) { return __uint_as_float(lds4(a)); }
+__device__ __forceinline__ float2 lds_f2(uint32_t a)
+{
+    float2 v;
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts_f(uint32_t a, float v)
+{
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
 }
 
 // floor(block * 32 / g) for blocks of 32 columns: block * mul >> 22, exact for
@@ -114,44 +132,16 @@ inline W4Layer w4_layer(const uint32_t* qw, const uint16_t* sc, const uint8_t* q
     return l;
 }
 
-// The rows of a group of row tiles: a uniform base for the first and the second
-// row of every lane, and the lane's own offsets from it (32 bits: an address is
-// a uniform register plus one lane register)
-struct W4Rows {
-    const uint8_t* q[2];
-    const __half* s[2];
-    const uint8_t* z[2];
-    uint32_t oq[2], os[2], oz[2];
-};
-
-// base[i]: uniform row; row[i]: the lane's row from there on
-__device__ __forceinline__ W4Rows w4_rows(const W4Layer& l, const int64_t (&base)[2],
-                                          const uint32_t (&row)[2])
+// Scale (low half) and minus the zero point (high half) as fp16, of group grp of
+// a row; sc, qz: of the sweep's first row
+__device__ __forceinline__ uint32_t w4_params(const W4Layer& l, const __half* sc, const uint8_t* qz,
+                                              uint32_t row, uint32_t grp)
 {
-    W4Rows r;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        r.q[i] = reinterpret_cast<const uint8_t*>(l.qw) + base[i] * l.rowb;
-        r.s[i] = l.sc + base[i] * l.G;
-        r.z[i] = l.qz + base[i] * l.Gb;
-        r.oq[i] = row[i] * uint32_t(l.rowb) + (threadIdx.x & 3) * 16;
-        r.os[i] = row[i] * uint32_t(l.G);
-        r.oz[i] = row[i] * uint32_t(l.Gb);
-    }
-    return r;
-}
-
-// Scale and zero point of a group, as two halves of a register: of the group of
-// column block 4 step + block (of 32 columns), for each of the lane's rows
-__device__ __forceinline__ void w4_load_params(uint32_t (&p)[2], const W4Rows& r, const W4Layer& l,
-                                               int block)
-{
-    const uint32_t grp = (uint32_t(block) * l.grp.mul) >> 22;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint32_t z = (r.z[i][r.oz[i] + (grp >> 1)] >> (4 * (grp & 1))) & 15u;
-        p[i] = uint32_t(__half_as_ushort(r.s[i][r.os[i] + grp])) | (z << 16);
-    }
+    const uint32_t s = __half_as_ushort(sc[row * uint32_t(l.G) + grp]);
+    const uint32_t z = (uint32_t(qz[row * uint32_t(l.Gb) + (grp >> 1)]) >> (4 * (grp & 1))) & 15u;
+    const __half m = __hsub(__ushort_as_half((unsigned short)0x6400),
+                            __ushort_as_half((unsigned short)(0x6400u | z)));   // 1024 - (1024 + z)
+    return s | (uint32_t(__half_as_ushort(m)) << 16);
 }
 
 // Staged activations: chunk ((step 4 + w) cols + n) 4 + t of 16 bytes holds, for
@@ -160,58 +150,79 @@ __device__ __forceinline__ void w4_load_params(uint32_t (&p)[2], const W4Rows& r
 // times the sums of a step's 128 (WIDE) or 32 columns, 8 floats each.  Lanes of
 // columns behind cols read another column; their results are not used.
 struct W4Stage {
-    const uint4* x;
-    const float* xs;
+    uint32_t x, xs;        // shared addresses
     int cols;              // columns that are staged
-    int plane;             // chunks of one plane
+    uint32_t plane;        // bytes of one plane
 };
 
-// A slot of the ring: row 8 i + g (the lane's row i) at 64 (8 i + g), its 16-byte
-// parts t exchanged by t ^ (g >> 1) so that the 32-bit reads of the narrow form
-// hit 32 banks
-__device__ __forceinline__ uint32_t w4_part(int g, int t) { return uint32_t(t ^ ((g >> 1) & 3)) * 16; }
+// The 16-byte part t of row r of a slot (rows of 64 bytes, 64-byte swizzle) is at 64 r
+// + 16 (t ^ ((r >> 1) & 3)): the eight rows of an operand hit 32 banks, in 16-byte
+// reads and in 32-bit ones.  Rows 8 apart have the same place in their 512 bytes.
+// Row 8 i + g of the warp's m16 tile m is row 16 m + 8 i + g of a slot; PAIR: 16 i
+// + 8 m + g (rows 0 .. 15 are gate rows, 16 .. 31 the up rows of the same elements).
+template <bool PAIR> __host__ __device__ constexpr int w4_row(int m, int i)
+{
+    return PAIR ? i * 16 + m * 8 : m * 16 + i * 8;
+}
 
-// y += 2^-24 times the step's product.  qa, qb: the lane's words of its rows.  p:
-// w4_load_params, held by lane t of the quad for (WIDE) step src of four or
+// y += 2^-24 times the step's product.  slot: shared address of the step's rows, of
+// the lane's part of row g; WIDE: its part t, else row g itself.  p: w4_params of
+// the lane's rows, held by lane t of the quad for (WIDE) step src of four or
 // (otherwise) block t of this step.
-template <bool WIDE, bool SPLIT>
-__device__ __forceinline__ void w4_step(float (&y)[4], const uint32_t (&qa)[4],
-                                        const uint32_t (&qb)[4], const uint32_t (&p)[2], int src,
-                                        const uint4* x, const float* xs, const W4Stage& st)
+template <bool WIDE, bool SPLIT, bool PAIR>
+__device__ __forceinline__ void w4_step(float (&y)[2][4], uint32_t slot, const uint32_t (&p)[2][2],
+                                        int src, uint32_t x, uint32_t xs, uint32_t xw,
+                                        uint32_t plane)
 {
     constexpr uint32_t LO = 0x000F000Fu, HI = 0x00F000F0u;
-    const int lane = threadIdx.x & 31, t = lane & 3;
-    float lo[4], hi[4];
+    const int g = (threadIdx.x & 31) >> 2;
+    uint32_t q[2][2][4];
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        const uint32_t a = qa[w], b = qb[w], a8 = a >> 8, b8 = b >> 8;
+    for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int h = 0; h < (SPLIT ? 2 : 1); ++h) {
-            const uint4 f = x[h * st.plane];
-            if (h == 0 && (!WIDE || w == 0)) {
-                mma_16816_first(lo, a & LO, b & LO, a8 & LO, b8 & LO, f.x, f.y);
-                mma_16816_first(hi, a & HI, b & HI, a8 & HI, b8 & HI, f.z, f.w);
+        for (int i = 0; i < 2; ++i) {
+            if constexpr (WIDE) {
+                const uint4 v = lds16(slot + w4_row<PAIR>(m, i) * 64);
+                q[m][i][0] = v.x; q[m][i][1] = v.y; q[m][i][2] = v.z; q[m][i][3] = v.w;
             } else {
-                mma_16816(lo, a & LO, b & LO, a8 & LO, b8 & LO, f.x, f.y);
-                mma_16816(hi, a & HI, b & HI, a8 & HI, b8 & HI, f.z, f.w);
+#pragma unroll
+                for (int w = 0; w < 4; ++w)
+                    q[m][i][w] = lds4(slot + w4_row<PAIR>(m, i) * 64 + (w ^ ((g >> 1) & 3)) * 16);
             }
         }
-        x += st.cols * 4;
+    float lo[2][4], hi[2][4];
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+#pragma unroll
+        for (int h = 0; h < (SPLIT ? 2 : 1); ++h) {
+            const uint4 f = lds16(h ? x + plane : x);
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const uint32_t a = q[m][0][w], b = q[m][1][w], a8 = a >> 8, b8 = b >> 8;
+                if (h == 0 && (!WIDE || w == 0)) {
+                    mma_16816_first(lo[m], a & LO, b & LO, a8 & LO, b8 & LO, f.x, f.y);
+                    mma_16816_first(hi[m], a & HI, b & HI, a8 & HI, b8 & HI, f.z, f.w);
+                } else {
+                    mma_16816(lo[m], a & LO, b & LO, a8 & LO, b8 & LO, f.x, f.y);
+                    mma_16816(hi[m], a & HI, b & HI, a8 & HI, b8 & HI, f.z, f.w);
+                }
+            }
+        }
+        x += xw;
         if (!WIDE || w == 3) {
-            float s[2], z[2];
+            const float2 k = lds_f2(xs + (WIDE ? 0 : w * W4_COLS * 4));
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint32_t u = __shfl_sync(0xffffffffu, p[i], (lane & ~3) | (WIDE ? src : w));
-                s[i] = __half2float(__ushort_as_half((unsigned short)(u & 0xffffu)));
-                z[i] = -float(u >> 16);
-            }
-            const float2 k = *reinterpret_cast<const float2*>(xs + 2 * t);
+            for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float c = fmaf(hi[i], 0.0625f, lo[i]);                 // 2^-24 sum c x
-                y[i] = fmaf(s[i >> 1], fmaf(z[i >> 1], (i & 1) ? k.y : k.x, c), y[i]);
-            }
-            xs += W4_COLS;
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t u = __shfl_sync(0xffffffffu, p[m][i], WIDE ? src : w, 4);
+                    const float2 sz = __half22float2(*reinterpret_cast<const __half2*>(&u));
+#pragma unroll
+                    for (int e = 2 * i; e < 2 * i + 2; ++e) {
+                        const float c = fmaf(hi[m][e], 0.0625f, lo[m][e]);   // 2^-24 sum c x
+                        y[m][e] = fmaf(sz.x, fmaf(sz.y, (e & 1) ? k.y : k.x, c), y[m][e]);
+                    }
+                }
         }
     }
 }
@@ -364,7 +375,14 @@ __device__ __forceinline__ void w4_stage_split(uint4* x, float* xs, float* undo,
     }
 }
 
-// Dynamic shared memory of a sweep, in this order
+// Dynamic shared memory of a kernel with sweeps: the ring, the joining buffers,
+// the barriers, then the staged activations and their sums
+constexpr int W4_WARPS = W4_THREADS / 32;
+constexpr int W4_RED = W4_WARPS * 32 * 8;                    // floats of one joining buffer
+constexpr size_t W4_AT_RED = size_t(W4_WARPS) * W4_RING * W4_SLOT;
+constexpr size_t W4_AT_BAR = W4_AT_RED + 2 * W4_RED * 4;
+constexpr size_t W4_AT_X = W4_AT_BAR + 512;
+static_assert(W4_WARPS * W4_RING * 8 <= 512, "barriers");
 inline __host__ __device__ size_t w4_x_bytes(int steps, int cols, bool split)
 {
     return size_t(steps) * 256 * cols * (split ? 2 : 1);
@@ -373,126 +391,193 @@ inline __host__ __device__ size_t w4_xs_bytes(int steps, bool wide)
 {
     return size_t(steps) * (wide ? 1 : 4) * W4_COLS * 4;
 }
-constexpr size_t W4_RED_BYTES = size_t(2) * W4_THREADS * 16;
-constexpr size_t W4_RING_BYTES = size_t(W4_THREADS / 32) * W4_RING * 1024;
-inline __host__ __device__ size_t w4_smem(int steps, int cols, bool wide, bool split)
+// (and up to 1023 bytes in front, for the alignment of the ring)
+inline size_t w4_smem(int steps, int cols, bool wide, bool split)
 {
-    return w4_x_bytes(steps, cols, split) + w4_xs_bytes(steps, wide) + W4_RED_BYTES + W4_RING_BYTES;
+    return 1024 + W4_AT_X + w4_x_bytes(steps, cols, split) + w4_xs_bytes(steps, wide);
 }
 
-// Sweeps the row-tile groups [g0, g1) over a slice of `steps` steps that starts
-// at step k0 of the rows.  red: W4_RED_BYTES, then the ring.
-//   rows(group): the lane's rows of a group of RW row tiles;
+// The packed rows as a TMA tensor, in boxes of 64 bytes x `rows`
+inline int w4_tmap(CUtensorMap* tm, const uint32_t* qw, int64_t rows, int64_t d, int box_rows)
+{
+    return encode_tmap_2d(tm, CU_TENSOR_MAP_DATA_TYPE_UINT32, qw, uint64_t(d / 8), uint64_t(rows),
+                          uint64_t(d / 2), 16, uint32_t(box_rows), CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
+// A warp's ring (shared addresses)
+struct W4Pipe {
+    uint32_t ring, bar, red;
+    uint32_t put, get;         // next slot to fill, to read
+    uint32_t phase;            // parity of the slot to read
+    int* abort;
+};
+
+// All threads; with a barrier
+__device__ __forceinline__ W4Pipe w4_pipe(uint8_t* smem, int* abort)
+{
+    const int warp = threadIdx.x >> 5;
+    W4Pipe p;
+    p.ring = smem_u32(smem) + warp * (W4_RING * W4_SLOT);
+    p.red = smem_u32(smem) + uint32_t(W4_AT_RED);
+    uint64_t* bar = reinterpret_cast<uint64_t*>(smem + W4_AT_BAR) + warp * W4_RING;
+    p.bar = smem_u32(bar);
+    p.abort = abort;
+    p.put = p.get = 0;
+    p.phase = 0;
+    if ((threadIdx.x & 31) == 0)
+        for (int i = 0; i < W4_RING; ++i) mbar_init(&bar[i], 1);
+    if (threadIdx.x == 0) *abort = 0;
+    fence_mbar_init();
+    __syncthreads();
+    return p;
+}
+
+__device__ __forceinline__ bool w4_try_wait(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// The rest of a wait that did not succeed at once: bounded like every wait of the
+// library; after it gave up the sweep goes on with what is there
+__device__ __noinline__ void w4_wait_long(uint32_t bar, uint32_t parity, volatile int* abort)
+{
+    const unsigned long long t0 = globaltimer_ns();
+    for (unsigned i = 1; !w4_try_wait(bar, parity); ++i)
+        if ((i & 63u) == 0) {
+            if (*abort) return;
+            if (globaltimer_ns() - t0 > kWaitLimitNs) {
+                atomicCAS(&g_device_status, 0, kErrWaitFull);
+                *abort = 1;
+                return;
+            }
+        }
+}
+
+// Sweeps the groups [0, groups) of RW row tiles over a slice of `steps` steps that
+// starts at step k0 of the rows.  Group 0 begins at row0 (of tm and l; end: the rows
+// behind it are not read).  PAIR: a tile is 16 rows from row0 on and the 16 rows that
+// lie `pair` rows further on.
 //   stage(): stages x (called after the first copies are issued; ends with a
 //            barrier);
-//   done(group, j, v): v the joined element j of the four of an m16n8 tile (row
-//            (lane >> 2) + 8 (j >> 1), column 2 (lane & 3) + (j & 1)) of row tile
-//            rw = warp / KW, times 2^24.  The KW warps of a tile share its four
-//            elements.
-// PAIR: done(group, j, v, v2) gets elements j and j + 2 together (rows r and r +
-// 8: gate and up).
-template <int KW, bool WIDE, bool SPLIT, bool PAIR, class RowsF, class StageF, class DoneF>
-__device__ __forceinline__ void w4_sweep(const W4Layer& l, const W4Stage& st, float* red, int g0,
-                                         int g1, int k0, int steps, RowsF rows, StageF stage,
-                                         DoneF done)
+//   done(group, r, n, v): the joined result of row r of the group (PAIR: of the
+//            group's gate rows), column n; PAIR: done(group, r, n, v, v2) with the up
+//            row's.
+template <int KW, bool WIDE, bool SPLIT, bool PAIR, class StageF, class DoneF>
+__device__ __forceinline__ void w4_sweep(W4Pipe& pipe, const CUtensorMap* tm, const W4Layer& l,
+                                         int64_t row0, int64_t end, uint32_t pair,
+                                         const W4Stage& st, int groups, int k0, int steps,
+                                         StageF stage, DoneF done)
 {
+    constexpr int RW = W4_WARPS / KW, ROWS = PAIR ? 16 : 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = lane & 3, g = lane >> 2;
     const int kw = warp % KW, rw = warp / KW;
     const int s0 = steps * kw / KW, n = steps * (kw + 1) / KW - s0;
-    uint8_t* ring = reinterpret_cast<uint8_t*>(red) + W4_RED_BYTES + warp * (W4_RING * 1024);
-    const uint32_t put = smem_u32(ring) + g * 64 + w4_part(g, t);
-    // producer: step pj of group pg goes into slot ps
-    int pg = n ? g0 : g1, pj = 0, ps = 0;
-    W4Rows prod = rows(g0);
+    // producer (lane 0): the rows and words of the next copy, copies left of the
+    // row tile and in all
+    const int col0 = (k0 + s0) * 16;
+    int prow = int(row0) + rw * ROWS, pcol = col0, pleft = n, left = n * groups;
     auto issue = [&]() {
-        if (pg < g1) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                cp_async16(put + ps * 1024 + i * 512, prod.q[i] + (k0 + s0 + pj) * 64 + prod.oq[i]);
-            if (++pj == n) {
-                pj = 0;
-                if (++pg < g1) prod = rows(pg);
-            }
+        if (left == 0) return;
+        --left;
+        if (lane == 0) {
+            const uint32_t dst = pipe.ring + pipe.put * W4_SLOT, bar = pipe.bar + pipe.put * 8;
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar),
+                         "r"(W4_SLOT)
+                         : "memory");
+            auto copy = [&](uint32_t to, int row) {
+                asm volatile(
+                    "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+                    " [%0], [%1, {%3, %4}], [%2];" ::"r"(to), "l"(reinterpret_cast<uint64_t>(tm)),
+                    "r"(bar), "r"(pcol), "r"(row)
+                    : "memory");
+            };
+            copy(dst, prow);
+            if (PAIR) copy(dst + W4_SLOT / 2, prow + int(pair));
         }
-        ps = ps + 1 == W4_RING ? 0 : ps + 1;
-        cp_async_commit();                                 // one (maybe empty) group per step
+        pipe.put = pipe.put + 1 == W4_RING ? 0 : pipe.put + 1;
+        pcol += 16;
+        if (--pleft == 0) { pleft = n; pcol = col0; prow += RW * ROWS; }
     };
 #pragma unroll
     for (int i = 0; i < W4_RING; ++i) issue();
-    // scales and zero points of four steps (WIDE: lane t those of step t; else
-    // block t of each), loaded four steps ahead
-    constexpr int PR = WIDE ? 1 : 4;
-    uint32_t par[PR][2] = {};
-    auto params = [&](uint32_t (&p)[PR][2], const W4Rows& r, int j) {
+    // scales and zero points: WIDE: of four steps at a time (lane t those of step
+    // t), four steps ahead; else of block t of a step, one step ahead
+    const __half* sc = l.sc + row0 * l.G;
+    const uint8_t* qz = l.qz + row0 * l.Gb;
+    const uint32_t last = uint32_t(end - row0 - 1);
+    auto params = [&](uint32_t (&p)[2][2], int grp, int j) {
+        const uint32_t block = (k0 + s0 + min(j + (WIDE ? t : 0), n - 1)) * 4 + (WIDE ? 0 : t);
+        const uint32_t at = (block * l.grp.mul) >> 22;
+        const uint32_t first = (grp * RW + rw) * ROWS + g;
 #pragma unroll
-        for (int i = 0; i < PR; ++i)
-            w4_load_params(p[i], r, l, (k0 + s0 + min(j + (WIDE ? t : i), n - 1)) * 4 + (WIDE ? 0 : t));
-    };
-    W4Rows cur = prod;
-    if (n) params(par, rows(g0), 0);
-    stage();
-    const uint4* xw = st.x + (min(g, st.cols - 1) * 4 + t) + s0 * st.cols * 16;
-    const float* xsw = st.xs + s0 * (WIDE ? 1 : 4) * W4_COLS;
-    int slot = 0;
-    for (int grp = g0; grp < g1; ++grp) {
-        const W4Rows next = rows(min(grp + 1, g1 - 1));
-        float y[4] = {0.f, 0.f, 0.f, 0.f};
-        const uint4* x = xw;
-        const float* xs = xsw;
-        for (int jb = 0; jb < n; jb += 4) {
-            uint32_t ahead[PR][2];
-            if (jb + 4 < n) params(ahead, cur, jb + 4);
-            else params(ahead, next, 0);
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                if (jb + r < n) {
-                    cp_async_wait<W4_RING - 1>();
-                    if (!WIDE) __syncwarp();
-                    uint32_t q[2][4];
-                    const uint8_t* from = ring + slot * 1024 + g * 64;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        if constexpr (WIDE) {
-                            const uint4 v =
-                                *reinterpret_cast<const uint4*>(from + i * 512 + w4_part(g, t));
-                            q[i][0] = v.x; q[i][1] = v.y; q[i][2] = v.z; q[i][3] = v.w;
-                        } else {
-#pragma unroll
-                            for (int w = 0; w < 4; ++w)
-                                q[i][w] = *reinterpret_cast<const uint32_t*>(
-                                    from + i * 512 + w4_part(g, w) + t * 4);
-                        }
-                    }
-                    if (!WIDE) __syncwarp();
-                    slot = slot + 1 == W4_RING ? 0 : slot + 1;
-                    issue();                               // into the slot just read
-                    w4_step<WIDE, SPLIT>(y, q[0], q[1], par[WIDE ? 0 : r], r, x, xs, st);
-                    x += st.cols * 16;
-                    xs += (WIDE ? 1 : 4) * W4_COLS;
-                }
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t r = PAIR ? first + m * 8 + i * pair
+                                        : min(first + w4_row<PAIR>(m, i), last);
+                p[m][i] = w4_params(l, sc, qz, r, at);
             }
+    };
+    constexpr int EVERY = WIDE ? 4 : 1;
+    uint32_t par[2][2] = {}, ahead[2][2] = {};
+    if (n) params(ahead, 0, 0);
+    stage();
+    const uint32_t xw = st.cols * 64;
+    const uint32_t x0 = st.x + (min(g, st.cols - 1) * 4 + t) * 16 + s0 * 4 * xw;
+    const uint32_t xs0 = st.xs + s0 * (WIDE ? 1 : 4) * W4_COLS * 4 + t * 8;
+    const uint32_t from = pipe.ring + g * 64 + (WIDE ? (t ^ ((g >> 1) & 3)) * 16 : t * 4);
+    uint32_t red = pipe.red + (warp * 32 + lane) * 4, flip = W4_RED * 4;
+    for (int grp = 0; grp < groups; ++grp) {
+        float y[2][4] = {};
+        uint32_t x = x0, xs = xs0;
+#pragma unroll 1
+        for (int j = 0; j < n; ++j) {
+            if (j % EVERY == 0) {
 #pragma unroll
-            for (int i = 0; i < PR; ++i) { par[i][0] = ahead[i][0]; par[i][1] = ahead[i][1]; }
+                for (int m = 0; m < 2; ++m) { par[m][0] = ahead[m][0]; par[m][1] = ahead[m][1]; }
+                if (j + EVERY < n) params(ahead, grp, j + EVERY);
+                else params(ahead, min(grp + 1, groups - 1), 0);
+            }
+            if (!w4_try_wait(pipe.bar + pipe.get * 8, pipe.phase))
+                w4_wait_long(pipe.bar + pipe.get * 8, pipe.phase, pipe.abort);
+            w4_step<WIDE, SPLIT, PAIR>(y, from + pipe.get * W4_SLOT, par, j & 3, x, xs, xw, st.plane);
+            if (++pipe.get == W4_RING) { pipe.get = 0; pipe.phase ^= 1u; }
+            x += 4 * xw;
+            xs += (WIDE ? 1 : 4) * W4_COLS * 4;
+            __syncwarp();                                  // every lane has read its slot
+            issue();
         }
-        float* out = red + ((grp - g0) & 1) * (W4_THREADS * 4);
-        *reinterpret_cast<float4*>(out + threadIdx.x * 4) = make_float4(y[0], y[1], y[2], y[3]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sts_f(red + e * W4_WARPS * 128, y[e >> 2][e & 3]);
         __syncthreads();                                   // the buffer of two groups ago is free
-        constexpr int OUT = PAIR ? 2 : 4;                  // results per lane of a tile
-        for (int j = kw; j < OUT; j += KW) {
+        constexpr int EL = PAIR ? 4 : 8;                   // results per lane of a tile
+#pragma unroll
+        for (int u = 0; u < (RW * EL + W4_WARPS - 1) / W4_WARPS; ++u) {
+            const int o = warp + u * W4_WARPS;
+            if (o >= RW * EL) break;
+            const int w = o / EL, m = (o % EL) / (EL / 2), j = o % (EL / 2);
+            const uint32_t p = red + ((m * 4 + j) * W4_WARPS + w * KW - warp) * 128;
             float v = 0.f, v2 = 0.f;
 #pragma unroll
             for (int k = 0; k < KW; ++k) {
-                const float* p = out + ((rw * KW + k) * 32 + lane) * 4 + j;
-                v += p[0];
-                if (PAIR) v2 += p[2];
+                v += lds_f(p + k * 128);
+                if (PAIR) v2 += lds_f(p + (2 * W4_WARPS + k) * 128);
             }
-            if constexpr (PAIR) done(grp, j, v * 0x1p24f, v2 * 0x1p24f);
-            else done(grp, j, v * 0x1p24f);
+            if constexpr (PAIR) done(grp, w * 16 + m * 8 + g, 2 * t + j, v * 0x1p24f, v2 * 0x1p24f);
+            else done(grp, w * 32 + m * 16 + (j >> 1) * 8 + g, 2 * t + (j & 1), v * 0x1p24f);
         }
-        cur = next;
+        red += flip;                                       // the other buffer
+        flip = 0u - flip;
     }
-    cp_async_wait<0>();
-    __syncthreads();                                       // x, red and the ring free again
+    __syncthreads();                                       // x and red free again
 }
 
 // A kernel on the stream that may start before its predecessor on it has ended

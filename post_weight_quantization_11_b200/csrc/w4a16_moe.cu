@@ -16,7 +16,11 @@
 namespace gptq {
 
 constexpr int kMoeTokens = 64, kMoeExperts = 256, kMoeTopK = 8;
-constexpr int MOE_KW = 4, MOE_RW = 4;       // of w4_sweep
+constexpr int64_t kMoeMaxModel = 24576;     // a row of x has to fit beside the ring
+// Of w4_sweep: more column shares make finer row groups, fewer make longer ones
+constexpr int MOE_IN_KW = 8, MOE_IN_ROWS = 16 * (W4_WARPS / MOE_IN_KW);
+constexpr int MOE_OUT_KW = 4, MOE_OUT_ROWS = 32 * (W4_WARPS / MOE_OUT_KW);
+constexpr int kMoeSms = 148;               // the plan does not depend on the device that is current
 constexpr int kMoePairs = kMoeTokens * kMoeTopK;
 
 struct MoeRoutes;
@@ -163,17 +167,18 @@ __device__ __forceinline__ void moe_routes(const MoeParams& p, MoeRoutes& r, int
 // up rows, so that a lane holds both of an element of h.  The CTAs share the
 // row tiles of all chunks evenly; a CTA stages a chunk's tokens once.
 template <bool WIDE>
-__global__ void __launch_bounds__(W4_THREADS, 1) moe_in_kernel(const MoeParams p)
+__global__ void __launch_bounds__(W4_THREADS, 1) moe_in_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p)
 {
-    extern __shared__ __align__(16) uint8_t smem[];
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ int abort;
     __shared__ MoeRoutes r;
     __shared__ int cnt[kMoeExperts], off[kMoeExperts], coff[kMoeExperts];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int rw = warp / MOE_KW, g = lane >> 2, t = lane & 3;
-    const int steps = int(p.d / W4_STEP), groups = int(p.f / (8 * MOE_RW));
-    uint4* x = reinterpret_cast<uint4*>(smem);
-    float* xs = reinterpret_cast<float*>(smem + w4_x_bytes(steps, p.chunk, false));
-    float* red = xs + w4_xs_bytes(steps, WIDE) / 4;
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int steps = int(p.d / W4_STEP), groups = int(p.f / MOE_IN_ROWS);
+    uint4* x = reinterpret_cast<uint4*>(smem + W4_AT_X);
+    float* xs = reinterpret_cast<float*>(smem + W4_AT_X + w4_x_bytes(steps, p.chunk, false));
+    W4Pipe pipe = w4_pipe(smem, &abort);
     moe_routes(p, r, cnt, off, coff);
     if (blockIdx.x == 0) {                                 // for the second kernel
         const int* src = reinterpret_cast<const int*>(&r);
@@ -189,26 +194,20 @@ __global__ void __launch_bounds__(W4_THREADS, 1) moe_in_kernel(const MoeParams p
         const int e = r.expert[c], cols = r.n[c];
         const int* list = r.list + r.start[c];
         const int64_t row0 = int64_t(e) * 2 * p.f;
-        const W4Stage st{x, xs, cols, 0};
-        w4_sweep<MOE_KW, WIDE, false, true>(
-            p.in, st, red, g0, g1, 0, steps,
-            [&](int grp) {
-                const int64_t ra = row0 + int64_t(grp) * (8 * MOE_RW);
-                const uint32_t lr = rw * 8 + g;
-                return w4_rows(p.in, {ra, ra + p.f}, {lr, lr});
-            },
+        const W4Stage st{smem_u32(x), smem_u32(xs), cols, 0};
+        w4_sweep<MOE_IN_KW, WIDE, false, true>(
+            pipe, &tm, p.in, row0 + int64_t(g0) * MOE_IN_ROWS, row0 + 2 * p.f, uint32_t(p.f), st,
+            g1 - g0, 0, steps,
             [&]() {
                 w4_stage_half<WIDE>(
                     x, xs, [&](int n) { return p.x + int64_t(list[n] / p.k) * p.d; },
                     p.pi ? p.pi + e * p.d : nullptr, 0, steps, cols, int(p.d));
                 __syncthreads();
             },
-            [&](int grp, int j, float gate, float up) {
-                const int n = 2 * t + j;
-                if (n < cols) {
-                    p.h[int64_t(list[n]) * p.f + (int64_t(grp) * MOE_RW + rw) * 8 + g] =
+            [&](int grp, int r, int n, float gate, float up) {
+                if (n < cols)
+                    p.h[int64_t(list[n]) * p.f + int64_t(g0 + grp) * MOE_IN_ROWS + r] =
                         gate / (1.f + expf(-gate)) * up;
-                }
             });
         u += g1 - g0;
     }
@@ -216,18 +215,19 @@ __global__ void __launch_bounds__(W4_THREADS, 1) moe_in_kernel(const MoeParams p
 
 // part[slice][pair] = D h over a slice of the columns
 template <bool WIDE>
-__global__ void __launch_bounds__(W4_THREADS, 1) moe_out_kernel(const MoeParams p)
+__global__ void __launch_bounds__(W4_THREADS, 1) moe_out_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p)
 {
-    extern __shared__ __align__(16) uint8_t smem[];
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ int abort;
     __shared__ MoeRoutes r;
     __shared__ float undo[8];
     __shared__ uint32_t top[8];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int rw = warp / MOE_KW, g = lane >> 2, t = lane & 3;
-    const int groups = int(p.d / (16 * MOE_RW)), nsteps = int(p.f / W4_STEP);
-    uint4* x = reinterpret_cast<uint4*>(smem);
-    float* xs = reinterpret_cast<float*>(smem + w4_x_bytes(p.slice, p.chunk, true));
-    float* red = xs + w4_xs_bytes(p.slice, WIDE) / 4;
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int groups = int(p.d / MOE_OUT_ROWS), nsteps = int(p.f / W4_STEP);
+    uint4* x = reinterpret_cast<uint4*>(smem + W4_AT_X);
+    float* xs = reinterpret_cast<float*>(smem + W4_AT_X + w4_x_bytes(p.slice, p.chunk, true));
+    W4Pipe pipe = w4_pipe(smem, &abort);
     pdl_wait();
     for (int i = threadIdx.x; i < int(sizeof(MoeRoutes) / 4); i += blockDim.x)
         reinterpret_cast<int*>(&r)[i] = reinterpret_cast<const int*>(p.routes)[i];
@@ -243,25 +243,19 @@ __global__ void __launch_bounds__(W4_THREADS, 1) moe_out_kernel(const MoeParams 
         const int k0 = sl * p.slice, steps = min(p.slice, nsteps - k0);
         const int* list = r.list + r.start[c];
         const int64_t row0 = int64_t(e) * p.d;
-        const W4Stage st{x, xs, cols, steps * 16 * cols};
-        w4_sweep<MOE_KW, WIDE, true, false>(
-            p.out, st, red, g0, g1, k0, steps,
-            [&](int grp) {
-                const int64_t ra = row0 + int64_t(grp) * (16 * MOE_RW);
-                const uint32_t lr = rw * 16 + g;
-                return w4_rows(p.out, {ra, ra}, {lr, lr + 8});
-            },
+        const W4Stage st{smem_u32(x), smem_u32(xs), cols, uint32_t(steps * 256 * cols)};
+        w4_sweep<MOE_OUT_KW, WIDE, true, false>(
+            pipe, &tm, p.out, row0 + int64_t(g0) * MOE_OUT_ROWS, row0 + p.d, 0u, st, g1 - g0, k0,
+            steps,
             [&]() {
                 w4_stage_split<WIDE>(
                     x, xs, undo, top, [&](int n) { return p.h + int64_t(list[n]) * p.f; },
                     p.po ? p.po + e * p.f : nullptr, k0 * W4_STEP, steps, cols, int(p.f));
                 __syncthreads();
             },
-            [&](int grp, int j, float v) {
-                const int n = 2 * t + (j & 1);
+            [&](int grp, int r, int n, float v) {
                 if (n < cols)
-                    p.part[(int64_t(sl) * p.T * p.k + list[n]) * p.d +
-                           (int64_t(grp) * MOE_RW + rw) * 16 + g + 8 * (j >> 1)] = v * undo[n];
+                    p.part[(int64_t(sl) * p.T * p.k + list[n]) * p.d + int64_t(g0 + grp) * MOE_OUT_ROWS + r] = v * undo[n];
             });
         u += g1 - g0;
     }
@@ -292,16 +286,24 @@ struct MoePlan {
 
 // Tokens of an expert that are staged together (up to 8, the columns of one
 // product; fewer where a row of x is so long that they would not fit beside the
-// ring) and slices of the second product's columns.
-MoePlan moe_plan(int64_t T, int k, int64_t d, int64_t f)
+// ring) and slices of the second product's columns: as few as fit, or more where
+// few row groups would leave CTAs idle.  A group of a slice costs about 190
+// instructions a step and warp and 100 to join, and the slowest CTA counts.
+MoePlan moe_plan(int64_t T, int64_t E, int k, int64_t d, int64_t f)
 {
-    constexpr int MOST = 72 * 1024;                        // bytes of staged activations
+    constexpr int MOST = 80 * 1024;                        // bytes of staged activations and sums
     MoePlan m{};
     const int si = int(d / W4_STEP), so = int(f / W4_STEP);
-    m.chunk = int(std::min<int64_t>(std::min<int64_t>(T, W4_COLS), MOST / (256 * si)));
-    m.slice = std::min(so, std::max(1, MOST / (512 * m.chunk)));
-    m.slices = (so + m.slice - 1) / m.slice;
-    m.slice = (so + m.slices - 1) / m.slices;
+    m.chunk = int(std::min<int64_t>(std::min<int64_t>(T, W4_COLS), (MOST / si - 128) / 256));
+    const int most = std::min(so, MOST / (512 * m.chunk + 128));
+    const int64_t chunks = std::max(std::min(T * k, E), ceil_div(T * k, m.chunk));
+    double best = 1e300;
+    for (int s = (so + most - 1) / most; s <= std::min(so, 32); ++s) {
+        const int steps = (so + s - 1) / s;
+        const int64_t rounds = ceil_div(chunks * s * (d / MOE_OUT_ROWS), kMoeSms);
+        const double cost = double(rounds) * (((steps + MOE_OUT_KW - 1) / MOE_OUT_KW) * 190 + 100);
+        if (cost < best * 0.97) { best = cost; m.slice = steps; }
+    }
     m.slices = (so + m.slice - 1) / m.slice;
     m.smem_in = w4_smem(si, m.chunk, false, false);
     m.smem_out = w4_smem(m.slice, m.chunk, false, true);
@@ -318,10 +320,10 @@ extern "C" size_t gptq_w4a16_moe_workspace_bytes(int64_t tokens, int64_t n_exper
                                                  int64_t d_model, int64_t d_ff)
 {
     if (tokens <= 0 || n_experts <= 0 || top_k <= 0 || d_model <= 0 || d_ff <= 0) return 0;
-    if (tokens > gptq::kMoeTokens || top_k > gptq::kMoeTopK || d_model % 128 != 0 ||
-        d_ff % 128 != 0 || d_model > gptq::kMaxDim || d_ff > gptq::kMaxDim)
+    if (tokens > gptq::kMoeTokens || top_k > gptq::kMoeTopK || n_experts > gptq::kMoeExperts || d_model % 128 != 0 ||
+        d_ff % 128 != 0 || d_model > gptq::kMoeMaxModel || d_ff > gptq::kMaxDim)
         return 0;
-    return gptq::moe_plan(tokens, top_k, d_model, d_ff).bytes;
+    return gptq::moe_plan(tokens, n_experts, top_k, d_model, d_ff).bytes;
 }
 
 extern "C" int gptq_w4a16_moe(const uint16_t* x, int64_t tokens, const float* logits,
@@ -334,7 +336,7 @@ extern "C" int gptq_w4a16_moe(const uint16_t* x, int64_t tokens, const float* lo
                               void* stream)
 {
     using namespace gptq;
-    if (d_model < 128 || d_model > kMaxDim || d_model % 128 != 0 || d_ff < 128 || d_ff > kMaxDim ||
+    if (d_model < 128 || d_model > kMoeMaxModel || d_model % 128 != 0 || d_ff < 128 || d_ff > kMaxDim ||
         d_ff % 128 != 0 || tokens < 0 || n_experts < 1 || top_k < 1)
         return GPTQ_ERR_SHAPE;
     if (tokens > kMoeTokens || n_experts > kMoeExperts || top_k > kMoeTopK || top_k > n_experts)
@@ -353,7 +355,7 @@ extern "C" int gptq_w4a16_moe(const uint16_t* x, int64_t tokens, const float* lo
         return GPTQ_ERR_INVALID_ARG;
     if (ws_bytes < gptq_w4a16_moe_workspace_bytes(tokens, n_experts, top_k, d_model, d_ff))
         return GPTQ_ERR_INVALID_ARG;
-    const MoePlan plan = moe_plan(tokens, top_k, d_model, d_ff);
+    const MoePlan plan = moe_plan(tokens, n_experts, top_k, d_model, d_ff);
     MoeParams p{};
     p.x = reinterpret_cast<const __half*>(x);
     p.logits = logits;
@@ -381,9 +383,13 @@ extern "C" int gptq_w4a16_moe(const uint16_t* x, int64_t tokens, const float* lo
                              (int)plan.smem_out) != cudaSuccess)
         return GPTQ_ERR_CUDA;
     const int64_t pairs = tokens * top_k;
-    in<<<ctas(pairs * (d_ff / (8 * MOE_RW))), W4_THREADS, plan.smem_in, st>>>(p);
-    if (launch_after(out, ctas(pairs * plan.slices * (d_model / (16 * MOE_RW))),
-                     W4_THREADS, plan.smem_out, st, p) != cudaSuccess ||
+    CUtensorMap ti, to;
+    if (w4_tmap(&ti, qweight_in, n_experts * 2 * d_ff, d_model, 16) != GPTQ_OK ||
+        w4_tmap(&to, qweight_out, n_experts * d_model, d_ff, 32) != GPTQ_OK)
+        return GPTQ_ERR_CUDA;
+    in<<<ctas(pairs * (d_ff / MOE_IN_ROWS)), W4_THREADS, plan.smem_in, st>>>(ti, p);
+    if (launch_after(out, ctas(pairs * plan.slices * (d_model / MOE_OUT_ROWS)),
+                     W4_THREADS, plan.smem_out, st, to, p) != cudaSuccess ||
         launch_after(moe_join_kernel, dim3((unsigned)ceil_div(d_model, 256), (unsigned)tokens), 256,
                      0, st, p) != cudaSuccess)
         return GPTQ_ERR_CUDA;
