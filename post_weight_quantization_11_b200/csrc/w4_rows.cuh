@@ -15,9 +15,10 @@
 //    applied; the zero point is applied there too, through the group's sum of
 //    x.  1.25 ALU instructions an operand register, against 2.75 for codes in
 //    the mantissa of 1024.  Products (11 by 4 bits) are exact, sums fp32.
-//  * Every warp has its own ring of W4_RING steps in shared memory, filled by one
-//    TMA copy a step (32 rows x 64 bytes, 64-byte swizzle) that runs ahead across
-//    row tiles: no barrier between warps, no registers, two instructions a step.
+//  * Every warp has its own ring of W4_RING slots of two steps in shared memory,
+//    filled by TMA copies that run ahead across row tiles: no barrier between
+//    warps and no registers.  With the 128-byte swizzle, and lane g of an operand
+//    on row (g >> 1) + 4 (g & 1) of its eight, the reads hit every bank once.
 //    (A ring of four steps in registers was bound by waiting for loads: a wait
 //    on one load waits for the younger ones that share its scoreboard.)
 //  * 32 rows a warp share each read of x.
@@ -37,8 +38,8 @@
 namespace gptq {
 
 constexpr int W4_THREADS = 512;
-constexpr int W4_RING = 3;                        // steps in flight per warp
-constexpr int W4_SLOT = 2048;                     // bytes of one
+constexpr int W4_RING = 2;                        // slots in flight per warp
+constexpr int W4_SLOT = 4096;                     // bytes of one: two steps of 32 rows
 constexpr int W4_STEP = 128;                      // columns per step
 constexpr int W4_COLS = 8;                        // columns n of a product
 
@@ -155,39 +156,39 @@ struct W4Stage {
     uint32_t plane;        // bytes of one plane
 };
 
-// The 16-byte part t of row r of a slot (rows of 64 bytes, 64-byte swizzle) is at 64 r
-// + 16 (t ^ ((r >> 1) & 3)): the eight rows of an operand hit 32 banks, in 16-byte
-// reads and in 32-bit ones.  Rows 8 apart have the same place in their 512 bytes.
-// Row 8 i + g of the warp's m16 tile m is row 16 m + 8 i + g of a slot; PAIR: 16 i
-// + 8 m + g (rows 0 .. 15 are gate rows, 16 .. 31 the up rows of the same elements).
+// A slot: rows of 128 bytes (two steps), the 16-byte part 4 u + t of row r (part t of
+// step u) at 128 r + 16 ((4 u + t) ^ (r & 7)).  Row 8 i + w4_rho(g) of the warp's m16
+// tile m is row 16 m + 8 i + w4_rho(g) of a slot; PAIR: row 8 m + w4_rho(g) of the gate
+// rows (i = 0) or of the up rows, which have the slot's second half.
+__device__ __forceinline__ int w4_rho(int g) { return (g >> 1) + 4 * (g & 1); }
 template <bool PAIR> __host__ __device__ constexpr int w4_row(int m, int i)
 {
     return PAIR ? i * 16 + m * 8 : m * 16 + i * 8;
 }
 
-// y += 2^-24 times the step's product.  slot: shared address of the step's rows, of
-// the lane's part of row g; WIDE: its part t, else row g itself.  p: w4_params of
+// y += 2^-24 times the step's product.  slot: shared address of the lane's row; WIDE:
+// of its part t of the step, else of word t of the row.  u: the step of the slot.  p: w4_params of
 // the lane's rows, held by lane t of the quad for (WIDE) step src of four or
 // (otherwise) block t of this step.
 template <bool WIDE, bool SPLIT, bool PAIR>
-__device__ __forceinline__ void w4_step(float (&y)[2][4], uint32_t slot, const uint32_t (&p)[2][2],
+__device__ __forceinline__ void w4_step(float (&y)[2][4], uint32_t slot, int u, const uint32_t (&p)[2][2],
                                         int src, uint32_t x, uint32_t xs, uint32_t xw,
                                         uint32_t plane)
 {
     constexpr uint32_t LO = 0x000F000Fu, HI = 0x00F000F0u;
-    const int g = (threadIdx.x & 31) >> 2;
+    const int rho = w4_rho((threadIdx.x & 31) >> 2);
     uint32_t q[2][2][4];
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             if constexpr (WIDE) {
-                const uint4 v = lds16(slot + w4_row<PAIR>(m, i) * 64);
+                const uint4 v = lds16(slot + w4_row<PAIR>(m, i) * 128);
                 q[m][i][0] = v.x; q[m][i][1] = v.y; q[m][i][2] = v.z; q[m][i][3] = v.w;
             } else {
 #pragma unroll
                 for (int w = 0; w < 4; ++w)
-                    q[m][i][w] = lds4(slot + w4_row<PAIR>(m, i) * 64 + (w ^ ((g >> 1) & 3)) * 16);
+                    q[m][i][w] = lds4(slot + w4_row<PAIR>(m, i) * 128 + ((4 * u + w) ^ rho) * 16);
             }
         }
     float lo[2][4], hi[2][4];
@@ -375,12 +376,12 @@ __device__ __forceinline__ void w4_stage_split(uint4* x, float* xs, float* undo,
     }
 }
 
-// Dynamic shared memory of a kernel with sweeps: the ring, the joining buffers,
+// Dynamic shared memory of a kernel with sweeps: the ring, the joining buffer,
 // the barriers, then the staged activations and their sums
 constexpr int W4_WARPS = W4_THREADS / 32;
-constexpr int W4_RED = W4_WARPS * 32 * 8;                    // floats of one joining buffer
+constexpr int W4_RED = W4_WARPS * 32 * 8;                    // floats of the joining buffer
 constexpr size_t W4_AT_RED = size_t(W4_WARPS) * W4_RING * W4_SLOT;
-constexpr size_t W4_AT_BAR = W4_AT_RED + 2 * W4_RED * 4;
+constexpr size_t W4_AT_BAR = W4_AT_RED + W4_RED * 4;
 constexpr size_t W4_AT_X = W4_AT_BAR + 512;
 static_assert(W4_WARPS * W4_RING * 8 <= 512, "barriers");
 inline __host__ __device__ size_t w4_x_bytes(int steps, int cols, bool split)
@@ -397,11 +398,22 @@ inline size_t w4_smem(int steps, int cols, bool wide, bool split)
     return 1024 + W4_AT_X + w4_x_bytes(steps, cols, split) + w4_xs_bytes(steps, wide);
 }
 
-// The packed rows as a TMA tensor, in boxes of 64 bytes x `rows`
+// The packed rows as a TMA tensor, in boxes of `rows` rows and two steps
 inline int w4_tmap(CUtensorMap* tm, const uint32_t* qw, int64_t rows, int64_t d, int box_rows)
 {
     return encode_tmap_2d(tm, CU_TENSOR_MAP_DATA_TYPE_UINT32, qw, uint64_t(d / 8), uint64_t(rows),
-                          uint64_t(d / 2), 16, uint32_t(box_rows), CU_TENSOR_MAP_SWIZZLE_64B);
+                          uint64_t(d / 2), 32, uint32_t(box_rows), CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+__device__ __forceinline__ bool w4_elect()
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok));
+    return ok != 0;
 }
 
 // A warp's ring (shared addresses)
@@ -415,7 +427,7 @@ struct W4Pipe {
 // All threads; with a barrier
 __device__ __forceinline__ W4Pipe w4_pipe(uint8_t* smem, int* abort)
 {
-    const int warp = threadIdx.x >> 5;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);    // uniform
     W4Pipe p;
     p.ring = smem_u32(smem) + warp * (W4_RING * W4_SLOT);
     p.red = smem_u32(smem) + uint32_t(W4_AT_RED);
@@ -477,17 +489,17 @@ __device__ __forceinline__ void w4_sweep(W4Pipe& pipe, const CUtensorMap* tm, co
                                          StageF stage, DoneF done)
 {
     constexpr int RW = W4_WARPS / KW, ROWS = PAIR ? 16 : 32;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = lane & 3, g = lane >> 2;
+    const int lane = threadIdx.x & 31, t = lane & 3, g = lane >> 2;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);    // uniform
     const int kw = warp % KW, rw = warp / KW;
     const int s0 = steps * kw / KW, n = steps * (kw + 1) / KW - s0;
-    // producer (lane 0): the rows and words of the next copy, copies left of the
-    // row tile and in all
-    const int col0 = (k0 + s0) * 16;
-    int prow = int(row0) + rw * ROWS, pcol = col0, pleft = n, left = n * groups;
+    // producer: the rows and step of the next copy, steps left of the row tile,
+    // row tiles left
+    const int first_step = k0 + s0;
+    int prow = int(row0) + rw * ROWS, pstep = first_step, pleft = n, tiles = n ? groups : 0;
     auto issue = [&]() {
-        if (left == 0) return;
-        --left;
-        if (lane == 0) {
+        if (tiles == 0) return;
+        if (w4_elect()) {
             const uint32_t dst = pipe.ring + pipe.put * W4_SLOT, bar = pipe.bar + pipe.put * 8;
             asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar),
                          "r"(W4_SLOT)
@@ -495,34 +507,36 @@ __device__ __forceinline__ void w4_sweep(W4Pipe& pipe, const CUtensorMap* tm, co
             auto copy = [&](uint32_t to, int row) {
                 asm volatile(
                     "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
-                    " [%0], [%1, {%3, %4}], [%2];" ::"r"(to), "l"(reinterpret_cast<uint64_t>(tm)),
-                    "r"(bar), "r"(pcol), "r"(row)
+                    " [%0], [%1, {%3, %4}], [%2];" ::"r"(to),
+                    "l"(reinterpret_cast<uint64_t>(tm)), "r"(bar), "r"(pstep * 16), "r"(row)
                     : "memory");
             };
             copy(dst, prow);
             if (PAIR) copy(dst + W4_SLOT / 2, prow + int(pair));
         }
-        pipe.put = pipe.put + 1 == W4_RING ? 0 : pipe.put + 1;
-        pcol += 16;
-        if (--pleft == 0) { pleft = n; pcol = col0; prow += RW * ROWS; }
+        pipe.put ^= 1u;
+        pstep += 2;
+        pleft -= 2;
+        if (pleft <= 0) { pleft = n; pstep = first_step; prow += RW * ROWS; --tiles; }
     };
-#pragma unroll
-    for (int i = 0; i < W4_RING; ++i) issue();
+    static_assert(W4_RING == 2, "pipe.put and get");
+    issue();
+    issue();
     // scales and zero points: WIDE: of four steps at a time (lane t those of step
     // t), four steps ahead; else of block t of a step, one step ahead
     const __half* sc = l.sc + row0 * l.G;
     const uint8_t* qz = l.qz + row0 * l.Gb;
     const uint32_t last = uint32_t(end - row0 - 1);
     auto params = [&](uint32_t (&p)[2][2], int grp, int j) {
-        const uint32_t block = (k0 + s0 + min(j + (WIDE ? t : 0), n - 1)) * 4 + (WIDE ? 0 : t);
+        const uint32_t block = (first_step + min(j + (WIDE ? t : 0), n - 1)) * 4 + (WIDE ? 0 : t);
         const uint32_t at = (block * l.grp.mul) >> 22;
-        const uint32_t first = (grp * RW + rw) * ROWS + g;
+        const uint32_t first = (grp * RW + rw) * ROWS + w4_rho(g);
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const uint32_t r = PAIR ? first + m * 8 + i * pair
-                                        : min(first + w4_row<PAIR>(m, i), last);
+                                        : min(first + m * 16 + i * 8, last);
                 p[m][i] = w4_params(l, sc, qz, r, at);
             }
     };
@@ -533,31 +547,40 @@ __device__ __forceinline__ void w4_sweep(W4Pipe& pipe, const CUtensorMap* tm, co
     const uint32_t xw = st.cols * 64;
     const uint32_t x0 = st.x + (min(g, st.cols - 1) * 4 + t) * 16 + s0 * 4 * xw;
     const uint32_t xs0 = st.xs + s0 * (WIDE ? 1 : 4) * W4_COLS * 4 + t * 8;
-    const uint32_t from = pipe.ring + g * 64 + (WIDE ? (t ^ ((g >> 1) & 3)) * 16 : t * 4);
-    uint32_t red = pipe.red + (warp * 32 + lane) * 4, flip = W4_RED * 4;
+    const uint32_t from = pipe.ring + w4_rho(g) * 128 + (WIDE ? (t ^ w4_rho(g)) * 16 : t * 4);
+    const uint32_t red = pipe.red + (warp * 32 + lane) * 4;
     for (int grp = 0; grp < groups; ++grp) {
         float y[2][4] = {};
         uint32_t x = x0, xs = xs0;
 #pragma unroll 1
-        for (int j = 0; j < n; ++j) {
-            if (j % EVERY == 0) {
-#pragma unroll
-                for (int m = 0; m < 2; ++m) { par[m][0] = ahead[m][0]; par[m][1] = ahead[m][1]; }
-                if (j + EVERY < n) params(ahead, grp, j + EVERY);
-                else params(ahead, min(grp + 1, groups - 1), 0);
-            }
+        for (int j = 0; j < n; j += 2) {
             if (!w4_try_wait(pipe.bar + pipe.get * 8, pipe.phase))
                 w4_wait_long(pipe.bar + pipe.get * 8, pipe.phase, pipe.abort);
-            w4_step<WIDE, SPLIT, PAIR>(y, from + pipe.get * W4_SLOT, par, j & 3, x, xs, xw, st.plane);
-            if (++pipe.get == W4_RING) { pipe.get = 0; pipe.phase ^= 1u; }
-            x += 4 * xw;
-            xs += (WIDE ? 1 : 4) * W4_COLS * 4;
+            const uint32_t slot = from + pipe.get * W4_SLOT;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                if (j + u < n) {
+                    if ((j + u) % EVERY == 0) {
+#pragma unroll
+                        for (int m = 0; m < 2; ++m) { par[m][0] = ahead[m][0]; par[m][1] = ahead[m][1]; }
+                        if (j + u + EVERY < n) params(ahead, grp, j + u + EVERY);
+                        else params(ahead, min(grp + 1, groups - 1), 0);
+                    }
+                    w4_step<WIDE, SPLIT, PAIR>(y, WIDE ? slot ^ (64 * u) : slot, u, par, (j & 2) + u,
+                                               x, xs, xw, st.plane);
+                    x += 4 * xw;
+                    xs += (WIDE ? 1 : 4) * W4_COLS * 4;
+                }
+            }
+            pipe.phase ^= pipe.get;
+            pipe.get ^= 1u;
             __syncwarp();                                  // every lane has read its slot
             issue();
         }
+        if (grp) __syncthreads();                          // the last group's sums have been read
 #pragma unroll
         for (int e = 0; e < 8; ++e) sts_f(red + e * W4_WARPS * 128, y[e >> 2][e & 3]);
-        __syncthreads();                                   // the buffer of two groups ago is free
+        __syncthreads();
         constexpr int EL = PAIR ? 4 : 8;                   // results per lane of a tile
 #pragma unroll
         for (int u = 0; u < (RW * EL + W4_WARPS - 1) / W4_WARPS; ++u) {
@@ -571,11 +594,9 @@ __device__ __forceinline__ void w4_sweep(W4Pipe& pipe, const CUtensorMap* tm, co
                 v += lds_f(p + k * 128);
                 if (PAIR) v2 += lds_f(p + (2 * W4_WARPS + k) * 128);
             }
-            if constexpr (PAIR) done(grp, w * 16 + m * 8 + g, 2 * t + j, v * 0x1p24f, v2 * 0x1p24f);
-            else done(grp, w * 32 + m * 16 + (j >> 1) * 8 + g, 2 * t + (j & 1), v * 0x1p24f);
+            if constexpr (PAIR) done(grp, w * 16 + m * 8 + w4_rho(g), 2 * t + j, v * 0x1p24f, v2 * 0x1p24f);
+            else done(grp, w * 32 + m * 16 + (j >> 1) * 8 + w4_rho(g), 2 * t + (j & 1), v * 0x1p24f);
         }
-        red += flip;                                       // the other buffer
-        flip = 0u - flip;
     }
     __syncthreads();                                       // x and red free again
 }

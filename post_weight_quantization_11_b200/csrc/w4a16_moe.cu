@@ -42,7 +42,7 @@ struct MoeParams {
 };
 
 // One warp: the routes of token t into ids / w[0 .. k)
-__device__ __forceinline__ void moe_route(const float* logits, int E, int k, int renorm, int* ids,
+__device__ __forceinline__ void moe_route(const float* logits, int E, int k, int renorm, int16_t* ids,
                                           float* w)
 {
     constexpr uint32_t ALL = 0xffffffffu;
@@ -94,11 +94,11 @@ __device__ __forceinline__ void moe_route(const float* logits, int E, int k, int
 // one expert, in expert order
 struct MoeRoutes {
     int chunks;
-    int expert[kMoePairs];
-    int start[kMoePairs];                  // in list
-    int n[kMoePairs];
-    int list[kMoePairs];                   // pairs (t k + j), expert by expert
-    int id[kMoePairs];                     // expert of each pair, -1: none
+    int16_t expert[kMoePairs];
+    int16_t start[kMoePairs];              // in list
+    int16_t n[kMoePairs];
+    int16_t list[kMoePairs];               // pairs (t k + j), expert by expert
+    int16_t id[kMoePairs];                 // expert of each pair, -1: none
     float w[kMoePairs];
 };
 
@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(W4_THREADS, 1) moe_in_kernel(const __grid_cons
         const int c = int(u / groups), g0 = int(u - int64_t(c) * groups);
         const int g1 = int(min(int64_t(groups), g0 + (u1 - u)));
         const int e = r.expert[c], cols = r.n[c];
-        const int* list = r.list + r.start[c];
+        const int16_t* list = r.list + r.start[c];
         const int64_t row0 = int64_t(e) * 2 * p.f;
         const W4Stage st{smem_u32(x), smem_u32(xs), cols, 0};
         w4_sweep<MOE_IN_KW, WIDE, false, true>(
@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(W4_THREADS, 1) moe_out_kernel(const __grid_con
         const int c = cs / p.slices, sl = cs - c * p.slices;
         const int e = r.expert[c], cols = r.n[c];
         const int k0 = sl * p.slice, steps = min(p.slice, nsteps - k0);
-        const int* list = r.list + r.start[c];
+        const int16_t* list = r.list + r.start[c];
         const int64_t row0 = int64_t(e) * p.d;
         const W4Stage st{smem_u32(x), smem_u32(xs), cols, uint32_t(steps * 256 * cols)};
         w4_sweep<MOE_OUT_KW, WIDE, true, false>(
@@ -291,7 +291,7 @@ struct MoePlan {
 // instructions a step and warp and 100 to join, and the slowest CTA counts.
 MoePlan moe_plan(int64_t T, int64_t E, int k, int64_t d, int64_t f)
 {
-    constexpr int MOST = 80 * 1024;                        // bytes of staged activations and sums
+    constexpr int MOST = 68 * 1024;                        // bytes of staged activations and sums
     MoePlan m{};
     const int si = int(d / W4_STEP), so = int(f / W4_STEP);
     m.chunk = int(std::min<int64_t>(std::min<int64_t>(T, W4_COLS), (MOST / si - 128) / 256));
@@ -301,7 +301,7 @@ MoePlan moe_plan(int64_t T, int64_t E, int k, int64_t d, int64_t f)
     for (int s = (so + most - 1) / most; s <= std::min(so, 32); ++s) {
         const int steps = (so + s - 1) / s;
         const int64_t rounds = ceil_div(chunks * s * (d / MOE_OUT_ROWS), kMoeSms);
-        const double cost = double(rounds) * (((steps + MOE_OUT_KW - 1) / MOE_OUT_KW) * 190 + 100);
+        const double cost = double(rounds) * (((steps + 2 * MOE_OUT_KW - 1) / (2 * MOE_OUT_KW)) * 2 * 190 + 100);
         if (cost < best * 0.97) { best = cost; m.slice = steps; }
     }
     m.slices = (so + m.slice - 1) / m.slice;
