@@ -133,15 +133,31 @@ inline W4Layer w4_layer(const uint32_t* qw, const uint16_t* sc, const uint8_t* q
     return l;
 }
 
-// Scale (low half) and minus the zero point (high half) as fp16, of group grp of
-// a row; sc, qz: of the sweep's first row
-__device__ __forceinline__ uint32_t w4_params(const W4Layer& l, const __half* sc, const uint8_t* qz,
-                                              uint32_t row, uint32_t grp)
+// Scale and byte of zero points of a group of the lane's four rows, as loaded: what
+// is computed from them waits for the loads, so that is done a round later
+struct W4Raw {
+    uint32_t s[2][2], z[2][2];
+    uint32_t shift;                        // of the zero point in its byte
+};
+
+__device__ __forceinline__ uint32_t ld_nc_u16(const void* p)
 {
-    const uint32_t s = __half_as_ushort(sc[row * uint32_t(l.G) + grp]);
-    const uint32_t z = (uint32_t(qz[row * uint32_t(l.Gb) + (grp >> 1)]) >> (4 * (grp & 1))) & 15u;
-    const __half m = __hsub(__ushort_as_half((unsigned short)0x6400),
-                            __ushort_as_half((unsigned short)(0x6400u | z)));   // 1024 - (1024 + z)
+    uint16_t v;
+    asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint32_t ld_nc_u8(const void* p)
+{
+    uint32_t v;
+    asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+
+// Scale (low half) and minus the zero point (high half) as fp16
+__device__ __forceinline__ uint32_t w4_param(uint32_t s, uint32_t z, uint32_t shift)
+{
+    const __half m = __hsub(__ushort_as_half((unsigned short)0x6400),      // 1024 - (1024 + z)
+                            __ushort_as_half((unsigned short)(0x6400u | ((z >> shift) & 15u))));
     return s | (uint32_t(__half_as_ushort(m)) << 16);
 }
 
@@ -167,7 +183,7 @@ template <bool PAIR> __host__ __device__ constexpr int w4_row(int m, int i)
 }
 
 // y += 2^-24 times the step's product.  slot: shared address of the lane's row; WIDE:
-// of its part t of the step, else of word t of the row.  u: the step of the slot.  p: w4_params of
+// of its part t of the step, else of word t of the row.  u: the step of the slot.  p: w4_param of
 // the lane's rows, held by lane t of the quad for (WIDE) step src of four or
 // (otherwise) block t of this step.
 template <bool WIDE, bool SPLIT, bool PAIR>
@@ -527,21 +543,24 @@ __device__ __forceinline__ void w4_sweep(W4Pipe& pipe, const CUtensorMap* tm, co
     const __half* sc = l.sc + row0 * l.G;
     const uint8_t* qz = l.qz + row0 * l.Gb;
     const uint32_t last = uint32_t(end - row0 - 1);
-    auto params = [&](uint32_t (&p)[2][2], int grp, int j) {
+    auto params = [&](W4Raw& p, int grp, int j) {
         const uint32_t block = (first_step + min(j + (WIDE ? t : 0), n - 1)) * 4 + (WIDE ? 0 : t);
         const uint32_t at = (block * l.grp.mul) >> 22;
         const uint32_t first = (grp * RW + rw) * ROWS + w4_rho(g);
+        p.shift = 4 * (at & 1);
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const uint32_t r = PAIR ? first + m * 8 + i * pair
                                         : min(first + m * 16 + i * 8, last);
-                p[m][i] = w4_params(l, sc, qz, r, at);
+                p.s[m][i] = ld_nc_u16(sc + (r * uint32_t(l.G) + at));
+                p.z[m][i] = ld_nc_u8(qz + (r * uint32_t(l.Gb) + (at >> 1)));
             }
     };
     constexpr int EVERY = WIDE ? 4 : 1;
-    uint32_t par[2][2] = {}, ahead[2][2] = {};
+    uint32_t par[2][2] = {};
+    W4Raw ahead{};
     if (n) params(ahead, 0, 0);
     stage();
     const uint32_t xw = st.cols * 64;
@@ -562,7 +581,10 @@ __device__ __forceinline__ void w4_sweep(W4Pipe& pipe, const CUtensorMap* tm, co
                 if (j + u < n) {
                     if ((j + u) % EVERY == 0) {
 #pragma unroll
-                        for (int m = 0; m < 2; ++m) { par[m][0] = ahead[m][0]; par[m][1] = ahead[m][1]; }
+                        for (int m = 0; m < 2; ++m)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                par[m][i] = w4_param(ahead.s[m][i], ahead.z[m][i], ahead.shift);
                         if (j + u + EVERY < n) params(ahead, grp, j + u + EVERY);
                         else params(ahead, min(grp + 1, groups - 1), 0);
                     }
