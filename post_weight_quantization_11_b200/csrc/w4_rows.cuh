@@ -6,15 +6,19 @@
 //
 // A CTA has 16 warps = KW shares of the columns x RW row tiles of 32 rows.  A
 // step is 128 columns of a row tile: 64 bytes a row, 2 KB a warp.
-//  * Products on m16n8k16 mma.sync, fp16 x fp16 -> fp32, rows as A, up to eight
-//    columns n.  A nibble alone in its half word is the fp16 subnormal c 2^-24,
+//  * Products on m16n8k16 mma.sync, fp16 x fp16 -> fp32, rows as A, up to 8
+//    NT columns n.  A nibble alone in its half word is the fp16 subnormal c 2^-24,
 //    and four bits up it is c 2^-20: one AND makes an operand register of two
 //    codes (nibbles 0 and 4, then 2 and 6, of the low positions; 1 and 5, 3 and
-//    7 of the high ones), with no OR, subtraction or conversion.  The two
-//    positions have their own accumulators, joined when the group's scale is
-//    applied; the zero point is applied there too, through the group's sum of
-//    x.  1.25 ALU instructions an operand register, against 2.75 for codes in
-//    the mantissa of 1024.  Products (11 by 4 bits) are exact, sums fp32.
+//    7 of the high ones).  The two positions have their own accumulators, joined
+//    when the group's scale is applied; the zero point is applied there too,
+//    through the group's sum of x.  Products (11 by 4 bits) are exact.  The
+//    matrix pipe aligns a subnormal operand's products by the exponent field, so
+//    its sums lose the operand's leading zero bits: 7 to 10 in the low position,
+//    which is therefore made normal (times 2^10, one packed multiplication on the
+//    otherwise idle FMA pipe), 3 to 6 in the high one, which is left.  Relative
+//    error of a 4096-column product against float64: 4.3e-6 without the
+//    multiplication.
 //  * Every warp has its own ring of W4_RING slots of two steps in shared memory,
 //    filled by TMA copies that run ahead across row tiles: no barrier between
 //    warps and no registers.  With the 128-byte swizzle, and lane g of an operand
@@ -41,7 +45,7 @@ constexpr int W4_THREADS = 512;
 constexpr int W4_RING = 2;                        // slots in flight per warp
 constexpr int W4_SLOT = 4096;                     // bytes of one: two steps of 32 rows
 constexpr int W4_STEP = 128;                      // columns per step
-constexpr int W4_COLS = 8;                        // columns n of a product
+constexpr int W4_COLS = 8;                        // columns n of an operand
 
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch()
@@ -69,6 +73,13 @@ __device__ __forceinline__ void mma_16816_first(float (&c)[4], uint32_t a0, uint
         "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
         : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// Two codes c 2^-24 -> c 2^-14
+__device__ __forceinline__ uint32_t w4_normal(uint32_t v)
+{
+    const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&v), __float2half2_rn(1024.f));
+    return *reinterpret_cast<const uint32_t*>(&r);
 }
 
 // Shared memory by its 32-bit address
@@ -163,8 +174,8 @@ __device__ __forceinline__ uint32_t w4_param(uint32_t s, uint32_t z, uint32_t sh
 
 // Staged activations: chunk ((step 4 + w) cols + n) 4 + t of 16 bytes holds, for
 // column n, the columns 128 step + 32 t + 8 w .. (WIDE) or 128 step + 32 w + 8 t ..
-// in the order 0 4 2 6 1 5 3 7; SPLIT: a second plane behind the first.  xs: 2^-24
-// times the sums of a step's 128 (WIDE) or 32 columns, 8 floats each.  Lanes of
+// in the order 0 4 2 6 1 5 3 7; SPLIT: a second plane behind the first.  xs: 2^-14
+// times the sums of a step's 128 (WIDE) or 32 columns, 8 NT floats each.  Lanes of
 // columns behind cols read another column; their results are not used.
 struct W4Stage {
     uint32_t x, xs;        // shared addresses
@@ -182,14 +193,15 @@ template <bool PAIR> __host__ __device__ constexpr int w4_row(int m, int i)
     return PAIR ? i * 16 + m * 8 : m * 16 + i * 8;
 }
 
-// y += 2^-24 times the step's product.  slot: shared address of the lane's row; WIDE:
+// y += 2^-14 times the step's product.  slot: shared address of the lane's row; WIDE:
 // of its part t of the step, else of word t of the row.  u: the step of the slot.  p: w4_param of
 // the lane's rows, held by lane t of the quad for (WIDE) step src of four or
 // (otherwise) block t of this step.
-template <bool WIDE, bool SPLIT, bool PAIR>
-__device__ __forceinline__ void w4_step(float (&y)[2][4], uint32_t slot, int u, const uint32_t (&p)[2][2],
-                                        int src, uint32_t x, uint32_t xs, uint32_t xw,
-                                        uint32_t plane)
+// x[c]: shared address of the lane's part of operand column 8 c + g.
+template <int NT, bool WIDE, bool SPLIT, bool PAIR>
+__device__ __forceinline__ void w4_step(float (&y)[NT][2][4], uint32_t slot, int u,
+                                        const uint32_t (&p)[2][2], int src, uint32_t (&x)[NT],
+                                        uint32_t xs, uint32_t xw, uint32_t plane)
 {
     constexpr uint32_t LO = 0x000F000Fu, HI = 0x00F000F0u;
     const int rho = w4_rho((threadIdx.x & 31) >> 2);
@@ -207,39 +219,56 @@ __device__ __forceinline__ void w4_step(float (&y)[2][4], uint32_t slot, int u, 
                     q[m][i][w] = lds4(slot + w4_row<PAIR>(m, i) * 128 + ((4 * u + w) ^ rho) * 16);
             }
         }
-    float lo[2][4], hi[2][4];
+    float lo[NT][2][4], hi[NT][2][4];
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
+        uint32_t a[2][4], b[2][4];                         // operands of the low and high nibbles
 #pragma unroll
-        for (int h = 0; h < (SPLIT ? 2 : 1); ++h) {
-            const uint4 f = lds16(h ? x + plane : x);
+        for (int m = 0; m < 2; ++m) {
+            const uint32_t v0 = q[m][0][w], v1 = q[m][1][w], w0 = v0 >> 8, w1 = v1 >> 8;
+            a[m][0] = w4_normal(v0 & LO); a[m][1] = w4_normal(v1 & LO);
+            a[m][2] = w4_normal(w0 & LO); a[m][3] = w4_normal(w1 & LO);
+            b[m][0] = v0 & HI; b[m][1] = v1 & HI; b[m][2] = w0 & HI; b[m][3] = w1 & HI;
+        }
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                const uint32_t a = q[m][0][w], b = q[m][1][w], a8 = a >> 8, b8 = b >> 8;
-                if (h == 0 && (!WIDE || w == 0)) {
-                    mma_16816_first(lo[m], a & LO, b & LO, a8 & LO, b8 & LO, f.x, f.y);
-                    mma_16816_first(hi[m], a & HI, b & HI, a8 & HI, b8 & HI, f.z, f.w);
-                } else {
-                    mma_16816(lo[m], a & LO, b & LO, a8 & LO, b8 & LO, f.x, f.y);
-                    mma_16816(hi[m], a & HI, b & HI, a8 & HI, b8 & HI, f.z, f.w);
+        for (int c = 0; c < NT; ++c) {
+#pragma unroll
+            for (int h = 0; h < (SPLIT ? 2 : 1); ++h) {
+                const uint4 f = lds16(h ? x[c] + plane : x[c]);
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    if (h == 0 && (!WIDE || w == 0)) {
+                        mma_16816_first(lo[c][m], a[m][0], a[m][1], a[m][2], a[m][3], f.x, f.y);
+                        mma_16816_first(hi[c][m], b[m][0], b[m][1], b[m][2], b[m][3], f.z, f.w);
+                    } else {
+                        mma_16816(lo[c][m], a[m][0], a[m][1], a[m][2], a[m][3], f.x, f.y);
+                        mma_16816(hi[c][m], b[m][0], b[m][1], b[m][2], b[m][3], f.z, f.w);
+                    }
                 }
             }
+            x[c] += xw;
         }
-        x += xw;
         if (!WIDE || w == 3) {
-            const float2 k = lds_f2(xs + (WIDE ? 0 : w * W4_COLS * 4));
+            float2 sz[2][2];
 #pragma unroll
             for (int m = 0; m < 2; ++m)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const uint32_t u = __shfl_sync(0xffffffffu, p[m][i], WIDE ? src : w, 4);
-                    const float2 sz = __half22float2(*reinterpret_cast<const __half2*>(&u));
-#pragma unroll
-                    for (int e = 2 * i; e < 2 * i + 2; ++e) {
-                        const float c = fmaf(hi[m][e], 0.0625f, lo[m][e]);   // 2^-24 sum c x
-                        y[m][e] = fmaf(sz.x, fmaf(sz.y, (e & 1) ? k.y : k.x, c), y[m][e]);
-                    }
+                    const uint32_t v = __shfl_sync(0xffffffffu, p[m][i], WIDE ? src : w, 4);
+                    sz[m][i] = __half22float2(*reinterpret_cast<const __half2*>(&v));
                 }
+#pragma unroll
+            for (int c = 0; c < NT; ++c) {
+                const float2 k = lds_f2(xs + ((WIDE ? 0 : w) * NT + c) * (W4_COLS * 4));
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float v = fmaf(hi[c][m][e], 64.f, lo[c][m][e]);   // 2^-14 sum c x
+                        y[c][m][e] = fmaf(sz[m][e >> 1].x,
+                                          fmaf(sz[m][e >> 1].y, (e & 1) ? k.y : k.x, v), y[c][m][e]);
+                    }
+            }
         }
     }
 }
@@ -277,11 +306,11 @@ template <bool WIDE> __device__ __forceinline__ float w4_join(float s)
 
 // Stages columns [k0, k0 + 128 steps) of `cols` fp16 rows (row(n): its first
 // element), through perm when given.  All threads; ends without a barrier.
-template <bool WIDE, class Row>
+template <int NT, bool WIDE, class Row>
 __device__ __forceinline__ void w4_stage_half(uint4* x, float* xs, Row row, const int32_t* perm,
                                               int k0, int steps, int cols, int d)
 {
-    constexpr int XS = W4_COLS;
+    constexpr int XS = W4_COLS * NT;
     const int nch = steps * 16, total = cols * nch;        // a multiple of 16
     for (int base = 0; base < total; base += blockDim.x) {
         const int i = base + threadIdx.x;
@@ -309,20 +338,20 @@ __device__ __forceinline__ void w4_stage_half(uint4* x, float* xs, Row row, cons
             x[w4_chunk<WIDE>(kc, n, cols)] = w4_order(h);
         }
         s = w4_join<WIDE>(s);
-        if (on && kc % (WIDE ? 16 : 4) == 0) xs[(kc / (WIDE ? 16 : 4)) * XS + n] = s * 0x1p-24f;
+        if (on && kc % (WIDE ? 16 : 4) == 0) xs[(kc / (WIDE ? 16 : 4)) * XS + n] = s * 0x1p-14f;
     }
 }
 
 // Stages fp32 rows in two fp16 parts: column n scaled by the power of two that
 // brings its largest magnitude to 2^14 .. 2^15 (undo[n]: its inverse; a column
-// with an infinity or NaN is not scaled).  top: W4_COLS words of scratch.  Holds
+// with an infinity or NaN is not scaled).  top: 8 NT words of scratch.  Holds
 // barriers; ends without one.
-template <bool WIDE, class Row>
+template <int NT, bool WIDE, class Row>
 __device__ __forceinline__ void w4_stage_split(uint4* x, float* xs, float* undo, uint32_t* top,
                                                Row row, const int32_t* perm, int k0, int steps,
                                                int cols, int d)
 {
-    constexpr int XS = W4_COLS;
+    constexpr int XS = W4_COLS * NT;
     for (int i = threadIdx.x; i < XS; i += blockDim.x) top[i] = 0u;
     __syncthreads();
     const int nch = steps * 16, total = cols * nch;
@@ -388,30 +417,29 @@ __device__ __forceinline__ void w4_stage_split(uint4* x, float* xs, float* undo,
             x[at + cols * nch] = w4_order(l);
         }
         s = w4_join<WIDE>(s);
-        if (on && kc % (WIDE ? 16 : 4) == 0) xs[(kc / (WIDE ? 16 : 4)) * XS + n] = s * 0x1p-24f;
+        if (on && kc % (WIDE ? 16 : 4) == 0) xs[(kc / (WIDE ? 16 : 4)) * XS + n] = s * 0x1p-14f;
     }
 }
 
 // Dynamic shared memory of a kernel with sweeps: the ring, the joining buffer,
 // the barriers, then the staged activations and their sums
 constexpr int W4_WARPS = W4_THREADS / 32;
-constexpr int W4_RED = W4_WARPS * 32 * 8;                    // floats of the joining buffer
 constexpr size_t W4_AT_RED = size_t(W4_WARPS) * W4_RING * W4_SLOT;
-constexpr size_t W4_AT_BAR = W4_AT_RED + W4_RED * 4;
-constexpr size_t W4_AT_X = W4_AT_BAR + 512;
+constexpr size_t w4_at_bar(int nt) { return W4_AT_RED + size_t(W4_WARPS) * 32 * 8 * 4 * nt; }
+constexpr size_t w4_at_x(int nt) { return w4_at_bar(nt) + 512; }
 static_assert(W4_WARPS * W4_RING * 8 <= 512, "barriers");
 inline __host__ __device__ size_t w4_x_bytes(int steps, int cols, bool split)
 {
     return size_t(steps) * 256 * cols * (split ? 2 : 1);
 }
-inline __host__ __device__ size_t w4_xs_bytes(int steps, bool wide)
+inline __host__ __device__ size_t w4_xs_bytes(int steps, int nt, bool wide)
 {
-    return size_t(steps) * (wide ? 1 : 4) * W4_COLS * 4;
+    return size_t(steps) * (wide ? 1 : 4) * W4_COLS * nt * 4;
 }
 // (and up to 1023 bytes in front, for the alignment of the ring)
-inline size_t w4_smem(int steps, int cols, bool wide, bool split)
+inline size_t w4_smem(int steps, int cols, int nt, bool wide, bool split)
 {
-    return 1024 + W4_AT_X + w4_x_bytes(steps, cols, split) + w4_xs_bytes(steps, wide);
+    return 1024 + w4_at_x(nt) + w4_x_bytes(steps, cols, split) + w4_xs_bytes(steps, nt, wide);
 }
 
 // The packed rows as a TMA tensor, in boxes of `rows` rows and two steps
@@ -441,13 +469,13 @@ struct W4Pipe {
 };
 
 // All threads; with a barrier
-__device__ __forceinline__ W4Pipe w4_pipe(uint8_t* smem, int* abort)
+template <int NT> __device__ __forceinline__ W4Pipe w4_pipe(uint8_t* smem, int* abort)
 {
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);    // uniform
     W4Pipe p;
     p.ring = smem_u32(smem) + warp * (W4_RING * W4_SLOT);
     p.red = smem_u32(smem) + uint32_t(W4_AT_RED);
-    uint64_t* bar = reinterpret_cast<uint64_t*>(smem + W4_AT_BAR) + warp * W4_RING;
+    uint64_t* bar = reinterpret_cast<uint64_t*>(smem + w4_at_bar(NT)) + warp * W4_RING;
     p.bar = smem_u32(bar);
     p.abort = abort;
     p.put = p.get = 0;
@@ -475,7 +503,7 @@ __device__ __forceinline__ bool w4_try_wait(uint32_t bar, uint32_t parity)
 
 // The rest of a wait that did not succeed at once: bounded like every wait of the
 // library; after it gave up the sweep goes on with what is there
-__device__ __noinline__ void w4_wait_long(uint32_t bar, uint32_t parity, volatile int* abort)
+static __device__ __noinline__ void w4_wait_long(uint32_t bar, uint32_t parity, volatile int* abort)
 {
     const unsigned long long t0 = globaltimer_ns();
     for (unsigned i = 1; !w4_try_wait(bar, parity); ++i)
@@ -498,7 +526,7 @@ __device__ __noinline__ void w4_wait_long(uint32_t bar, uint32_t parity, volatil
 //   done(group, r, n, v): the joined result of row r of the group (PAIR: of the
 //            group's gate rows), column n; PAIR: done(group, r, n, v, v2) with the up
 //            row's.
-template <int KW, bool WIDE, bool SPLIT, bool PAIR, class StageF, class DoneF>
+template <int NT, int KW, bool WIDE, bool SPLIT, bool PAIR, class StageF, class DoneF>
 __device__ __forceinline__ void w4_sweep(W4Pipe& pipe, const CUtensorMap* tm, const W4Layer& l,
                                          int64_t row0, int64_t end, uint32_t pair,
                                          const W4Stage& st, int groups, int k0, int steps,
@@ -564,13 +592,18 @@ __device__ __forceinline__ void w4_sweep(W4Pipe& pipe, const CUtensorMap* tm, co
     if (n) params(ahead, 0, 0);
     stage();
     const uint32_t xw = st.cols * 64;
-    const uint32_t x0 = st.x + (min(g, st.cols - 1) * 4 + t) * 16 + s0 * 4 * xw;
-    const uint32_t xs0 = st.xs + s0 * (WIDE ? 1 : 4) * W4_COLS * 4 + t * 8;
+    uint32_t x0[NT];
+#pragma unroll
+    for (int c = 0; c < NT; ++c)
+        x0[c] = st.x + (min(c * 8 + g, st.cols - 1) * 4 + t) * 16 + s0 * 4 * xw;
+    const uint32_t xs0 = st.xs + s0 * (WIDE ? 1 : 4) * W4_COLS * NT * 4 + t * 8;
     const uint32_t from = pipe.ring + w4_rho(g) * 128 + (WIDE ? (t ^ w4_rho(g)) * 16 : t * 4);
     const uint32_t red = pipe.red + (warp * 32 + lane) * 4;
     for (int grp = 0; grp < groups; ++grp) {
-        float y[2][4] = {};
-        uint32_t x = x0, xs = xs0;
+        float y[NT][2][4] = {};
+        uint32_t x[NT], xs = xs0;
+#pragma unroll
+        for (int c = 0; c < NT; ++c) x[c] = x0[c];
 #pragma unroll 1
         for (int j = 0; j < n; j += 2) {
             if (!w4_try_wait(pipe.bar + pipe.get * 8, pipe.phase))
@@ -588,10 +621,9 @@ __device__ __forceinline__ void w4_sweep(W4Pipe& pipe, const CUtensorMap* tm, co
                         if (j + u + EVERY < n) params(ahead, grp, j + u + EVERY);
                         else params(ahead, min(grp + 1, groups - 1), 0);
                     }
-                    w4_step<WIDE, SPLIT, PAIR>(y, WIDE ? slot ^ (64 * u) : slot, u, par, (j & 2) + u,
-                                               x, xs, xw, st.plane);
-                    x += 4 * xw;
-                    xs += (WIDE ? 1 : 4) * W4_COLS * 4;
+                    w4_step<NT, WIDE, SPLIT, PAIR>(y, WIDE ? slot ^ (64 * u) : slot, u, par,
+                                                   (j & 2) + u, x, xs, xw, st.plane);
+                    xs += (WIDE ? 1 : 4) * W4_COLS * NT * 4;
                 }
             }
             pipe.phase ^= pipe.get;
@@ -601,23 +633,28 @@ __device__ __forceinline__ void w4_sweep(W4Pipe& pipe, const CUtensorMap* tm, co
         }
         if (grp) __syncthreads();                          // the last group's sums have been read
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sts_f(red + e * W4_WARPS * 128, y[e >> 2][e & 3]);
+        for (int e = 0; e < 8 * NT; ++e)
+            sts_f(red + e * W4_WARPS * 128, y[e >> 3][(e >> 2) & 1][e & 3]);
         __syncthreads();
-        constexpr int EL = PAIR ? 4 : 8;                   // results per lane of a tile
+        constexpr int EL = (PAIR ? 4 : 8) * NT;            // results per lane of a tile
 #pragma unroll
         for (int u = 0; u < (RW * EL + W4_WARPS - 1) / W4_WARPS; ++u) {
             const int o = warp + u * W4_WARPS;
             if (o >= RW * EL) break;
-            const int w = o / EL, m = (o % EL) / (EL / 2), j = o % (EL / 2);
-            const uint32_t p = red + ((m * 4 + j) * W4_WARPS + w * KW - warp) * 128;
+            const int w = o / EL, r = o % EL, c = r / (EL / NT), m = (r / (EL / NT / 2)) & 1;
+            const int j = r % (EL / NT / 2);
+            const uint32_t p = red + ((c * 8 + m * 4 + j) * W4_WARPS + w * KW - warp) * 128;
             float v = 0.f, v2 = 0.f;
 #pragma unroll
             for (int k = 0; k < KW; ++k) {
                 v += lds_f(p + k * 128);
                 if (PAIR) v2 += lds_f(p + (2 * W4_WARPS + k) * 128);
             }
-            if constexpr (PAIR) done(grp, w * 16 + m * 8 + w4_rho(g), 2 * t + j, v * 0x1p24f, v2 * 0x1p24f);
-            else done(grp, w * 32 + m * 16 + (j >> 1) * 8 + w4_rho(g), 2 * t + (j & 1), v * 0x1p24f);
+            if constexpr (PAIR)
+                done(grp, w * 16 + m * 8 + w4_rho(g), c * 8 + 2 * t + j, v * 0x1p14f, v2 * 0x1p14f);
+            else
+                done(grp, w * 32 + m * 16 + (j >> 1) * 8 + w4_rho(g), c * 8 + 2 * t + (j & 1),
+                     v * 0x1p14f);
         }
     }
     __syncthreads();                                       // x and red free again

@@ -3,72 +3,207 @@
 //
 //   y[b] = x[b] Q^T + scaling[a] (x[b] A_a^T) B_a^T,   a = adapter[b]
 //
-// Two kernels: t[b] = scaling[a] A_a x[b] (one warp per row and rank), then one
-// warp per output.
+// Two kernels.  The first sweeps the packed rows (w4_rows.cuh) for chunks of up to
+// 16 rows of x and slices of the columns, and computes t[b] = scaling A_a x[b]
+// beside it; the second joins the slices and adds B_a t.  Partial results go
+// through memory, not atomics: their order is fixed.
 #include "common.cuh"
 #include "tc_common.cuh"
+#include "w4_rows.cuh"
 
 namespace gptq {
 
+constexpr int LORA_KW = 8, LORA_ROWS = 32 * (W4_WARPS / LORA_KW);   // of w4_sweep
+constexpr int LORA_JOIN = 4;                     // rows of x per thread of the join
+
 struct LoraParams {
     const __half* x;
-    const uint32_t* qweight;
-    const __half* scales;
-    const uint8_t* qzeros;
     const int32_t* perm;
     const __half* a;
     const __half* b;
     const float* scaling;
     const int32_t* adapter;
-    int64_t batch, m, d, g, n;
+    int64_t batch, m, d, n;
     int rank;
-    float* t;
+    W4Layer lay;
+    int chunk, chunks, slice, slices, groups;
+    float* t;          // batch x rank
+    float* part;       // slices x batch x m
     float* y;
 };
 
-__global__ void __launch_bounds__(256) lora_shrink_simple_kernel(const LoraParams p)
+// t[b][r] = scaling (A_a[r] . x[b]): one warp per (rank row, four rows of x), which
+// share a load of A where they have the same adapter
+__device__ __forceinline__ void lora_shrink(const LoraParams& p)
 {
     const int lane = threadIdx.x & 31;
-    const int64_t item = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    const int64_t b = item / p.rank, r = item - b * p.rank;
-    if (b >= p.batch) return;
-    int64_t a = p.adapter[b];
-    if (a < -1 || a >= p.n) {
-        if (lane == 0) atomicCAS(&g_device_status, 0, kErrIndex);
-        a = -1;
+    const int64_t items = ((p.batch + 3) / 4) * p.rank;
+    for (int64_t it = int64_t(blockIdx.x) + int64_t(threadIdx.x >> 5) * gridDim.x; it < items;
+         it += int64_t(gridDim.x) * W4_WARPS) {
+        const int64_t b0 = it / p.rank * 4;
+        const int r = int(it % p.rank);
+        int id[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            id[i] = b0 + i < p.batch ? p.adapter[b0 + i] : -1;
+            if (id[i] < -1 || id[i] >= p.n) {
+                if (lane == 0) atomicCAS(&g_device_status, 0, kErrIndex);
+                id[i] = -1;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (b0 + i >= p.batch) break;
+            bool first = true;                             // of the rows with this adapter
+#pragma unroll
+            for (int j = 0; j < i; ++j) first = first && (id[j] != id[i]);
+            if (!first) continue;
+            float s[4] = {0.f, 0.f, 0.f, 0.f};
+            if (id[i] >= 0) {
+                const __half* a = p.a + (int64_t(id[i]) * p.rank + r) * p.d;
+                for (int64_t k = lane * 8; k < p.d; k += 256) {
+                    const uint4 av = *reinterpret_cast<const uint4*>(a + k);
+                    const __half2* ah = reinterpret_cast<const __half2*>(&av);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (j < i || id[j] != id[i]) continue;
+                        const uint4 xv = *reinterpret_cast<const uint4*>(p.x + (b0 + j) * p.d + k);
+                        const __half2* xh = reinterpret_cast<const __half2*>(&xv);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 u = __half22float2(ah[e]), v = __half22float2(xh[e]);
+                            s[j] = fmaf(u.x, v.x, s[j]);
+                            s[j] = fmaf(u.y, v.y, s[j]);
+                        }
+                    }
+                }
+            }
+            const float c = id[i] >= 0 ? p.scaling[id[i]] : 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (j < i || id[j] != id[i] || b0 + j >= p.batch) continue;
+                for (int o = 16; o; o >>= 1) s[j] += __shfl_xor_sync(0xffffffffu, s[j], o);
+                if (lane == 0) p.t[(b0 + j) * p.rank + r] = s[j] * c;
+            }
+        }
     }
-    float s = 0.f;
-    if (a >= 0)
-        for (int64_t j = lane; j < p.d; j += 32)
-            s += __half2float(p.x[b * p.d + j]) * __half2float(p.a[(a * p.rank + r) * p.d + j]);
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) p.t[b * p.rank + r] = a >= 0 ? s * p.scaling[a] : 0.f;
 }
 
-__global__ void __launch_bounds__(256) lora_product_simple_kernel(const LoraParams p)
+template <int NT, bool WIDE>
+__global__ void __launch_bounds__(W4_THREADS, 1)
+lora_product_kernel(const __grid_constant__ CUtensorMap tm, const LoraParams p)
 {
-    const int lane = threadIdx.x & 31;
-    const int64_t r = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5), b = blockIdx.y;
-    if (r >= p.m) return;
-    const int64_t G = p.d / p.g;
-    float s = 0.f;
-    for (int64_t k = lane; k < p.d; k += 32) {
-        const int64_t src = p.perm ? p.perm[k] : k;
-        if (src < 0 || src >= p.d) {
-            atomicCAS(&g_device_status, 0, kErrIndex);
-            continue;
-        }
-        const int64_t gi = k / p.g;
-        const int c = (p.qweight[r * (p.d / 8) + k / 8] >> (4 * (k % 8))) & 15;
-        const int z = (p.qzeros[r * ((G + 1) / 2) + gi / 2] >> (4 * (gi & 1))) & 15;
-        s += __half2float(p.x[b * p.d + src]) * (__half2float(p.scales[r * G + gi]) * float(c - z));
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ int abort;
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int nsteps = int(p.d / W4_STEP);
+    uint4* x = reinterpret_cast<uint4*>(smem + w4_at_x(NT));
+    float* xs = reinterpret_cast<float*>(smem + w4_at_x(NT) + w4_x_bytes(p.slice, p.chunk, false));
+    W4Pipe pipe = w4_pipe<NT>(smem, &abort);
+    // units in the order (slice, chunk of x, row group), shared evenly
+    const int64_t units = int64_t(p.slices) * p.groups * p.chunks;
+    int64_t u = units * blockIdx.x / gridDim.x;
+    const int64_t u1 = units * (blockIdx.x + 1) / gridDim.x;
+    bool shrunk = false;
+    while (u < u1) {
+        // a run of row groups of one (chunk, slice)
+        const int64_t cs = u / p.groups;
+        const int g0 = int(u - cs * p.groups);
+        const int g1 = int(min(int64_t(p.groups), g0 + (u1 - u)));
+        const int c = int(cs % p.chunks), sl = int(cs / p.chunks);
+        const int k0 = sl * p.slice, steps = min(p.slice, nsteps - k0);
+        const int64_t b0 = int64_t(c) * p.chunk;
+        const int cols = int(min(int64_t(p.chunk), p.batch - b0));
+        const W4Stage st{smem_u32(x), smem_u32(xs), cols, 0u};
+        w4_sweep<NT, LORA_KW, WIDE, false, false>(
+            pipe, &tm, p.lay, int64_t(g0) * LORA_ROWS, p.m, 0u, st, g1 - g0, k0, steps,
+            [&]() {
+                w4_stage_half<NT, WIDE>(x, xs, [&](int n) { return p.x + (b0 + n) * p.d; }, p.perm,
+                                        k0 * W4_STEP, steps, cols, int(p.d));
+                if (!shrunk) lora_shrink(p);               // beside the first copies
+                shrunk = true;
+                __syncthreads();
+            },
+            [&](int grp, int r, int n, float v) {
+                const int64_t row = int64_t(g0 + grp) * LORA_ROWS + r;
+                if (n < cols && row < p.m) p.part[(int64_t(sl) * p.batch + b0 + n) * p.m + row] = v;
+            });
+        u += g1 - g0;
     }
-    const int64_t a = p.adapter[b];
-    if (a >= 0 && a < p.n)
-        for (int k = lane; k < p.rank; k += 32)
-            s += p.t[b * p.rank + k] * __half2float(p.b[(a * p.m + r) * p.rank + k]);
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) p.y[b * p.m + r] = s;
+    if (!shrunk) lora_shrink(p);
+}
+
+// y[b][r] = sum of part over the slices + B_a[r] . t[b]
+__global__ void __launch_bounds__(256) lora_join_kernel(const LoraParams p)
+{
+    const int64_t r = int64_t(blockIdx.x) * 256 + threadIdx.x;
+    const int64_t b0 = int64_t(blockIdx.y) * LORA_JOIN;
+    int id[LORA_JOIN];
+#pragma unroll
+    for (int i = 0; i < LORA_JOIN; ++i) {
+        id[i] = b0 + i < p.batch ? p.adapter[b0 + i] : -1;
+        if (id[i] >= p.n) id[i] = -1;
+    }
+    pdl_wait();
+    if (r >= p.m) return;
+    float y[LORA_JOIN] = {};
+#pragma unroll
+    for (int i = 0; i < LORA_JOIN; ++i)
+        if (b0 + i < p.batch)
+            for (int s = 0; s < p.slices; ++s) y[i] += p.part[(int64_t(s) * p.batch + b0 + i) * p.m + r];
+    for (int k = 0; k < p.rank; k += 8) {
+        uint4 bv = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int i = 0; i < LORA_JOIN; ++i) {
+            if (id[i] < 0) continue;
+            if (i == 0 || id[i] != id[i - 1])              // neighbours share the load
+                bv = *reinterpret_cast<const uint4*>(p.b + (int64_t(id[i]) * p.m + r) * p.rank + k);
+            const float4 t0 = *reinterpret_cast<const float4*>(p.t + (b0 + i) * p.rank + k);
+            const float4 t1 = *reinterpret_cast<const float4*>(p.t + (b0 + i) * p.rank + k + 4);
+            const __half2* h = reinterpret_cast<const __half2*>(&bv);
+            const float2 v0 = __half22float2(h[0]), v1 = __half22float2(h[1]);
+            const float2 v2 = __half22float2(h[2]), v3 = __half22float2(h[3]);
+            y[i] = fmaf(v0.x, t0.x, y[i]); y[i] = fmaf(v0.y, t0.y, y[i]);
+            y[i] = fmaf(v1.x, t0.z, y[i]); y[i] = fmaf(v1.y, t0.w, y[i]);
+            y[i] = fmaf(v2.x, t1.x, y[i]); y[i] = fmaf(v2.y, t1.y, y[i]);
+            y[i] = fmaf(v3.x, t1.z, y[i]); y[i] = fmaf(v3.y, t1.w, y[i]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < LORA_JOIN; ++i)
+        if (b0 + i < p.batch) p.y[(b0 + i) * p.m + r] = y[i];
+}
+
+struct LoraPlan {
+    int nt, chunk, chunks, slice, slices, groups;
+    size_t at_part, bytes;
+};
+
+// Rows of x that are staged together (one operand of 8, or two) and slices of the
+// columns: as few as fit beside the ring, or more where few row groups would leave
+// CTAs idle.  A group costs about 190 instructions a step and warp (two operands:
+// 260, bound by the matrix pipe) and 150 to join, and the slowest CTA counts.
+LoraPlan lora_plan(int64_t T, int64_t m, int64_t d, int rank)
+{
+    LoraPlan p{};
+    p.nt = T > W4_COLS ? 2 : 1;
+    p.chunk = int(std::min<int64_t>(T, W4_COLS * p.nt));
+    p.chunks = int((T + p.chunk - 1) / p.chunk);
+    p.groups = int((m + LORA_ROWS - 1) / LORA_ROWS);
+    const int so = int(d / W4_STEP), room = (p.nt == 1 ? 72 : 56) * 1024;
+    const int most = std::min(so, room / (256 * p.chunk + 128 * p.nt));
+    double best = 1e300;
+    for (int s = (so + most - 1) / most; s <= std::min(so, 64); ++s) {
+        const int steps = (so + s - 1) / s;
+        const int64_t rounds = ((int64_t(p.chunks) * s * p.groups) + 147) / 148;
+        const double cost = double(rounds) * (((steps + LORA_KW - 1) / LORA_KW) * (p.nt == 1 ? 190 : 260) + 150);
+        if (cost < best * 0.97) { best = cost; p.slice = steps; }
+    }
+    p.slices = (so + p.slice - 1) / p.slice;
+    p.at_part = align_up(size_t(T) * rank * 4, 256);
+    p.bytes = p.at_part + align_up(size_t(p.slices) * T * m * 4, 256);
+    return p;
 }
 
 }  // namespace gptq
@@ -77,7 +212,9 @@ extern "C" size_t gptq_w4a16_lora_workspace_bytes(int64_t batch, int64_t d_out, 
                                                   int rank)
 {
     if (batch <= 0 || d_out <= 0 || d_in <= 0 || rank <= 0) return 0;
-    return gptq::align_up(size_t(batch) * size_t(rank) * 4, 256);
+    if (batch > 65535 || d_out > gptq::kMaxRows || d_in > gptq::kMaxDim || d_in % 128 != 0 || rank > 256)
+        return 0;
+    return gptq::lora_plan(batch, d_out, d_in, rank).bytes;
 }
 
 extern "C" int gptq_w4a16_lora(const uint16_t* x, int64_t batch, const uint32_t* qweight,
@@ -104,21 +241,36 @@ extern "C" int gptq_w4a16_lora(const uint16_t* x, int64_t batch, const uint32_t*
         return GPTQ_ERR_INVALID_ARG;
     if (ws_bytes < gptq_w4a16_lora_workspace_bytes(batch, d_out, d_in, rank))
         return GPTQ_ERR_INVALID_ARG;
+    const LoraPlan plan = lora_plan(batch, d_out, d_in, rank);
     LoraParams p{};
     p.x = reinterpret_cast<const __half*>(x);
-    p.qweight = qweight;
-    p.scales = reinterpret_cast<const __half*>(scales);
-    p.qzeros = qzeros; p.perm = perm;
+    p.perm = perm;
     p.a = reinterpret_cast<const __half*>(lora_a);
     p.b = reinterpret_cast<const __half*>(lora_b);
     p.scaling = lora_scaling; p.adapter = adapter;
-    p.batch = batch; p.m = d_out; p.d = d_in; p.g = g; p.n = n_adapters; p.rank = rank;
+    p.batch = batch; p.m = d_out; p.d = d_in; p.n = n_adapters; p.rank = rank;
+    p.lay = w4_layer(qweight, scales, qzeros, d_in, g);
+    p.chunk = plan.chunk; p.chunks = plan.chunks; p.slice = plan.slice; p.slices = plan.slices;
+    p.groups = plan.groups;
     p.t = static_cast<float*>(ws);
+    p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + plan.at_part);
     p.y = y;
     cudaStream_t st = as_stream(stream);
     KernelTimer kt(kKLora, st);
-    lora_shrink_simple_kernel<<<(unsigned)ceil_div(batch * rank, 8), 256, 0, st>>>(p);
-    lora_product_simple_kernel<<<dim3((unsigned)ceil_div(d_out, 8), (unsigned)batch), 256, 0, st>>>(p);
+    CUtensorMap tm;
+    if (w4_tmap(&tm, qweight, d_out, d_in, 32) != GPTQ_OK) return GPTQ_ERR_CUDA;
+    const bool wide = g % W4_STEP == 0;
+    const size_t smem = w4_smem(plan.slice, plan.chunk, plan.nt, wide, false);
+    auto kern = plan.nt == 1 ? (wide ? lora_product_kernel<1, true> : lora_product_kernel<1, false>)
+                             : (wide ? lora_product_kernel<2, true> : lora_product_kernel<2, false>);
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+        cudaSuccess)
+        return GPTQ_ERR_CUDA;
+    const int64_t units = int64_t(plan.chunks) * plan.slices * plan.groups;
+    kern<<<(unsigned)std::min<int64_t>(device_sm_count(), units), W4_THREADS, smem, st>>>(tm, p);
+    if (launch_after(lora_join_kernel, dim3((unsigned)ceil_div(d_out, 256), (unsigned)ceil_div(batch, LORA_JOIN)),
+                     256, 0, st, p) != cudaSuccess)
+        return GPTQ_ERR_CUDA;
     count_launches(2);
     return launch_status();
 }

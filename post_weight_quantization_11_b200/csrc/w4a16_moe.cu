@@ -176,9 +176,9 @@ __global__ void __launch_bounds__(W4_THREADS, 1) moe_in_kernel(const __grid_cons
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int steps = int(p.d / W4_STEP), groups = int(p.f / MOE_IN_ROWS);
-    uint4* x = reinterpret_cast<uint4*>(smem + W4_AT_X);
-    float* xs = reinterpret_cast<float*>(smem + W4_AT_X + w4_x_bytes(steps, p.chunk, false));
-    W4Pipe pipe = w4_pipe(smem, &abort);
+    uint4* x = reinterpret_cast<uint4*>(smem + w4_at_x(1));
+    float* xs = reinterpret_cast<float*>(smem + w4_at_x(1) + w4_x_bytes(steps, p.chunk, false));
+    W4Pipe pipe = w4_pipe<1>(smem, &abort);
     moe_routes(p, r, cnt, off, coff);
     if (blockIdx.x == 0) {                                 // for the second kernel
         const int* src = reinterpret_cast<const int*>(&r);
@@ -195,11 +195,11 @@ __global__ void __launch_bounds__(W4_THREADS, 1) moe_in_kernel(const __grid_cons
         const int16_t* list = r.list + r.start[c];
         const int64_t row0 = int64_t(e) * 2 * p.f;
         const W4Stage st{smem_u32(x), smem_u32(xs), cols, 0};
-        w4_sweep<MOE_IN_KW, WIDE, false, true>(
+        w4_sweep<1, MOE_IN_KW, WIDE, false, true>(
             pipe, &tm, p.in, row0 + int64_t(g0) * MOE_IN_ROWS, row0 + 2 * p.f, uint32_t(p.f), st,
             g1 - g0, 0, steps,
             [&]() {
-                w4_stage_half<WIDE>(
+                w4_stage_half<1, WIDE>(
                     x, xs, [&](int n) { return p.x + int64_t(list[n] / p.k) * p.d; },
                     p.pi ? p.pi + e * p.d : nullptr, 0, steps, cols, int(p.d));
                 __syncthreads();
@@ -225,9 +225,9 @@ __global__ void __launch_bounds__(W4_THREADS, 1) moe_out_kernel(const __grid_con
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int groups = int(p.d / MOE_OUT_ROWS), nsteps = int(p.f / W4_STEP);
-    uint4* x = reinterpret_cast<uint4*>(smem + W4_AT_X);
-    float* xs = reinterpret_cast<float*>(smem + W4_AT_X + w4_x_bytes(p.slice, p.chunk, true));
-    W4Pipe pipe = w4_pipe(smem, &abort);
+    uint4* x = reinterpret_cast<uint4*>(smem + w4_at_x(1));
+    float* xs = reinterpret_cast<float*>(smem + w4_at_x(1) + w4_x_bytes(p.slice, p.chunk, true));
+    W4Pipe pipe = w4_pipe<1>(smem, &abort);
     pdl_wait();
     for (int i = threadIdx.x; i < int(sizeof(MoeRoutes) / 4); i += blockDim.x)
         reinterpret_cast<int*>(&r)[i] = reinterpret_cast<const int*>(p.routes)[i];
@@ -244,11 +244,11 @@ __global__ void __launch_bounds__(W4_THREADS, 1) moe_out_kernel(const __grid_con
         const int16_t* list = r.list + r.start[c];
         const int64_t row0 = int64_t(e) * p.d;
         const W4Stage st{smem_u32(x), smem_u32(xs), cols, uint32_t(steps * 256 * cols)};
-        w4_sweep<MOE_OUT_KW, WIDE, true, false>(
+        w4_sweep<1, MOE_OUT_KW, WIDE, true, false>(
             pipe, &tm, p.out, row0 + int64_t(g0) * MOE_OUT_ROWS, row0 + p.d, 0u, st, g1 - g0, k0,
             steps,
             [&]() {
-                w4_stage_split<WIDE>(
+                w4_stage_split<1, WIDE>(
                     x, xs, undo, top, [&](int n) { return p.h + int64_t(list[n]) * p.f; },
                     p.po ? p.po + e * p.f : nullptr, k0 * W4_STEP, steps, cols, int(p.f));
                 __syncthreads();
@@ -305,8 +305,8 @@ MoePlan moe_plan(int64_t T, int64_t E, int k, int64_t d, int64_t f)
         if (cost < best * 0.97) { best = cost; m.slice = steps; }
     }
     m.slices = (so + m.slice - 1) / m.slice;
-    m.smem_in = w4_smem(si, m.chunk, false, false);
-    m.smem_out = w4_smem(m.slice, m.chunk, false, true);
+    m.smem_in = w4_smem(si, m.chunk, 1, false, false);
+    m.smem_out = w4_smem(m.slice, m.chunk, 1, false, true);
     const size_t pairs = size_t(T) * k;
     m.at_h = align_up(sizeof(MoeRoutes), 256);
     m.at_part = m.at_h + align_up(pairs * f * 4, 256);
