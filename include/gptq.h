@@ -547,6 +547,8 @@ int gptq_kv4_append(const void* q, int64_t q_stride, const void* k, int64_t k_st
  *    q_start: seqs + 1 int32, non-decreasing, within 0 .. tokens.
  * max_q_len, max_seq_len: host bounds of n and seq_lens (max_seq_len <=
  *    table_width * page_size): they size the launch and the workspace.
+ *    kv_heads times the tiles of 8 rows in max_q_len q_heads / kv_heads is at
+ *    most 65535.
  * A sequence whose length or query range breaks these bounds is recorded in
  * the device status (0x201) and its rows are left as they are; a page outside
  * 0 .. pages - 1 is recorded and its keys are not seen.

@@ -3,19 +3,42 @@
 //
 //   out = sum_j p_j V_j,  p = softmax_j(scale q . K_j),  K_j = s_j (c_j - z_j)
 //
-// One CTA per (query, head): its warps walk the keys, each with a running
-// maximum and sum, and join at the end.
+// The rows (query, head) of a sequence that share a key head are the columns of the
+// products, eight to a CTA; keys and values are their row operands, read once.
+//  * Work: (chunk of keys, key head and row tile, sequence).  Chunks have one size,
+//    so ragged batches balance; CTAs whose chunk lies behind a sequence's end leave
+//    at once.  The four warps of a CTA take tiles of 32 keys in turn, each with its
+//    own running maximum, sum and output, joined at the end; chunks are joined by a
+//    second kernel in a fixed order.
+//  * A tile's 16-key halves are contiguous in the cache (a page is a multiple of
+//    16): eight bulk copies (codes and parameters of keys and values, two halves),
+//    one instruction of eight lanes, KV_RING tiles ahead on one mbarrier a tile.
+//  * Scores: S^T = K q^T on m16n8k16 mma.sync, keys as rows.  A code alone in a half
+//    word is the fp16 subnormal c 2^-24 (low nibble) or c 2^-20 (high): one AND per
+//    operand register.  A key's scale and zero point are applied to the product:
+//    s (sum c q - z sum q).
+//  * out^T = V^T p: two keys' words of the same elements, merged half by half, give
+//    operand registers of two keys again by one AND.  A value's scale goes into its
+//    probability: u = p s, in two fp16 parts (22 bits), scaled by a power of two that
+//    follows the largest s; its zero point into sum u z, subtracted at the end.
+//  * The rows of an operand are the keys kv_key(g) of its eight: the same keys are
+//    then two neighbouring columns of the other product's operand, and the reads of
+//    shared memory hit every bank as often (keys) or twice (values).
+
 #include <cmath>
 
 #include "common.cuh"
 #include "tc_common.cuh"
+#include "w4_rows.cuh"
 
 namespace gptq {
 
+constexpr int KV_WARPS = 4, KV_TILE = 32, KV_RING = 3;
+
 struct KvAttn {
     const __half* q;
-    int64_t tokens, seqs, pages, width, window, max_q, max_len;
-    int hq, hkv, g, page_shift;
+    int64_t tokens, seqs, pages, width, window;
+    int max_q, max_len, hq, hkv, page_shift;
     const uint32_t* kc;
     const __half2* kp;
     const uint32_t* vc;
@@ -24,83 +47,477 @@ struct KvAttn {
     const int32_t* lens;
     const int32_t* start;
     float scale;                           // times log2(e)
+    int chunk, splits, row_tiles;
+    float* part;                           // unit x 8 rows x (D, then maximum and sum)
     __half* out;
 };
 
-template <int E>
-__global__ void __launch_bounds__(128) kv4_attention_simple_kernel(const KvAttn p)
+// Key of row g of an operand's eight
+__device__ __forceinline__ int kv_key(int g) { return (g & 1) ? 4 + ((g >> 1) ^ 1) : (g >> 1); }
+
+__device__ __forceinline__ uint32_t movmatrix(uint32_t v)
 {
-    constexpr int D = 32 * E, NB = D / 32;
-    __shared__ float part[4][D], ml[4][2];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int b = blockIdx.z, h = blockIdx.y;
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+__device__ __forceinline__ void kv_bulk(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+        ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
+        : "memory");
+}
+
+// What a row tile of a sequence sees
+struct KvSpan {
+    bool ok;                               // the sequence's range and length are valid
+    int64_t s0;
+    int n, L, rows, lo, base, hi;          // queries, keys, rows; keys [lo, hi) are seen, base: lo's tile
+};
+
+__device__ __forceinline__ KvSpan kv_span(const KvAttn& p, int b, int rt)
+{
+    KvSpan s;
     const int64_t s0 = p.start[b], s1 = p.start[b + 1], L = p.lens[b];
-    if (s0 < 0 || s1 < s0 || s1 > p.tokens || s1 - s0 > p.max_q || L < 0 || L > p.max_len) {
+    s.ok = s0 >= 0 && s1 >= s0 && s1 <= p.tokens && s1 - s0 <= p.max_q && L >= 0 && L <= p.max_len;
+    s.s0 = s0;
+    s.n = int(s1 - s0);
+    s.L = int(L);
+    const int grp = p.hq / p.hkv;
+    s.rows = s.n * grp - rt * 8;           // from the tile's first row on
+    if (!s.ok || s.rows <= 0) { s.rows = s.lo = s.base = s.hi = 0; return s; }
+    const int i0 = rt * 8 / grp, i1 = (rt * 8 + min(s.rows, 8) - 1) / grp;
+    s.hi = max(0, s.L - s.n + i1 + 1);
+    const int64_t lo = p.window > 0 ? int64_t(s.L) - s.n + i0 + 1 - p.window : 0;
+    s.lo = int(max(lo, int64_t(0)));
+    s.base = s.lo & ~(KV_TILE - 1);
+    return s;
+}
+
+template <int D, int G> struct KvShape {
+    static constexpr int NB = D / 32, GB = NB / G;         // blocks of 32 elements, of a group
+    static constexpr int CODES = KV_TILE * D / 2, PARAMS = KV_TILE * G * 4;
+    static constexpr int SLOT = 2 * (CODES + PARAMS);
+    static constexpr int RING = KV_WARPS * KV_RING * SLOT;
+    static constexpr int JOIN = KV_WARPS * 8 * D * 4;      // in the ring's place, at the end
+    static constexpr int SMEM = (RING > JOIN ? RING : JOIN) + 128;
+};
+
+template <int D, int G>
+__global__ void __launch_bounds__(KV_WARPS * 32) kv4_attention_kernel(const KvAttn p)
+{
+    using Sh = KvShape<D, G>;
+    constexpr int NB = Sh::NB, GB = Sh::GB;
+    constexpr uint32_t LO = 0x000F000Fu, HI = 0x00F000F0u, ALL = 0xffffffffu;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ __align__(16) float qsum[G][8];             // read in pairs
+    __shared__ float wm[KV_WARPS][8], wl[KV_WARPS][8];
+    __shared__ __align__(8) uint64_t bars[KV_WARPS * KV_RING];
+    __shared__ int abort;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int warp = __shfl_sync(ALL, threadIdx.x >> 5, 0);
+    const int b = blockIdx.z, hk = blockIdx.y / p.row_tiles, rt = blockIdx.y - hk * p.row_tiles;
+    const int grp = p.hq / p.hkv;
+    const KvSpan sp = kv_span(p, b, rt);
+    if (!sp.ok) {
         if (threadIdx.x == 0) atomicCAS(&g_device_status, 0, kErrIndex);
         return;
     }
-    const int64_t t = s0 + blockIdx.x;
-    if (t >= s1) return;
-    const int64_t hi = L - (s1 - s0) + int64_t(blockIdx.x) + 1;      // keys [lo, hi)
-    const int64_t lo = p.window > 0 && hi - p.window > 0 ? hi - p.window : 0;
-    const int hk = h / (p.hq / p.hkv);
-    const __half* q = p.q + (t * p.hq + h) * D;
-    float qv[E], acc[E];
-    int kd[E], vd[E];
+    if (sp.rows <= 0) return;
+    const int c0 = sp.base + int(blockIdx.x) * p.chunk, c1 = min(sp.hi, c0 + p.chunk);
+    if (c0 >= sp.hi && (blockIdx.x > 0 || p.splits > 1)) return;
+    const int tiles = c1 > c0 ? (c1 - c0 + KV_TILE - 1) / KV_TILE : 0;
+
+    if (lane == 0)
+        for (int i = 0; i < KV_RING; ++i) mbar_init(&bars[warp * KV_RING + i], 1);
+    if (threadIdx.x == 0) abort = 0;
+    fence_mbar_init();
+    __syncwarp();
+    // producer: lanes 0 .. 7, half tile lane / 4, array lane % 4 (key codes, value codes,
+    // key and value parameters); the page of the next tile is looked up a tile ahead
+    const uint32_t ring = smem_u32(smem) + warp * (KV_RING * Sh::SLOT);
+    const uint32_t bar0 = smem_u32(&bars[warp * KV_RING]);
+    const int half = (lane >> 2) & 1, what = lane & 3;
+    const int32_t* table = p.table + int64_t(b) * p.width;
+    int ptile = warp, pslot = 0;
+    uint32_t seen = 0;                                     // two bits a slot: halves with a valid page
+    int page = 0;
+    auto look = [&]() {
+        const int key = c0 + ptile * KV_TILE + half * 16;
+        page = key < c1 ? table[key >> p.page_shift] : 0;
+    };
+    auto issue = [&]() {
+        if (ptile >= tiles) return;
+        const int key = c0 + ptile * KV_TILE + half * 16;
+        const bool in = key < c1;
+        const bool valid = page >= 0 && page < p.pages;
+        if (lane < 8 && in && !valid) atomicCAS(&g_device_status, 0, kErrIndex);
+        const bool go = lane < 8 && in && valid;
+        const uint32_t who = __ballot_sync(ALL, go);
+        const uint32_t halves = (who & 1u) | ((who >> 3) & 2u);
+        seen = (seen & ~(3u << (2 * pslot))) | (halves << (2 * pslot));
+        const uint32_t bar = bar0 + pslot * 8;
+        if (lane == 0)
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar),
+                         "r"(uint32_t(__popc(halves)) * (Sh::SLOT / 2))
+                         : "memory");
+        __syncwarp();
+        if (go) {
+            const int64_t row = ((int64_t(page) * p.hkv + hk) << p.page_shift) +
+                                (key & ((1 << p.page_shift) - 1));
+            const uint32_t dst = ring + pslot * Sh::SLOT;
+            if (what < 2)
+                kv_bulk(dst + what * Sh::CODES + half * (Sh::CODES / 2),
+                        (what ? p.vc : p.kc) + row * (D / 8), Sh::CODES / 2, bar);
+            else
+                kv_bulk(dst + 2 * Sh::CODES + (what - 2) * Sh::PARAMS + half * (Sh::PARAMS / 2),
+                        (what == 3 ? p.vp : p.kp) + row * G, Sh::PARAMS / 2, bar);
+        }
+        ptile += KV_WARPS;
+        pslot = pslot + 1 == KV_RING ? 0 : pslot + 1;
+        look();
+    };
+    look();
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const int n = lane * E + e;                        // nibble of the row
-        const int w = n / 8, u = n / 4;
-        kd[e] = 32 * (w % NB) + 8 * (w / NB) + n % 8;
-        vd[e] = 32 * (u % NB) + 4 * (u / NB) + n % 4;
-        qv[e] = __half2float(q[kd[e]]);
-        acc[e] = 0.f;
+    for (int i = 0; i < KV_RING; ++i) issue();
+
+    // the queries' operand (row g of the tile: elements 32 i + 8 t .. of block i, in the
+    // order of a word's nibbles) and the sums over each group
+    uint32_t qf[NB][4];
+    {
+        const int r = rt * 8 + g;
+        const bool on = g < sp.rows;
+        const __half* src = p.q + ((sp.s0 + (on ? r / grp : 0)) * p.hq + hk * grp + (on ? r % grp : 0)) * D;
+        float qs[G] = {};
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (on) v = *reinterpret_cast<const uint4*>(src + 32 * i + 8 * t);
+            const __half2* h = reinterpret_cast<const __half2*>(&v);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 f = __half22float2(h[e]);
+                qs[i / GB] += f.x + f.y;
+            }
+            qf[i][0] = __byte_perm(v.x, v.z, 0x5410);      // elements 0, 4
+            qf[i][1] = __byte_perm(v.y, v.w, 0x5410);      // 2, 6
+            qf[i][2] = __byte_perm(v.x, v.z, 0x7632);      // 1, 5
+            qf[i][3] = __byte_perm(v.y, v.w, 0x7632);      // 3, 7
+        }
+#pragma unroll
+        for (int k = 0; k < G; ++k) {
+            qs[k] += __shfl_xor_sync(ALL, qs[k], 1);
+            qs[k] += __shfl_xor_sync(ALL, qs[k], 2);
+            if (warp == 0 && t == 0) qsum[k][g] = qs[k] * 0x1p-24f;
+        }
     }
-    float m = -INFINITY, l = 0.f;
-    for (int64_t j = lo + warp; j < hi; j += 4) {
-        const int64_t page = p.table[int64_t(b) * p.width + (j >> p.page_shift)];
-        if (page < 0 || page >= p.pages) {
-            if (lane == 0) atomicCAS(&g_device_status, 0, kErrIndex);
-            continue;
-        }
-        const int64_t row = ((page * p.hkv + hk) << p.page_shift) + (j & ((1 << p.page_shift) - 1));
-        float dot = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int n = lane * E + e;
-            const float c = float((p.kc[row * (D / 8) + n / 8] >> (4 * (n % 8))) & 15u);
-            const float2 sz = __half22float2(p.kp[row * (D / p.g) + kd[e] / p.g]);
-            dot += qv[e] * (sz.x * (c - sz.y));
-        }
-        for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        dot *= p.scale;
-        const float mx = fmaxf(m, dot), al = exp2f(m - mx), pr = exp2f(dot - mx);
-        m = mx;
-        l = l * al + pr;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int n = lane * E + e;
-            const float c = float((p.vc[row * (D / 8) + n / 8] >> (4 * (n % 8))) & 15u);
-            const float2 sz = __half22float2(p.vp[row * (D / p.g) + vd[e] / p.g]);
-            acc[e] = acc[e] * al + pr * (sz.x * (c - sz.y));
-        }
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e) part[warp][vd[e]] = acc[e];
-    if (lane == 0) { ml[warp][0] = m; ml[warp][1] = l; }
     __syncthreads();
-    float top = -INFINITY;
-    for (int w = 0; w < 4; ++w) top = fmaxf(top, ml[w][0]);
-    float wt[4], sum = 0.f;
-    for (int w = 0; w < 4; ++w) {
-        wt[w] = ml[w][0] == -INFINITY ? 0.f : exp2f(ml[w][0] - top);
-        sum += wt[w] * ml[w][1];
+    // rows 2 t and 2 t + 1: the keys they see
+    int lim[2], from[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int r = rt * 8 + min(2 * t + j, sp.rows - 1);
+        lim[j] = sp.L - sp.n + r / grp + 1;
+        const int64_t lo = p.window > 0 ? int64_t(lim[j]) - p.window : 0;
+        from[j] = int(max(lo, int64_t(0)));
     }
-    for (int d = threadIdx.x; d < D; d += 128) {
-        float o = 0.f;
-        for (int w = 0; w < 4; ++w) o += wt[w] * part[w][d];
-        p.out[(t * p.hq + h) * D + d] = __float2half_rn(sum > 0.f ? o / sum : 0.f);
+    const int all_lim = sp.L - sp.n + rt * 8 / grp + 1;    // keys [all_from, all_lim): seen by every row
+    const int last = sp.L - sp.n + (rt * 8 + min(sp.rows, 8) - 1) / grp + 1;
+    const int all_from = p.window > 0 ? int(max(int64_t(last) - p.window, int64_t(0))) : 0;
+
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, zs[G][2] = {};
+    float o[NB][2][4] = {};                                // [block][nibbles 0, 2 | 1, 3]
+    uint32_t top_exp = 0;                                  // biased fp16 exponent of the largest value scale
+    float factor = 0x1p28f;                                // 2^(28 - top_exp)
+    int slot = 0;
+    uint32_t phase = 0;
+    for (int tile = warp; tile < tiles; tile += KV_WARPS) {
+        const int k0 = c0 + tile * KV_TILE;
+        mbar_wait(&bars[warp * KV_RING + slot], phase, kErrWaitFull, &abort);
+        const uint8_t* base = smem + warp * (KV_RING * Sh::SLOT) + slot * Sh::SLOT;
+        const uint32_t halves = (seen >> (2 * slot)) & 3u;
+        float sc[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {                      // scores of 16 keys
+            uint32_t kw[2][NB];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint8_t* src = base + (h * 16 + i * 8 + kv_key(g)) * (D / 2) + t * (NB * 4);
+                if constexpr (NB == 2) {
+                    const uint2 v = *reinterpret_cast<const uint2*>(src);
+                    kw[i][0] = v.x; kw[i][1] = v.y;
+                } else {
+#pragma unroll
+                    for (int u = 0; u < NB / 4; ++u) {
+                        const uint4 v = *reinterpret_cast<const uint4*>(src + u * 16);
+                        kw[i][4 * u] = v.x; kw[i][4 * u + 1] = v.y;
+                        kw[i][4 * u + 2] = v.z; kw[i][4 * u + 3] = v.w;
+                    }
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[h][e] = 0.f;
+#pragma unroll
+            for (int k = 0; k < G; ++k) {
+                float lo[4], hi[4];
+#pragma unroll
+                for (int i = 0; i < GB; ++i) {
+                    const uint32_t a = kw[0][k * GB + i], c = kw[1][k * GB + i];
+                    const uint32_t a8 = a >> 8, c8 = c >> 8;
+                    const uint32_t (&f)[4] = qf[k * GB + i];
+                    if (i == 0) {
+                        mma_16816_first(lo, a & LO, c & LO, a8 & LO, c8 & LO, f[0], f[1]);
+                        mma_16816_first(hi, a & HI, c & HI, a8 & HI, c8 & HI, f[2], f[3]);
+                    } else {
+                        mma_16816(lo, a & LO, c & LO, a8 & LO, c8 & LO, f[0], f[1]);
+                        mma_16816(hi, a & HI, c & HI, a8 & HI, c8 & HI, f[2], f[3]);
+                    }
+                }
+                const float2 qs = *reinterpret_cast<const float2*>(&qsum[k][2 * t]);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float2 sz = __half22float2(*reinterpret_cast<const __half2*>(
+                        base + 2 * Sh::CODES + ((h * 16 + i * 8 + kv_key(g)) * G + k) * 4));
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float v = fmaf(hi[2 * i + e], 0.0625f, lo[2 * i + e]);
+                        sc[h][2 * i + e] =
+                            fmaf(sz.x, fmaf(-sz.y, e ? qs.y : qs.x, v), sc[h][2 * i + e]);
+                    }
+                }
+            }
+        }
+        const float up = p.scale * 0x1p24f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[h][e] *= up;
+        if (k0 < all_from || k0 + KV_TILE > all_lim || halves != 3u) {     // some keys are not seen
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int key = k0 + h * 16 + (e >> 1) * 8 + kv_key(g);
+                    if (key >= lim[e & 1] || key < from[e & 1] || !((halves >> h) & 1u))
+                        sc[h][e] = -INFINITY;
+                }
+        }
+        // scales and zero points of the lane's four values
+        float2 vz[2][2][G];
+        uint32_t big = 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int k = 0; k < G; ++k) {
+                    const uint32_t w = *reinterpret_cast<const uint32_t*>(
+                        base + 2 * Sh::CODES + Sh::PARAMS +
+                        ((h * 16 + i * 8 + kv_key(g)) * G + k) * 4);
+                    vz[h][i][k] = __half22float2(*reinterpret_cast<const __half2*>(&w));
+                    const int key = k0 + h * 16 + i * 8 + kv_key(g);
+                    // (keys that no row sees: whatever the slot holds)
+                    const bool in = key >= sp.lo && key < c1 && ((halves >> h) & 1u);
+                    if (!in) vz[h][i][k] = make_float2(0.f, 0.f);
+                    big = max(big, in ? (w & 0x7fffu) >> 10 : 0u);
+                }
+        float mx[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            mx[j] = fmaxf(fmaxf(sc[0][j], sc[0][2 + j]), fmaxf(sc[1][j], sc[1][2 + j]));
+#pragma unroll
+            for (int s = 4; s < 32; s <<= 1) mx[j] = fmaxf(mx[j], __shfl_xor_sync(ALL, mx[j], s));
+        }
+        big = __reduce_max_sync(ALL, big);
+        if (__any_sync(ALL, mx[0] > m[0] || mx[1] > m[1]) || big > top_exp) {
+            float down = 1.f;                              // of the outputs, for a larger value scale
+            if (big > top_exp) {
+                down = __uint_as_float((127u - (big - top_exp)) << 23);
+                top_exp = big;
+                factor = __uint_as_float((127u + 28u - big) << 23);
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float mn = fmaxf(m[j], mx[j]);
+                const float al = m[j] == -INFINITY ? 0.f : exp2f(m[j] - mn), ad = al * down;
+                m[j] = mn;
+                l[j] *= al;
+#pragma unroll
+                for (int k = 0; k < G; ++k) zs[k][j] *= ad;
+#pragma unroll
+                for (int i = 0; i < NB; ++i)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        o[i][x][j] *= ad;
+                        o[i][x][2 + j] *= ad;
+                    }
+            }
+        }
+        const float mu[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                sc[h][e] = exp2f(sc[h][e] - mu[e & 1]);
+                l[e & 1] += sc[h][e];
+            }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {                      // out += V^T u of 16 keys
+            uint32_t vw[4][(NB + 1) / 2];                  // keys 2 t, 2 t + 1, and 8 on
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint8_t* src = base + Sh::CODES +
+                                     (h * 16 + (i >> 1) * 8 + kv_key(2 * t + (i & 1))) * (D / 2) +
+                                     g * (NB * 2);
+                if constexpr (NB == 2) {
+                    vw[i][0] = *reinterpret_cast<const uint32_t*>(src);
+                } else if constexpr (NB == 4) {
+                    const uint2 v = *reinterpret_cast<const uint2*>(src);
+                    vw[i][0] = v.x; vw[i][1] = v.y;
+                } else {
+                    const uint4 v = *reinterpret_cast<const uint4*>(src);
+                    vw[i][0] = v.x; vw[i][1] = v.y; vw[i][2] = v.z; vw[i][3] = v.w;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < G; ++k) {
+                uint32_t bh[2], bl[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float s = vz[h][i][k].x * factor;
+                    const float u0 = sc[h][2 * i] * s, u1 = sc[h][2 * i + 1] * s;
+                    zs[k][0] = fmaf(u0, vz[h][i][k].y, zs[k][0]);
+                    zs[k][1] = fmaf(u1, vz[h][i][k].y, zs[k][1]);
+                    const __half2 uh = __floats2half2_rn(u0, u1);
+                    const float2 f = __half22float2(uh);
+                    const __half2 ul = __floats2half2_rn(u0 - f.x, u1 - f.y);
+                    bh[i] = movmatrix(*reinterpret_cast<const uint32_t*>(&uh));
+                    bl[i] = movmatrix(*reinterpret_cast<const uint32_t*>(&ul));
+                }
+#pragma unroll
+                for (int i = k * GB; i < (k + 1) * GB; ++i) {
+                    const uint32_t pick = (i & 1) ? 0x7632 : 0x5410;
+                    const uint32_t a = __byte_perm(vw[0][i / 2], vw[1][i / 2], pick);
+                    const uint32_t c = __byte_perm(vw[2][i / 2], vw[3][i / 2], pick);
+                    const uint32_t a8 = a >> 8, c8 = c >> 8;
+                    mma_16816(o[i][0], a & LO, a8 & LO, c & LO, c8 & LO, bh[0], bh[1]);
+                    mma_16816(o[i][1], a & HI, a8 & HI, c & HI, c8 & HI, bh[0], bh[1]);
+                    mma_16816(o[i][0], a & LO, a8 & LO, c & LO, c8 & LO, bl[0], bl[1]);
+                    mma_16816(o[i][1], a & HI, a8 & HI, c & HI, c8 & HI, bl[0], bl[1]);
+                }
+            }
+        }
+        if (++slot == KV_RING) { slot = 0; phase ^= 1u; }
+        __syncwarp();                                      // every lane has read the slot
+        issue();
     }
+    // sums over the keys of all lanes, then the warp's result in its own units
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int s = 4; s < 32; s <<= 1) {
+            l[j] += __shfl_xor_sync(ALL, l[j], s);
+#pragma unroll
+            for (int k = 0; k < G; ++k) zs[k][j] += __shfl_xor_sync(ALL, zs[k][j], s);
+        }
+    __syncthreads();                                       // every warp is done with its ring
+    const float undo = 1.f / factor;
+    float* mine = reinterpret_cast<float*>(smem) + warp * (8 * D);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        if (g == 0) { wm[warp][2 * t + j] = m[j]; wl[warp][2 * t + j] = l[j]; }
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            const float z = zs[i / GB][j];
+            *reinterpret_cast<float4*>(mine + (2 * t + j) * D + 32 * i + 4 * g) = make_float4(
+                fmaf(o[i][0][j], 0x1p24f, -z) * undo, fmaf(o[i][1][j], 0x1p20f, -z) * undo,
+                fmaf(o[i][0][2 + j], 0x1p24f, -z) * undo, fmaf(o[i][1][2 + j], 0x1p20f, -z) * undo);
+        }
+    }
+    __syncthreads();
+    const int rows = min(sp.rows, 8);
+    const int64_t unit = (int64_t(b) * gridDim.y + blockIdx.y) * p.splits + blockIdx.x;
+    for (int e = threadIdx.x; e < rows * D; e += KV_WARPS * 32) {
+        const int r = e / D, d = e - r * D;
+        float top = -INFINITY, sum = 0.f, v = 0.f;
+#pragma unroll
+        for (int w = 0; w < KV_WARPS; ++w) top = fmaxf(top, wm[w][r]);
+        if (top > -INFINITY) {
+#pragma unroll
+            for (int w = 0; w < KV_WARPS; ++w) {
+                if (wm[w][r] == -INFINITY) continue;
+                const float c = exp2f(wm[w][r] - top);
+                sum = fmaf(c, wl[w][r], sum);
+                v = fmaf(c, reinterpret_cast<const float*>(smem)[w * (8 * D) + e], v);
+            }
+        }
+        if (p.splits == 1) {
+            const int rr = rt * 8 + r;
+            p.out[((sp.s0 + rr / grp) * p.hq + hk * grp + rr % grp) * D + d] =
+                __float2half_rn(sum > 0.f ? v / sum : 0.f);
+        } else {
+            float* dst = p.part + unit * (8 * (D + 2));
+            dst[e] = v;
+            if (d == 0) { dst[8 * D + r] = top; dst[8 * D + 8 + r] = sum; }
+        }
+    }
+}
+
+// out = the chunks' results joined: one warp per row
+template <int D> __global__ void __launch_bounds__(256) kv4_join_kernel(const KvAttn p)
+{
+    constexpr int E = D / 32;
+    pdl_wait();
+    const int lane = threadIdx.x & 31, r = threadIdx.x >> 5;
+    const int b = blockIdx.y, hk = blockIdx.x / p.row_tiles, rt = blockIdx.x - hk * p.row_tiles;
+    const int grp = p.hq / p.hkv;
+    const KvSpan sp = kv_span(p, b, rt);
+    if (!sp.ok || r >= sp.rows) return;
+    const int n = sp.hi > sp.base ? (sp.hi - sp.base + p.chunk - 1) / p.chunk : 0;
+    const float* part = p.part + (int64_t(b) * gridDim.x + blockIdx.x) * p.splits * (8 * (D + 2));
+    float top = -INFINITY, sum = 0.f, v[E] = {};
+    for (int s = lane; s < n; s += 32) top = fmaxf(top, part[int64_t(s) * (8 * (D + 2)) + 8 * D + r]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (top > -INFINITY)
+        for (int s = 0; s < n; ++s) {
+            const float* src = part + int64_t(s) * (8 * (D + 2));
+            const float c = exp2f(src[8 * D + r] - top);   // 0 for a chunk this row does not see
+            sum = fmaf(c, src[8 * D + 8 + r], sum);
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[e] = fmaf(c, src[r * D + e * 32 + lane], v[e]);
+        }
+    const int rr = rt * 8 + r;
+    __half* dst = p.out + ((sp.s0 + rr / grp) * p.hq + hk * grp + rr % grp) * D;
+#pragma unroll
+    for (int e = 0; e < E; ++e) dst[e * 32 + lane] = __float2half_rn(sum > 0.f ? v[e] / sum : 0.f);
+}
+
+// Keys per chunk: a multiple of a CTA's round of tiles, and as few chunks as keep
+// eight CTAs (four at a time) on each SM when every sequence has the bound's length
+struct KvPlan { int chunk, splits, row_tiles; size_t bytes; };
+
+KvPlan kv_plan(int64_t seqs, int hq, int hkv, int D, int64_t max_q, int64_t max_len, int64_t window)
+{
+    KvPlan k{};
+    k.row_tiles = int((max_q * (hq / hkv) + 7) / 8);
+    int64_t span = max_len;
+    if (window > 0) span = std::min(span, window + max_q + 2 * KV_TILE);
+    span = std::max<int64_t>(span, 1);
+    constexpr int ROUND = KV_WARPS * KV_TILE;
+    const int64_t units = seqs * hkv * k.row_tiles;
+    int64_t chunk = (units * span + 148 * 8 - 1) / (148 * 8);
+    chunk = std::max<int64_t>(ROUND, (chunk + ROUND - 1) / ROUND * ROUND);
+    chunk = std::max<int64_t>(chunk, ((span + 4095) / 4096 + ROUND - 1) / ROUND * ROUND);
+    k.chunk = int(std::min<int64_t>(chunk, int64_t(1) << 30));
+    k.splits = int((span + k.chunk - 1) / k.chunk);
+    // splits <= ceil(1184 / units) by the choice of chunk; this bound grows with every
+    // argument, so a workspace for the bounds serves every smaller call
+    const int64_t most = std::min(units * ((max_len + ROUND - 1) / ROUND + 1), units + 148 * 8);
+    k.bytes = align_up(size_t(most) * 8 * (D + 2) * 4, 256);
+    return k;
 }
 
 }  // namespace gptq
@@ -112,7 +529,10 @@ extern "C" size_t gptq_kv4_attention_workspace_bytes(int64_t seqs, int q_heads, 
     if (seqs <= 0 || q_heads <= 0 || kv_heads <= 0 || head_dim <= 0 || max_q_len <= 0 ||
         max_seq_len <= 0)
         return 0;
-    return 256;
+    if (seqs > 65535 || q_heads > 1024 || kv_heads > 1024 || q_heads % kv_heads != 0 || head_dim > 256 ||
+        max_q_len > (int64_t(1) << 24) || max_seq_len > (int64_t(1) << 30))
+        return 0;
+    return gptq::kv_plan(seqs, q_heads, kv_heads, head_dim, max_q_len, max_seq_len, 0).bytes;
 }
 
 extern "C" int gptq_kv4_attention(const uint16_t* q, int64_t tokens, int64_t seqs, int q_heads,
@@ -150,28 +570,46 @@ extern "C" int gptq_kv4_attention(const uint16_t* q, int64_t tokens, int64_t seq
     if (ws_bytes < gptq_kv4_attention_workspace_bytes(seqs, q_heads, kv_heads, head_dim, max_q_len,
                                                       max_seq_len))
         return GPTQ_ERR_INVALID_ARG;
+    const int64_t max_q = std::min(max_q_len, tokens);
+    const KvPlan plan = kv_plan(seqs, q_heads, kv_heads, head_dim, max_q, max_seq_len, window);
+    if (plan.bytes > ws_bytes) return GPTQ_ERR_INVALID_ARG;
+    if (int64_t(kv_heads) * plan.row_tiles > 65535) return GPTQ_ERR_SHAPE;
     KvAttn p{};
     p.q = reinterpret_cast<const __half*>(q);
     p.tokens = tokens; p.seqs = seqs; p.pages = pages; p.width = table_width;
-    p.window = window; p.max_q = std::min(max_q_len, tokens); p.max_len = max_seq_len;
-    p.hq = q_heads; p.hkv = kv_heads; p.g = g;
+    p.window = window; p.max_q = (int)max_q; p.max_len = (int)max_seq_len;
+    p.hq = q_heads; p.hkv = kv_heads;
     while ((1 << p.page_shift) < page_size) ++p.page_shift;
     p.kc = k_codes; p.kp = reinterpret_cast<const __half2*>(k_params);
     p.vc = v_codes; p.vp = reinterpret_cast<const __half2*>(v_params);
     p.table = block_table; p.lens = seq_lens; p.start = q_start;
     p.scale = scale * 1.4426950408889634f;
+    p.chunk = plan.chunk; p.splits = plan.splits; p.row_tiles = plan.row_tiles;
+    p.part = static_cast<float*>(ws);
     p.out = reinterpret_cast<__half*>(out);
     cudaStream_t st = as_stream(stream);
     KernelTimer kt(kKKvAttention, st);
-    const dim3 grid((unsigned)p.max_q, (unsigned)q_heads, (unsigned)seqs);
-    auto run = [&](auto kern) {
-        kern<<<grid, 128, 0, st>>>(p);
+    auto run = [&](auto kern, auto join, int smem) -> int {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+            cudaSuccess)
+            return GPTQ_ERR_CUDA;
+        kern<<<dim3((unsigned)p.splits, (unsigned)(kv_heads * p.row_tiles), (unsigned)seqs),
+               KV_WARPS * 32, smem, st>>>(p);
         count_launches();
+        if (p.splits > 1) {
+            if (launch_after(join, dim3((unsigned)(kv_heads * p.row_tiles), (unsigned)seqs), 256, 0,
+                             st, p) != cudaSuccess)
+                return GPTQ_ERR_CUDA;
+            count_launches();
+        }
         return launch_status();
     };
-    switch (head_dim) {
-        case 64: return run(kv4_attention_simple_kernel<2>);
-        case 128: return run(kv4_attention_simple_kernel<4>);
-        default: return run(kv4_attention_simple_kernel<8>);
-    }
+#define KV_RUN(D, G)                                                                            \
+    if (head_dim == D && g * G == D)                                                            \
+        return run(kv4_attention_kernel<D, G>, kv4_join_kernel<D>, KvShape<D, G>::SMEM);
+    KV_RUN(64, 1) KV_RUN(64, 2)
+    KV_RUN(128, 1) KV_RUN(128, 2) KV_RUN(128, 4)
+    KV_RUN(256, 1) KV_RUN(256, 2) KV_RUN(256, 4) KV_RUN(256, 8)
+#undef KV_RUN
+    return GPTQ_ERR_UNSUPPORTED;
 }
