@@ -20,7 +20,10 @@
 //  * out^T = V^T p: two keys' words of the same elements, merged half by half, give
 //    operand registers of two keys again by one AND.  A value's scale goes into its
 //    probability: u = p s, in two fp16 parts (22 bits), scaled by a power of two that
-//    follows the largest s; its zero point into sum u z, subtracted at the end.
+//    follows the largest s; its zero point into sum u (z - 8), subtracted at the end
+//    from the sum over the codes c - 8.
+//  * The running maximum follows the scores in steps of KV_LAZY: p = 2^(score - m) may
+//    reach 2^KV_LAZY before the outputs are scaled again, which few tiles ask for.
 //  * The rows of an operand are the keys kv_key(g) of its eight: the same keys are
 //    then two neighbouring columns of the other product's operand, and the reads of
 //    shared memory hit every bank as often (keys) or twice (values).
@@ -34,6 +37,7 @@
 namespace gptq {
 
 constexpr int KV_WARPS = 4, KV_TILE = 32, KV_RING = 3;
+constexpr float KV_LAZY = 7.f;
 
 struct KvAttn {
     const __half* q;
@@ -54,6 +58,24 @@ struct KvAttn {
 
 // Key of row g of an operand's eight
 __device__ __forceinline__ int kv_key(int g) { return (g & 1) ? 4 + ((g >> 1) ^ 1) : (g >> 1); }
+
+// 2^x, 2 ulp, 0 for -inf and below the normal numbers
+__device__ __forceinline__ float ex2(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// Two codes, c 2^-14 / scale each -> (c - 8) 2^-14, exact: normal numbers around 0, so
+// that neither the matrix pipe's alignment of subnormals nor the rounding of long sums of
+// codes of one sign costs bits of their difference to the zero points
+__device__ __forceinline__ uint32_t kv_center(uint32_t v, float scale)
+{
+    const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&v), __float2half2_rn(scale),
+                              __float2half2_rn(-8.f * 0x1p-14f));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
 
 __device__ __forceinline__ uint32_t movmatrix(uint32_t v)
 {
@@ -103,10 +125,11 @@ template <int D, int G> struct KvShape {
     static constexpr int RING = KV_WARPS * KV_RING * SLOT;
     static constexpr int JOIN = KV_WARPS * 8 * D * 4;      // in the ring's place, at the end
     static constexpr int SMEM = (RING > JOIN ? RING : JOIN) + 128;
+    static constexpr int CTAS = D == 64 ? 4 : D == 128 && G < 4 ? 4 : 2;   // per SM, by registers
 };
 
 template <int D, int G>
-__global__ void __launch_bounds__(KV_WARPS * 32) kv4_attention_kernel(const KvAttn p)
+__global__ void __launch_bounds__(KV_WARPS * 32, KvShape<D, G>::CTAS) kv4_attention_kernel(const KvAttn p)
 {
     using Sh = KvShape<D, G>;
     constexpr int NB = Sh::NB, GB = Sh::GB;
@@ -141,20 +164,25 @@ __global__ void __launch_bounds__(KV_WARPS * 32) kv4_attention_kernel(const KvAt
     const uint32_t bar0 = smem_u32(&bars[warp * KV_RING]);
     const int half = (lane >> 2) & 1, what = lane & 3;
     const int32_t* table = p.table + int64_t(b) * p.width;
-    int ptile = warp, pslot = 0;
+    const uint32_t keyb = what < 2 ? D / 2 : G * 4;        // bytes of a key
+    const uint32_t bytes = keyb * 16, mask = (1u << p.page_shift) - 1u;
+    const uint32_t pageb = (uint32_t(p.hkv) * keyb) << p.page_shift;
+    const uint8_t* from0 =
+        (what == 0 ? reinterpret_cast<const uint8_t*>(p.kc)
+                   : what == 1 ? reinterpret_cast<const uint8_t*>(p.vc)
+                               : what == 2 ? reinterpret_cast<const uint8_t*>(p.kp)
+                                           : reinterpret_cast<const uint8_t*>(p.vp)) +
+        ((uint32_t(hk) * keyb) << p.page_shift);
+    const uint32_t to0 = ring + (what < 2 ? what * Sh::CODES : 2 * Sh::CODES + (what - 2) * Sh::PARAMS) +
+                         half * bytes;
+    int ptile = warp, pslot = 0, pkey = c0 + warp * KV_TILE + half * 16;
     uint32_t seen = 0;                                     // two bits a slot: halves with a valid page
-    int page = 0;
-    auto look = [&]() {
-        const int key = c0 + ptile * KV_TILE + half * 16;
-        page = key < c1 ? table[key >> p.page_shift] : 0;
-    };
+    uint32_t page = 0;
+    auto look = [&]() { page = pkey < c1 ? uint32_t(table[pkey >> p.page_shift]) : 0u; };
     auto issue = [&]() {
         if (ptile >= tiles) return;
-        const int key = c0 + ptile * KV_TILE + half * 16;
-        const bool in = key < c1;
-        const bool valid = page >= 0 && page < p.pages;
-        if (lane < 8 && in && !valid) atomicCAS(&g_device_status, 0, kErrIndex);
-        const bool go = lane < 8 && in && valid;
+        const bool in = pkey < c1 && lane < 8, go = in && page < uint32_t(p.pages);
+        if (in && !go) atomicCAS(&g_device_status, 0, kErrIndex);
         const uint32_t who = __ballot_sync(ALL, go);
         const uint32_t halves = (who & 1u) | ((who >> 3) & 2u);
         seen = (seen & ~(3u << (2 * pslot))) | (halves << (2 * pslot));
@@ -164,18 +192,11 @@ __global__ void __launch_bounds__(KV_WARPS * 32) kv4_attention_kernel(const KvAt
                          "r"(uint32_t(__popc(halves)) * (Sh::SLOT / 2))
                          : "memory");
         __syncwarp();
-        if (go) {
-            const int64_t row = ((int64_t(page) * p.hkv + hk) << p.page_shift) +
-                                (key & ((1 << p.page_shift) - 1));
-            const uint32_t dst = ring + pslot * Sh::SLOT;
-            if (what < 2)
-                kv_bulk(dst + what * Sh::CODES + half * (Sh::CODES / 2),
-                        (what ? p.vc : p.kc) + row * (D / 8), Sh::CODES / 2, bar);
-            else
-                kv_bulk(dst + 2 * Sh::CODES + (what - 2) * Sh::PARAMS + half * (Sh::PARAMS / 2),
-                        (what == 3 ? p.vp : p.kp) + row * G, Sh::PARAMS / 2, bar);
-        }
+        if (go)
+            kv_bulk(to0 + pslot * Sh::SLOT, from0 + (uint64_t(page) * pageb + (uint32_t(pkey) & mask) * keyb),
+                    bytes, bar);
         ptile += KV_WARPS;
+        pkey += KV_WARPS * KV_TILE;
         pslot = pslot + 1 == KV_RING ? 0 : pslot + 1;
         look();
     };
@@ -230,7 +251,8 @@ __global__ void __launch_bounds__(KV_WARPS * 32) kv4_attention_kernel(const KvAt
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, zs[G][2] = {};
     float o[NB][2][4] = {};                                // [block][nibbles 0, 2 | 1, 3]
     uint32_t top_exp = 0;                                  // biased fp16 exponent of the largest value scale
-    float factor = 0x1p28f;                                // 2^(28 - top_exp)
+    float factor = 0x1p21f;                                // 2^(21 - top_exp): u < 2^(7 + KV_LAZY)
+    const float up = p.scale * 0x1p24f;
     int slot = 0;
     uint32_t phase = 0;
     for (int tile = warp; tile < tiles; tile += KV_WARPS) {
@@ -278,8 +300,9 @@ __global__ void __launch_bounds__(KV_WARPS * 32) kv4_attention_kernel(const KvAt
                 const float2 qs = *reinterpret_cast<const float2*>(&qsum[k][2 * t]);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const float2 sz = __half22float2(*reinterpret_cast<const __half2*>(
+                    float2 sz = __half22float2(*reinterpret_cast<const __half2*>(
                         base + 2 * Sh::CODES + ((h * 16 + i * 8 + kv_key(g)) * G + k) * 4));
+                    sz.x *= up;
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const float v = fmaf(hi[2 * i + e], 0.0625f, lo[2 * i + e]);
@@ -289,12 +312,8 @@ __global__ void __launch_bounds__(KV_WARPS * 32) kv4_attention_kernel(const KvAt
                 }
             }
         }
-        const float up = p.scale * 0x1p24f;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sc[h][e] *= up;
-        if (k0 < all_from || k0 + KV_TILE > all_lim || halves != 3u) {     // some keys are not seen
+        const bool edge = k0 < all_from || k0 + KV_TILE > all_lim || halves != 3u;
+        if (edge) {                                        // some keys are not seen by some row
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -305,24 +324,33 @@ __global__ void __launch_bounds__(KV_WARPS * 32) kv4_attention_kernel(const KvAt
                 }
         }
         // scales and zero points of the lane's four values
-        float2 vz[2][2][G];
-        uint32_t big = 0;
+        uint32_t vz[2][2][G], big = 0;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int k = 0; k < G; ++k) {
-                    const uint32_t w = *reinterpret_cast<const uint32_t*>(
+                for (int k = 0; k < G; ++k)
+                    vz[h][i][k] = *reinterpret_cast<const uint32_t*>(
                         base + 2 * Sh::CODES + Sh::PARAMS +
                         ((h * 16 + i * 8 + kv_key(g)) * G + k) * 4);
-                    vz[h][i][k] = __half22float2(*reinterpret_cast<const __half2*>(&w));
+        if (edge) {                                        // keys that no row sees: whatever the slot holds
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
                     const int key = k0 + h * 16 + i * 8 + kv_key(g);
-                    // (keys that no row sees: whatever the slot holds)
-                    const bool in = key >= sp.lo && key < c1 && ((halves >> h) & 1u);
-                    if (!in) vz[h][i][k] = make_float2(0.f, 0.f);
-                    big = max(big, in ? (w & 0x7fffu) >> 10 : 0u);
+                    if (key < sp.lo || key >= c1 || !((halves >> h) & 1u))
+#pragma unroll
+                        for (int k = 0; k < G; ++k) vz[h][i][k] = 0u;
                 }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int k = 0; k < G; ++k) big = max(big, vz[h][i][k] & 0x7fffu);
         float mx[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -330,18 +358,18 @@ __global__ void __launch_bounds__(KV_WARPS * 32) kv4_attention_kernel(const KvAt
 #pragma unroll
             for (int s = 4; s < 32; s <<= 1) mx[j] = fmaxf(mx[j], __shfl_xor_sync(ALL, mx[j], s));
         }
-        big = __reduce_max_sync(ALL, big);
-        if (__any_sync(ALL, mx[0] > m[0] || mx[1] > m[1]) || big > top_exp) {
+        big = __reduce_max_sync(ALL, big) >> 10;
+        if (__any_sync(ALL, mx[0] > m[0] + KV_LAZY || mx[1] > m[1] + KV_LAZY) || big > top_exp) {
             float down = 1.f;                              // of the outputs, for a larger value scale
             if (big > top_exp) {
                 down = __uint_as_float((127u - (big - top_exp)) << 23);
                 top_exp = big;
-                factor = __uint_as_float((127u + 28u - big) << 23);
+                factor = __uint_as_float((127u + 21u - big) << 23);
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const float mn = fmaxf(m[j], mx[j]);
-                const float al = m[j] == -INFINITY ? 0.f : exp2f(m[j] - mn), ad = al * down;
+                const float al = m[j] == -INFINITY ? 0.f : ex2(m[j] - mn), ad = al * down;
                 m[j] = mn;
                 l[j] *= al;
 #pragma unroll
@@ -360,7 +388,7 @@ __global__ void __launch_bounds__(KV_WARPS * 32) kv4_attention_kernel(const KvAt
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                sc[h][e] = exp2f(sc[h][e] - mu[e & 1]);
+                sc[h][e] = ex2(sc[h][e] - mu[e & 1]);
                 l[e & 1] += sc[h][e];
             }
 #pragma unroll
@@ -386,10 +414,11 @@ __global__ void __launch_bounds__(KV_WARPS * 32) kv4_attention_kernel(const KvAt
                 uint32_t bh[2], bl[2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const float s = vz[h][i][k].x * factor;
+                    const float2 sz = __half22float2(*reinterpret_cast<const __half2*>(&vz[h][i][k]));
+                    const float s = sz.x * factor, z = sz.y - 8.f;
                     const float u0 = sc[h][2 * i] * s, u1 = sc[h][2 * i + 1] * s;
-                    zs[k][0] = fmaf(u0, vz[h][i][k].y, zs[k][0]);
-                    zs[k][1] = fmaf(u1, vz[h][i][k].y, zs[k][1]);
+                    zs[k][0] = fmaf(u0, z, zs[k][0]);
+                    zs[k][1] = fmaf(u1, z, zs[k][1]);
                     const __half2 uh = __floats2half2_rn(u0, u1);
                     const float2 f = __half22float2(uh);
                     const __half2 ul = __floats2half2_rn(u0 - f.x, u1 - f.y);
@@ -402,10 +431,14 @@ __global__ void __launch_bounds__(KV_WARPS * 32) kv4_attention_kernel(const KvAt
                     const uint32_t a = __byte_perm(vw[0][i / 2], vw[1][i / 2], pick);
                     const uint32_t c = __byte_perm(vw[2][i / 2], vw[3][i / 2], pick);
                     const uint32_t a8 = a >> 8, c8 = c >> 8;
-                    mma_16816(o[i][0], a & LO, a8 & LO, c & LO, c8 & LO, bh[0], bh[1]);
-                    mma_16816(o[i][1], a & HI, a8 & HI, c & HI, c8 & HI, bh[0], bh[1]);
-                    mma_16816(o[i][0], a & LO, a8 & LO, c & LO, c8 & LO, bl[0], bl[1]);
-                    mma_16816(o[i][1], a & HI, a8 & HI, c & HI, c8 & HI, bl[0], bl[1]);
+                    const uint32_t n0 = kv_center(a & LO, 1024.f), n1 = kv_center(a8 & LO, 1024.f);
+                    const uint32_t n2 = kv_center(c & LO, 1024.f), n3 = kv_center(c8 & LO, 1024.f);
+                    const uint32_t h0 = kv_center(a & HI, 64.f), h1 = kv_center(a8 & HI, 64.f);
+                    const uint32_t h2 = kv_center(c & HI, 64.f), h3 = kv_center(c8 & HI, 64.f);
+                    mma_16816(o[i][0], n0, n1, n2, n3, bh[0], bh[1]);
+                    mma_16816(o[i][1], h0, h1, h2, h3, bh[0], bh[1]);
+                    mma_16816(o[i][0], n0, n1, n2, n3, bl[0], bl[1]);
+                    mma_16816(o[i][1], h0, h1, h2, h3, bl[0], bl[1]);
                 }
             }
         }
@@ -432,8 +465,8 @@ __global__ void __launch_bounds__(KV_WARPS * 32) kv4_attention_kernel(const KvAt
         for (int i = 0; i < NB; ++i) {
             const float z = zs[i / GB][j];
             *reinterpret_cast<float4*>(mine + (2 * t + j) * D + 32 * i + 4 * g) = make_float4(
-                fmaf(o[i][0][j], 0x1p24f, -z) * undo, fmaf(o[i][1][j], 0x1p20f, -z) * undo,
-                fmaf(o[i][0][2 + j], 0x1p24f, -z) * undo, fmaf(o[i][1][2 + j], 0x1p20f, -z) * undo);
+                fmaf(o[i][0][j], 0x1p14f, -z) * undo, fmaf(o[i][1][j], 0x1p14f, -z) * undo,
+                fmaf(o[i][0][2 + j], 0x1p14f, -z) * undo, fmaf(o[i][1][2 + j], 0x1p14f, -z) * undo);
         }
     }
     __syncthreads();
@@ -448,7 +481,7 @@ __global__ void __launch_bounds__(KV_WARPS * 32) kv4_attention_kernel(const KvAt
 #pragma unroll
             for (int w = 0; w < KV_WARPS; ++w) {
                 if (wm[w][r] == -INFINITY) continue;
-                const float c = exp2f(wm[w][r] - top);
+                const float c = ex2(wm[w][r] - top);
                 sum = fmaf(c, wl[w][r], sum);
                 v = fmaf(c, reinterpret_cast<const float*>(smem)[w * (8 * D) + e], v);
             }
@@ -484,7 +517,7 @@ template <int D> __global__ void __launch_bounds__(256) kv4_join_kernel(const Kv
     if (top > -INFINITY)
         for (int s = 0; s < n; ++s) {
             const float* src = part + int64_t(s) * (8 * (D + 2));
-            const float c = exp2f(src[8 * D + r] - top);   // 0 for a chunk this row does not see
+            const float c = ex2(src[8 * D + r] - top);   // 0 for a chunk this row does not see
             sum = fmaf(c, src[8 * D + 8 + r], sum);
 #pragma unroll
             for (int e = 0; e < E; ++e) v[e] = fmaf(c, src[r * D + e * 32 + lane], v[e]);
