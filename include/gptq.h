@@ -462,7 +462,7 @@ int gptq_w4a16_lora(const uint16_t* x, int64_t batch, const uint32_t* qweight,
  * qweight_out / scales_out / qzeros_out: n_experts packed layers D_e of d_model
  *    x d_ff; perm_out: n_experts x d_ff int32 or NULL.
  * group_size: a multiple of 32 dividing d_model and d_ff, or -1 (one group per
- *    row).  d_model, d_ff: multiples of 128; d_model 128 .. 24576, d_ff 128 ..
+ *    row).  d_model, d_ff: multiples of 128; d_model 128 .. 20480, d_ff 128 ..
  *    32768.
  * 0 <= tokens <= 64 (0: no-op), 1 <= n_experts <= 256, 1 <= top_k <=
  * min(8, n_experts).

@@ -622,12 +622,11 @@ extern "C" int gptq_kv4_attention(const uint16_t* q, int64_t tokens, int64_t seq
     p.out = reinterpret_cast<__half*>(out);
     cudaStream_t st = as_stream(stream);
     KernelTimer kt(kKKvAttention, st);
-    auto run = [&](auto kern, auto join, int smem) -> int {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-            cudaSuccess)
-            return GPTQ_ERR_CUDA;
+    auto run = [&](auto kern, auto join, int smem, std::atomic<bool> (&done)[64]) -> int {
+        if (!smem_opt_in(reinterpret_cast<const void*>(kern), smem, done)) return GPTQ_ERR_CUDA;
         kern<<<dim3((unsigned)p.splits, (unsigned)(kv_heads * p.row_tiles), (unsigned)seqs),
                KV_WARPS * 32, smem, st>>>(p);
+        if (launch_status() != GPTQ_OK) return GPTQ_ERR_CUDA;
         count_launches();
         if (p.splits > 1) {
             if (launch_after(join, dim3((unsigned)(kv_heads * p.row_tiles), (unsigned)seqs), 256, 0,
@@ -638,8 +637,10 @@ extern "C" int gptq_kv4_attention(const uint16_t* q, int64_t tokens, int64_t seq
         return launch_status();
     };
 #define KV_RUN(D, G)                                                                            \
-    if (head_dim == D && g * G == D)                                                            \
-        return run(kv4_attention_kernel<D, G>, kv4_join_kernel<D>, KvShape<D, G>::SMEM);
+    if (head_dim == D && g * G == D) {                                                          \
+        static std::atomic<bool> done[64];                                                      \
+        return run(kv4_attention_kernel<D, G>, kv4_join_kernel<D>, KvShape<D, G>::SMEM, done);  \
+    }
     KV_RUN(64, 1) KV_RUN(64, 2)
     KV_RUN(128, 1) KV_RUN(128, 2) KV_RUN(128, 4)
     KV_RUN(256, 1) KV_RUN(256, 2) KV_RUN(256, 4) KV_RUN(256, 8)

@@ -36,6 +36,8 @@
 // of two per column.
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 #include "tc_common.cuh"
 
@@ -44,6 +46,7 @@ namespace gptq {
 constexpr int W4_THREADS = 512;
 constexpr int W4_RING = 2;                        // slots in flight per warp
 constexpr int W4_SLOT = 4096;                     // bytes of one: two steps of 32 rows
+constexpr int W4_MAX_SMEM = 226 * 1024;           // dynamic shared memory of a CTA
 constexpr int W4_STEP = 128;                      // columns per step
 constexpr int W4_COLS = 8;                        // columns n of an operand
 
@@ -658,6 +661,19 @@ __device__ __forceinline__ void w4_sweep(W4Pipe& pipe, const CUtensorMap* tm, co
         }
     }
     __syncthreads();                                       // x and red free again
+}
+
+// The opt-in to dynamic shared memory, set once per kernel and device (most:
+// the largest that any call of the kernel asks for)
+inline bool smem_opt_in(const void* kern, int most, std::atomic<bool> (&done)[64])
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    if (dev >= 0 && dev < 64 && done[dev].load(std::memory_order_acquire)) return true;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess)
+        return false;
+    if (dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_release);
+    return true;
 }
 
 // A kernel on the stream that may start before its predecessor on it has ended

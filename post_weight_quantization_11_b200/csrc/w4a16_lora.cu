@@ -263,12 +263,15 @@ extern "C" int gptq_w4a16_lora(const uint16_t* x, int64_t batch, const uint32_t*
     const size_t smem = w4_smem(plan.slice, plan.chunk, plan.nt, wide, false);
     auto kern = plan.nt == 1 ? (wide ? lora_product_kernel<1, true> : lora_product_kernel<1, false>)
                              : (wide ? lora_product_kernel<2, true> : lora_product_kernel<2, false>);
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-        cudaSuccess)
+    static std::atomic<bool> done[4][64];
+    if (smem > W4_MAX_SMEM) return GPTQ_ERR_SHAPE;
+    if (!smem_opt_in(reinterpret_cast<const void*>(kern), W4_MAX_SMEM,
+                     done[(plan.nt - 1) * 2 + (wide ? 1 : 0)]))
         return GPTQ_ERR_CUDA;
     const int64_t units = int64_t(plan.chunks) * plan.slices * plan.groups;
     kern<<<(unsigned)std::min<int64_t>(device_sm_count(), units), W4_THREADS, smem, st>>>(tm, p);
-    if (launch_after(lora_join_kernel, dim3((unsigned)ceil_div(d_out, 256), (unsigned)ceil_div(batch, LORA_JOIN)),
+    if (launch_status() != GPTQ_OK ||
+        launch_after(lora_join_kernel, dim3((unsigned)ceil_div(d_out, 256), (unsigned)ceil_div(batch, LORA_JOIN)),
                      256, 0, st, p) != cudaSuccess)
         return GPTQ_ERR_CUDA;
     count_launches(2);

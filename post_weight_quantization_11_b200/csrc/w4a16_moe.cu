@@ -16,8 +16,9 @@
 namespace gptq {
 
 constexpr int kMoeTokens = 64, kMoeExperts = 256, kMoeTopK = 8;
-constexpr int64_t kMoeMaxModel = 24576;     // a row of x has to fit beside the ring
+constexpr int64_t kMoeMaxModel = 20480;     // a row of x has to fit beside the ring
 // Of w4_sweep: more column shares make finer row groups, fewer make longer ones
+constexpr int MOE_MAX_SMEM = W4_MAX_SMEM - 11 * 1024;     // beside the routes
 constexpr int MOE_IN_KW = 8, MOE_IN_ROWS = 16 * (W4_WARPS / MOE_IN_KW);
 constexpr int MOE_OUT_KW = 4, MOE_OUT_ROWS = 32 * (W4_WARPS / MOE_OUT_KW);
 constexpr int kMoeSms = 148;               // the plan does not depend on the device that is current
@@ -279,6 +280,8 @@ __global__ void __launch_bounds__(256) moe_join_kernel(const MoeParams p)
     p.y[t * p.d + r] = y;
 }
 
+static_assert(sizeof(MoeRoutes) + 3 * 4 * kMoeExperts + 256 <= 11 * 1024 - 256, "static shared memory");
+
 struct MoePlan {
     int chunk, slices, slice;
     size_t smem_in, smem_out, at_h, at_part, bytes;
@@ -377,19 +380,21 @@ extern "C" int gptq_w4a16_moe(const uint16_t* x, int64_t tokens, const float* lo
     auto ctas = [&](int64_t units) { return (unsigned)std::min<int64_t>(sms, units); };
     auto in = gi % W4_STEP == 0 ? moe_in_kernel<true> : moe_in_kernel<false>;
     auto out = go % W4_STEP == 0 ? moe_out_kernel<true> : moe_out_kernel<false>;
-    if (cudaFuncSetAttribute(in, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)plan.smem_in) !=
-            cudaSuccess ||
-        cudaFuncSetAttribute(out, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)plan.smem_out) != cudaSuccess)
+    static std::atomic<bool> done[4][64];
+    if (!smem_opt_in(reinterpret_cast<const void*>(in), MOE_MAX_SMEM, done[gi % W4_STEP == 0]) ||
+        !smem_opt_in(reinterpret_cast<const void*>(out), MOE_MAX_SMEM, done[2 + (go % W4_STEP == 0)]))
         return GPTQ_ERR_CUDA;
     const int64_t pairs = tokens * top_k;
     CUtensorMap ti, to;
     if (w4_tmap(&ti, qweight_in, n_experts * 2 * d_ff, d_model, 16) != GPTQ_OK ||
         w4_tmap(&to, qweight_out, n_experts * d_model, d_ff, 32) != GPTQ_OK)
         return GPTQ_ERR_CUDA;
+    if (plan.smem_in > MOE_MAX_SMEM || plan.smem_out > MOE_MAX_SMEM) return GPTQ_ERR_SHAPE;
     in<<<ctas(pairs * (d_ff / MOE_IN_ROWS)), W4_THREADS, plan.smem_in, st>>>(ti, p);
-    if (launch_after(out, ctas(pairs * plan.slices * (d_model / MOE_OUT_ROWS)),
-                     W4_THREADS, plan.smem_out, st, to, p) != cudaSuccess ||
+    // what follows reads what the kernel before it wrote: not launched without it
+    if (launch_status() != GPTQ_OK ||
+        launch_after(out, ctas(pairs * plan.slices * (d_model / MOE_OUT_ROWS)), W4_THREADS,
+                     plan.smem_out, st, to, p) != cudaSuccess ||
         launch_after(moe_join_kernel, dim3((unsigned)ceil_div(d_model, 256), (unsigned)tokens), 256,
                      0, st, p) != cudaSuccess)
         return GPTQ_ERR_CUDA;

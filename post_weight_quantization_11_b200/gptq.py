@@ -577,56 +577,76 @@ def gptq_w4a16_matmul(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tens
     return y
 
 
-def _same_device(dev, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} must be on {dev}, got {t.device}")
+# The decode-step calls below run once per token and layer, so their checks are
+# written to be cheap: a call costs the host less than the kernels it launches.
+
+def _bad(t, name: str, dtype, index):
+    _need(t, name, dtype)
+    raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
 
 
-def _call(fn: str, dev, *args):
-    """The entry point on the device's current stream (made current for the call)."""
-    f = getattr(load_library(), fn)
-    if dev.index == torch.cuda.current_device():
-        _check(fn, f(*args, torch.cuda.current_stream(dev).cuda_stream))
+def _on(t, name: str, dtype, index: int):
+    """_need, and on the device with this index"""
+    if not (t.dtype is dtype and t.get_device() == index and t.is_contiguous()):
+        _bad(t, name, dtype, index)
+
+
+def _tensor(t, name: str):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.get_device()
+
+
+def _call(fn: str, index: int, *args):
+    """The entry point on the device's current stream (the device made current for the call)."""
+    f = getattr(_lib or load_library(), fn)
+    if index == torch._C._cuda_getDevice():
+        status = f(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
-        with torch.cuda.device(dev):
-            _check(fn, f(*args, torch.cuda.current_stream(dev).cuda_stream))
+        with torch.cuda.device(index):
+            status = f(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status:
+        raise GptqError(fn, status)
 
 
 def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _out(t, name: str, shape, dtype, dev):
+def _out(t, name: str, shape, dtype, like):
     """The caller's output, checked, or a new one."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    _need(t, name, dtype)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+        return like.new_empty(shape, dtype=dtype)
+    _on(t, name, dtype, like.get_device())
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
     return t
 
 
-def _workspace(ws, nbytes: int, dev):
+def _workspace(ws, nbytes: int, like):
+    """(workspace, its bytes): the caller's, checked, or a new one."""
     if ws is None:
-        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
-    _need(ws, "ws")
-    return ws
+        return like.new_empty(max(nbytes, 16), dtype=torch.uint8), max(nbytes, 16)
+    if not isinstance(ws, torch.Tensor):
+        raise ValueError("ws must be a CUDA tensor")
+    _on(ws, "ws", ws.dtype, like.get_device())
+    return ws, ws.numel() * ws.element_size()
 
 
-def _packed_layer(qweight, scales, qzeros, perm, lead, m, d, group_size, tag=""):
+def _packed_layer(qweight, scales, qzeros, perm, lead, m, d, group_size, index, tag=""):
     """Checks a packed layer (or a stack of them, lead = (E,)) of m x d."""
-    _need(qweight, "qweight" + tag, torch.int32)
-    _need(scales, "scales" + tag, torch.float16)
-    _need(qzeros, "qzeros" + tag, torch.uint8)
+    _on(qweight, "qweight" + tag, torch.int32, index)
+    _on(scales, "scales" + tag, torch.float16, index)
+    _on(qzeros, "qzeros" + tag, torch.uint8, index)
     G = 1 if group_size == -1 else d // max(1, group_size)
-    for t, name, shape in ((qweight, "qweight", (m, d // 8)), (scales, "scales", (m, G)),
-                           (qzeros, "qzeros", (m, (G + 1) // 2))):
-        if tuple(t.shape) != (*lead, *shape):
-            raise ValueError(f"{name}{tag} must be {(*lead, *shape)}, got {tuple(t.shape)}")
+    if qweight.shape != (*lead, m, d // 8) or scales.shape != (*lead, m, G) or \
+            qzeros.shape != (*lead, m, (G + 1) // 2):
+        raise ValueError(f"qweight{tag}, scales{tag}, qzeros{tag} must be {(*lead, m, d // 8)}, "
+                         f"{(*lead, m, G)}, {(*lead, m, (G + 1) // 2)}, got {tuple(qweight.shape)}, "
+                         f"{tuple(scales.shape)}, {tuple(qzeros.shape)}")
     if perm is not None:
-        _need(perm, "perm" + tag, torch.int32)
-        if tuple(perm.shape) != (*lead, d):
+        _on(perm, "perm" + tag, torch.int32, index)
+        if perm.shape != (*lead, d):
             raise ValueError(f"perm{tag} must be {(*lead, d)}, got {tuple(perm.shape)}")
 
 
@@ -643,27 +663,26 @@ def gptq_w4a16_lora(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor
     A_a^T) B_a^T (batch x d_out fp32).  x: batch x d_in fp16; lora_a: adapters x
     rank x d_in, lora_b: adapters x d_out x rank fp16; adapter: batch int32
     (-1: none); lora_scaling: adapters fp32."""
-    _need(x, "x", torch.float16)
-    _need(lora_a, "lora_a", torch.float16)
-    _need(lora_b, "lora_b", torch.float16)
-    _need(adapter, "adapter", torch.int32)
-    _need(lora_scaling, "lora_scaling", torch.float32)
+    dev = _tensor(x, "x")
+    _on(x, "x", torch.float16, dev)
+    _on(lora_a, "lora_a", torch.float16, dev)
+    _on(lora_b, "lora_b", torch.float16, dev)
+    _on(adapter, "adapter", torch.int32, dev)
+    _on(lora_scaling, "lora_scaling", torch.float32, dev)
     b, d = x.shape
     m = qweight.shape[0]
     n, r = lora_a.shape[0], lora_a.shape[1]
-    _packed_layer(qweight, scales, qzeros, perm, (), m, d, group_size)
+    _packed_layer(qweight, scales, qzeros, perm, (), m, d, group_size, dev)
     if lora_a.shape != (n, r, d) or lora_b.shape != (n, m, r):
         raise ValueError("lora_a must be adapters x rank x d_in, lora_b adapters x d_out x rank")
     if adapter.shape != (b,) or lora_scaling.shape != (n,):
         raise ValueError("adapter must have one entry per row of x, lora_scaling one per adapter")
-    dev = x.device
-    y = _out(y, "y", (b, m), torch.float32, dev)
-    ws = _workspace(ws, gptq_w4a16_lora_workspace_bytes(b, m, d, r), dev)
-    _same_device(dev, qweight=qweight, scales=scales, qzeros=qzeros, perm=perm, lora_a=lora_a,
-                 lora_b=lora_b, adapter=adapter, lora_scaling=lora_scaling, y=y, ws=ws)
-    _call("gptq_w4a16_lora", dev, _addr(x), b, _addr(qweight), _addr(scales), _addr(qzeros),
-          _addr(perm), m, d, int(group_size), _addr(lora_a), _addr(lora_b), _addr(lora_scaling),
-          _addr(adapter), n, r, _addr(y), _addr(ws), ws.numel() * ws.element_size())
+    y = _out(y, "y", (b, m), torch.float32, x)
+    lib = _lib or load_library()
+    ws, nb = _workspace(ws, lib.gptq_w4a16_lora_workspace_bytes(b, m, d, r), x)
+    _call("gptq_w4a16_lora", dev, x.data_ptr(), b, qweight.data_ptr(), scales.data_ptr(),
+          qzeros.data_ptr(), _addr(perm), m, d, group_size, lora_a.data_ptr(), lora_b.data_ptr(),
+          lora_scaling.data_ptr(), adapter.data_ptr(), n, r, y.data_ptr(), ws.data_ptr(), nb)
     return y
 
 
@@ -684,25 +703,23 @@ def gptq_w4a16_moe(x: torch.Tensor, logits: torch.Tensor, qweight_in: torch.Tens
     (-inf or NaN: masked); the packed stacks: E x 2 d_ff x d_model (gate rows,
     then up rows) and E x d_model x d_ff, as quantize_moe_from_inputs packs
     them; perm_in: E x d_model, perm_out: E x d_ff."""
-    _need(x, "x", torch.float16)
-    _need(logits, "logits", torch.float32)
+    dev = _tensor(x, "x")
+    _on(x, "x", torch.float16, dev)
+    _on(logits, "logits", torch.float32, dev)
     T, d = x.shape
     E = logits.shape[1]
     f = qweight_out.shape[-1] * 8
     if logits.shape != (T, E):
         raise ValueError("logits must be tokens x experts")
-    _packed_layer(qweight_in, scales_in, qzeros_in, perm_in, (E,), 2 * f, d, group_size, "_in")
-    _packed_layer(qweight_out, scales_out, qzeros_out, perm_out, (E,), d, f, group_size, "_out")
-    dev = x.device
-    y = _out(y, "y", (T, d), torch.float32, dev)
-    ws = _workspace(ws, gptq_w4a16_moe_workspace_bytes(T, E, top_k, d, f), dev)
-    _same_device(dev, logits=logits, qweight_in=qweight_in, scales_in=scales_in,
-                 qzeros_in=qzeros_in, perm_in=perm_in, qweight_out=qweight_out,
-                 scales_out=scales_out, qzeros_out=qzeros_out, perm_out=perm_out, y=y, ws=ws)
-    _call("gptq_w4a16_moe", dev, _addr(x), T, _addr(logits), E, int(top_k), int(bool(renormalize)),
-          _addr(qweight_in), _addr(scales_in), _addr(qzeros_in), _addr(perm_in),
-          _addr(qweight_out), _addr(scales_out), _addr(qzeros_out), _addr(perm_out), d, f,
-          int(group_size), _addr(y), _addr(ws), ws.numel() * ws.element_size())
+    _packed_layer(qweight_in, scales_in, qzeros_in, perm_in, (E,), 2 * f, d, group_size, dev, "_in")
+    _packed_layer(qweight_out, scales_out, qzeros_out, perm_out, (E,), d, f, group_size, dev, "_out")
+    y = _out(y, "y", (T, d), torch.float32, x)
+    lib = _lib or load_library()
+    ws, nb = _workspace(ws, lib.gptq_w4a16_moe_workspace_bytes(T, E, top_k, d, f), x)
+    _call("gptq_w4a16_moe", dev, x.data_ptr(), T, logits.data_ptr(), E, top_k, bool(renormalize),
+          qweight_in.data_ptr(), scales_in.data_ptr(), qzeros_in.data_ptr(), _addr(perm_in),
+          qweight_out.data_ptr(), scales_out.data_ptr(), qzeros_out.data_ptr(), _addr(perm_out), d,
+          f, group_size, y.data_ptr(), ws.data_ptr(), nb)
     return y
 
 
@@ -713,26 +730,26 @@ class KV4Cache:
     elements in its words is that of gptq_kv4_append in include/gptq.h."""
 
     def __init__(self, k_codes, k_params, v_codes, v_params):
-        for t, name, dt in ((k_codes, "k_codes", torch.int32), (k_params, "k_params", torch.float16),
-                            (v_codes, "v_codes", torch.int32), (v_params, "v_params", torch.float16)):
-            _need(t, name, dt)
-        if k_codes.dim() != 4 or k_params.dim() != 5 or k_params.shape[4] != 2:
+        dev = _tensor(k_codes, "k_codes")
+        _on(k_codes, "k_codes", torch.int32, dev)
+        _on(k_params, "k_params", torch.float16, dev)
+        _on(v_codes, "v_codes", torch.int32, dev)
+        _on(v_params, "v_params", torch.float16, dev)
+        if k_codes.dim() != 4 or k_params.dim() != 5 or k_params.shape[4] != 2 or \
+                k_codes.shape[:3] != k_params.shape[:3]:
             raise ValueError("codes must be pages x kv_heads x page_size x head_dim / 8, params "
                              "pages x kv_heads x page_size x groups x 2")
-        if k_codes.shape[:3] != k_params.shape[:3]:
-            raise ValueError("codes and params must have the same pages, heads and page size")
         if v_codes.shape != k_codes.shape or v_params.shape != k_params.shape:
             raise ValueError("keys and values must have the same shapes")
         self.k_codes, self.k_params = k_codes, k_params
         self.v_codes, self.v_params = v_codes, v_params
-        self.pages, self.kv_heads, self.page_size = k_codes.shape[:3]
-        self.head_dim = k_codes.shape[3] * 8
+        self.pages, self.kv_heads, self.page_size, words = k_codes.shape
+        self.head_dim = words * 8
         groups = k_params.shape[3]
         if groups < 1 or self.head_dim % groups != 0:
             raise ValueError("the groups must divide head_dim")
         self.group_size = self.head_dim // groups
-        self.device = k_codes.device
-        _same_device(self.device, k_params=k_params, v_codes=v_codes, v_params=v_params)
+        self.index = dev                                   # of its device
 
     @classmethod
     def empty(cls, pages: int, kv_heads: int, page_size: int, head_dim: int,
@@ -746,18 +763,18 @@ class KV4Cache:
         return cls(codes(), params(), codes(), params())
 
 
-def _rows(t, name: str, tokens: int, heads, head_dim: int, dtype):
+def _rows(t, name: str, tokens: int, heads, head_dim: int, dtype, index: int):
     """A tokens x heads x head_dim tensor or view with dense rows: its token stride."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[0] != tokens or t.shape[2] != head_dim or \
-            (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} must be tokens x heads x head_dim, got {tuple(t.shape)}")
-    if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != head_dim)):
+    if t.dtype is not dtype or t.get_device() != index:
+        raise ValueError(f"{name} must be {dtype} on cuda:{index}, got {t.dtype} on {t.device}")
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != tokens or shape[2] != head_dim or \
+            (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name} must be tokens x heads x head_dim, got {tuple(shape)}")
+    s0, s1, s2 = t.stride()
+    if tokens and shape[1] and (s2 != 1 or (shape[1] > 1 and s1 != head_dim)):
         raise ValueError(f"{name}: the heads of a token must be dense")
-    return t.stride(0) if tokens > 1 else t.shape[1] * head_dim
+    return s0 if tokens > 1 else shape[1] * head_dim
 
 
 def gptq_kv4_append(k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
@@ -769,38 +786,44 @@ def gptq_kv4_append(k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
     the cache.  cos_sin: positions x rot_dim fp32 (cosines, then sines) or None.
     Returns (q_out fp16 or None, k_values, v_values): with values=True the fp16
     keys and values that the cache now holds, else None."""
-    dt = _wdtype(k)
+    dev = _tensor(k, "k")
+    if dev != cache.index:
+        raise ValueError(f"k must be on cuda:{cache.index}")
+    dtype = k.dtype
+    dt = GPTQ_DTYPE_F32 if dtype is torch.float32 else GPTQ_DTYPE_F16
+    if dtype is not torch.float32 and dtype is not torch.float16:
+        raise ValueError("k must be float16 or float32")
     if k.dim() != 3:
         raise ValueError("k must be tokens x kv_heads x head_dim")
-    T, D, dev = k.shape[0], cache.head_dim, k.device
-    ks = _rows(k, "k", T, cache.kv_heads, D, k.dtype)
-    vs = _rows(v, "v", T, cache.kv_heads, D, k.dtype)
+    T, hkv, D = k.shape[0], cache.kv_heads, cache.head_dim
+    ks = _rows(k, "k", T, hkv, D, dtype, dev)
+    vs = _rows(v, "v", T, hkv, D, dtype, dev)
     qs, hq = 0, 0
     if q is not None:
-        qs = _rows(q, "q", T, None, D, k.dtype)
+        qs = _rows(q, "q", T, None, D, dtype, dev)
         hq = q.shape[1]
-        q_out = _out(q_out, "q_out", (T, hq, D), torch.float16, dev)
+        q_out = _out(q_out, "q_out", (T, hq, D), torch.float16, k)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    _need(slots, "slots", torch.int64)
-    rot, n_pos = 0, 0
+    _on(slots, "slots", torch.int64, dev)
+    if slots.shape != (T,):
+        raise ValueError("slots must have one entry per token")
+    rot, n_pos, pos_ptr, table_ptr = 0, 0, None, None
     if cos_sin is not None:
-        _need(cos_sin, "cos_sin", torch.float32)
-        _need(positions, "positions", torch.int32)
+        _on(cos_sin, "cos_sin", torch.float32, dev)
+        _on(positions, "positions", torch.int32, dev)
         n_pos, rot = cos_sin.shape
         if positions.shape != (T,):
             raise ValueError("positions must have one entry per token")
-    if slots.shape != (T,):
-        raise ValueError("slots must have one entry per token")
-    kv = torch.empty(2, T, cache.kv_heads, D, dtype=torch.float16, device=dev) if values else None
-    kval, vval = (kv[0], kv[1]) if values else (None, None)
-    _same_device(dev, v=v, q=q, slots=slots, positions=positions, cos_sin=cos_sin,
-                 cache=cache.k_codes, q_out=q_out)
-    _call("gptq_kv4_append", dev, _addr(q), qs, _addr(k), ks, _addr(v), vs, dt, T, hq,
-          cache.kv_heads, D, _addr(positions), _addr(slots), _addr(cos_sin), n_pos, rot,
-          int(bool(interleaved)), cache.group_size, cache.pages, cache.page_size,
-          _addr(cache.k_codes), _addr(cache.k_params), _addr(cache.v_codes),
-          _addr(cache.v_params), _addr(q_out), _addr(kval), _addr(vval))
+        pos_ptr, table_ptr = positions.data_ptr(), cos_sin.data_ptr()
+    kval = vval = None
+    if values:
+        kval, vval = k.new_empty((2, T, hkv, D), dtype=torch.float16).unbind(0)
+    _call("gptq_kv4_append", dev, _addr(q), qs, k.data_ptr(), ks, v.data_ptr(), vs, dt, T, hq, hkv,
+          D, pos_ptr, slots.data_ptr(), table_ptr, n_pos, rot, bool(interleaved),
+          cache.group_size, cache.pages, cache.page_size, cache.k_codes.data_ptr(),
+          cache.k_params.data_ptr(), cache.v_codes.data_ptr(), cache.v_params.data_ptr(),
+          _addr(q_out), _addr(kval), _addr(vval))
     return q_out, kval, vval
 
 
@@ -820,30 +843,32 @@ def gptq_kv4_attention(q: torch.Tensor, cache: KV4Cache, block_table: torch.Tens
     max_q_len, max_seq_len (default: the table's width in keys) bound the
     queries and keys of a sequence.  Returns out (as q; rows behind the last
     sequence are not written)."""
-    _need(q, "q", torch.float16)
-    _need(block_table, "block_table", torch.int32)
-    _need(seq_lens, "seq_lens", torch.int32)
-    _need(q_start, "q_start", torch.int32)
-    if q.dim() != 3 or q.shape[2] != cache.head_dim:
+    dev = _tensor(q, "q")
+    if dev != cache.index:
+        raise ValueError(f"q must be on cuda:{cache.index}")
+    _on(q, "q", torch.float16, dev)
+    _on(block_table, "block_table", torch.int32, dev)
+    _on(seq_lens, "seq_lens", torch.int32, dev)
+    _on(q_start, "q_start", torch.int32, dev)
+    hkv, D = cache.kv_heads, cache.head_dim
+    if q.dim() != 3 or q.shape[2] != D:
         raise ValueError("q must be tokens x q_heads x head_dim")
-    T, hq, D = q.shape
+    T, hq = q.shape[0], q.shape[1]
     B = seq_lens.shape[0]
     if block_table.dim() != 2 or block_table.shape[0] != B or q_start.shape != (B + 1,):
         raise ValueError("block_table must be seqs x width, q_start seqs + 1")
     width = block_table.shape[1]
     if max_seq_len is None:
         max_seq_len = width * cache.page_size
-    dev = q.device
-    out = _out(out, "out", (T, hq, D), torch.float16, dev)
-    ws = _workspace(ws, gptq_kv4_attention_workspace_bytes(B, hq, cache.kv_heads, D, max_q_len,
-                                                           max_seq_len), dev)
-    _same_device(dev, cache=cache.k_codes, block_table=block_table, seq_lens=seq_lens,
-                 q_start=q_start, out=out, ws=ws)
-    _call("gptq_kv4_attention", dev, _addr(q), T, B, hq, cache.kv_heads, D, _addr(cache.k_codes),
-          _addr(cache.k_params), _addr(cache.v_codes), _addr(cache.v_params), cache.pages,
-          cache.page_size, cache.group_size, _addr(block_table), width, _addr(seq_lens),
-          _addr(q_start), float(scale), int(window), int(max_q_len), int(max_seq_len), _addr(out),
-          _addr(ws), ws.numel() * ws.element_size())
+    out = _out(out, "out", (T, hq, D), torch.float16, q)
+    lib = _lib or load_library()
+    ws, nb = _workspace(ws, lib.gptq_kv4_attention_workspace_bytes(B, hq, hkv, D, max_q_len,
+                                                                   max_seq_len), q)
+    _call("gptq_kv4_attention", dev, q.data_ptr(), T, B, hq, hkv, D, cache.k_codes.data_ptr(),
+          cache.k_params.data_ptr(), cache.v_codes.data_ptr(), cache.v_params.data_ptr(),
+          cache.pages, cache.page_size, cache.group_size, block_table.data_ptr(), width,
+          seq_lens.data_ptr(), q_start.data_ptr(), scale, window, max_q_len, max_seq_len,
+          out.data_ptr(), ws.data_ptr(), nb)
     return out
 
 
