@@ -15,6 +15,7 @@ namespace gptq {
 
 constexpr int LORA_KW = 8, LORA_ROWS = 32 * (W4_WARPS / LORA_KW);   // of w4_sweep
 constexpr int LORA_JOIN = 4;                     // rows of x per thread of the join
+constexpr int LORA_MAX_RANK = 256;
 
 struct LoraParams {
     const __half* x;
@@ -32,60 +33,55 @@ struct LoraParams {
     float* y;
 };
 
-// t[b][r] = scaling (A_a[r] . x[b]): one warp per (rank row, four rows of x), which
-// share a load of A where they have the same adapter
+// t[b][r] = scaling (A_a[r] . x[b]): one warp per (r, b), the warps of a CTA on
+// neighbouring rows b, which find a shared adapter's row in L1
 __device__ __forceinline__ void lora_shrink(const LoraParams& p)
 {
     const int lane = threadIdx.x & 31;
-    const int64_t items = ((p.batch + 3) / 4) * p.rank;
-    for (int64_t it = int64_t(blockIdx.x) + int64_t(threadIdx.x >> 5) * gridDim.x; it < items;
+    const int64_t items = p.batch * p.rank;
+    for (int64_t it = int64_t(blockIdx.x) * W4_WARPS + (threadIdx.x >> 5); it < items;
          it += int64_t(gridDim.x) * W4_WARPS) {
-        const int64_t b0 = it / p.rank * 4;
-        const int r = int(it % p.rank);
-        int id[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            id[i] = b0 + i < p.batch ? p.adapter[b0 + i] : -1;
-            if (id[i] < -1 || id[i] >= p.n) {
-                if (lane == 0) atomicCAS(&g_device_status, 0, kErrIndex);
-                id[i] = -1;
-            }
+        const int r = int(it / p.batch);
+        const int64_t b = it - r * p.batch;
+        int id = p.adapter[b];
+        if (id < -1 || id >= p.n) {
+            if (lane == 0) atomicCAS(&g_device_status, 0, kErrIndex);
+            id = -1;
         }
+        float s = 0.f;
+        if (id >= 0) {
+            const __half* a = p.a + (int64_t(id) * p.rank + r) * p.d + lane * 8;
+            const __half* x = p.x + b * p.d + lane * 8;
+            auto add = [&](uint4 av, uint4 xv) {
+                const __half2* ah = reinterpret_cast<const __half2*>(&av);
+                const __half2* xh = reinterpret_cast<const __half2*>(&xv);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (b0 + i >= p.batch) break;
-            bool first = true;                             // of the rows with this adapter
-#pragma unroll
-            for (int j = 0; j < i; ++j) first = first && (id[j] != id[i]);
-            if (!first) continue;
-            float s[4] = {0.f, 0.f, 0.f, 0.f};
-            if (id[i] >= 0) {
-                const __half* a = p.a + (int64_t(id[i]) * p.rank + r) * p.d;
-                for (int64_t k = lane * 8; k < p.d; k += 256) {
-                    const uint4 av = *reinterpret_cast<const uint4*>(a + k);
-                    const __half2* ah = reinterpret_cast<const __half2*>(&av);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        if (j < i || id[j] != id[i]) continue;
-                        const uint4 xv = *reinterpret_cast<const uint4*>(p.x + (b0 + j) * p.d + k);
-                        const __half2* xh = reinterpret_cast<const __half2*>(&xv);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float2 u = __half22float2(ah[e]), v = __half22float2(xh[e]);
-                            s[j] = fmaf(u.x, v.x, s[j]);
-                            s[j] = fmaf(u.y, v.y, s[j]);
-                        }
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    const float2 u = __half22float2(ah[e]), v = __half22float2(xh[e]);
+                    s = fmaf(u.x, v.x, s);
+                    s = fmaf(u.y, v.y, s);
                 }
-            }
-            const float c = id[i] >= 0 ? p.scaling[id[i]] : 0.f;
+            };
+            const int n = int(p.d / 256);                  // rounds of the warp, eight in flight
+            int k = 0;
+            for (; k + 8 <= n; k += 8) {
+                uint4 av[8], xv[8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (j < i || id[j] != id[i] || b0 + j >= p.batch) continue;
-                for (int o = 16; o; o >>= 1) s[j] += __shfl_xor_sync(0xffffffffu, s[j], o);
-                if (lane == 0) p.t[(b0 + j) * p.rank + r] = s[j] * c;
+                for (int u = 0; u < 8; ++u) {
+                    av[u] = __ldg(reinterpret_cast<const uint4*>(a + (k + u) * 256));
+                    xv[u] = __ldg(reinterpret_cast<const uint4*>(x + (k + u) * 256));
+                }
+#pragma unroll
+                for (int u = 0; u < 8; ++u) add(av[u], xv[u]);
             }
+            for (; k * 256 + lane * 8 < p.d; ++k)
+                add(__ldg(reinterpret_cast<const uint4*>(a + k * 256)),
+                    __ldg(reinterpret_cast<const uint4*>(x + k * 256)));
+            s *= p.scaling[id];
         }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (lane == 0) p.t[b * p.rank + r] = s;
     }
 }
 
@@ -134,34 +130,49 @@ lora_product_kernel(const __grid_constant__ CUtensorMap tm, const LoraParams p)
     if (!shrunk) lora_shrink(p);
 }
 
-// y[b][r] = sum of part over the slices + B_a[r] . t[b]
+// y[b][r] = sum of part over the slices + B_a[r] . t[b]; one row r and LORA_JOIN rows
+// of x per thread
 __global__ void __launch_bounds__(256) lora_join_kernel(const LoraParams p)
 {
+    __shared__ float4 ts[LORA_JOIN][LORA_MAX_RANK / 4];
     const int64_t r = int64_t(blockIdx.x) * 256 + threadIdx.x;
     const int64_t b0 = int64_t(blockIdx.y) * LORA_JOIN;
+    const int rows = int(min(int64_t(LORA_JOIN), p.batch - b0));
     int id[LORA_JOIN];
 #pragma unroll
     for (int i = 0; i < LORA_JOIN; ++i) {
-        id[i] = b0 + i < p.batch ? p.adapter[b0 + i] : -1;
+        id[i] = i < rows ? p.adapter[b0 + i] : -1;
         if (id[i] >= p.n) id[i] = -1;
     }
     pdl_wait();
+    for (int i = threadIdx.x; i < rows * (p.rank / 4); i += 256)
+        ts[i / (p.rank / 4)][i % (p.rank / 4)] =
+            *reinterpret_cast<const float4*>(p.t + b0 * p.rank + int64_t(i) * 4);
+    __syncthreads();
     if (r >= p.m) return;
     float y[LORA_JOIN] = {};
+    {
+        const float* src = p.part + b0 * p.m + r;
+        const int64_t slice = p.batch * p.m;
+#pragma unroll 4
+        for (int s = 0; s < p.slices; ++s, src += slice)
 #pragma unroll
-    for (int i = 0; i < LORA_JOIN; ++i)
-        if (b0 + i < p.batch)
-            for (int s = 0; s < p.slices; ++s) y[i] += p.part[(int64_t(s) * p.batch + b0 + i) * p.m + r];
+            for (int i = 0; i < LORA_JOIN; ++i)
+                if (i < rows) y[i] += src[i * p.m];
+    }
+#pragma unroll 2
     for (int k = 0; k < p.rank; k += 8) {
-        uint4 bv = make_uint4(0u, 0u, 0u, 0u);
+        uint4 bv[LORA_JOIN];
+#pragma unroll
+        for (int i = 0; i < LORA_JOIN; ++i)
+            bv[i] = id[i] < 0 ? make_uint4(0u, 0u, 0u, 0u)
+                              : __ldg(reinterpret_cast<const uint4*>(
+                                    p.b + (int64_t(id[i]) * p.m + r) * p.rank + k));
 #pragma unroll
         for (int i = 0; i < LORA_JOIN; ++i) {
             if (id[i] < 0) continue;
-            if (i == 0 || id[i] != id[i - 1])              // neighbours share the load
-                bv = *reinterpret_cast<const uint4*>(p.b + (int64_t(id[i]) * p.m + r) * p.rank + k);
-            const float4 t0 = *reinterpret_cast<const float4*>(p.t + (b0 + i) * p.rank + k);
-            const float4 t1 = *reinterpret_cast<const float4*>(p.t + (b0 + i) * p.rank + k + 4);
-            const __half2* h = reinterpret_cast<const __half2*>(&bv);
+            const float4 t0 = ts[i][k / 4], t1 = ts[i][k / 4 + 1];
+            const __half2* h = reinterpret_cast<const __half2*>(&bv[i]);
             const float2 v0 = __half22float2(h[0]), v1 = __half22float2(h[1]);
             const float2 v2 = __half22float2(h[2]), v3 = __half22float2(h[3]);
             y[i] = fmaf(v0.x, t0.x, y[i]); y[i] = fmaf(v0.y, t0.y, y[i]);
@@ -172,7 +183,7 @@ __global__ void __launch_bounds__(256) lora_join_kernel(const LoraParams p)
     }
 #pragma unroll
     for (int i = 0; i < LORA_JOIN; ++i)
-        if (b0 + i < p.batch) p.y[(b0 + i) * p.m + r] = y[i];
+        if (i < rows) p.y[(b0 + i) * p.m + r] = y[i];
 }
 
 struct LoraPlan {
