@@ -429,11 +429,11 @@ int gptq_w4a16_matmul(const uint16_t* x, int64_t batch, const uint32_t* qweight,
  *    adjacent; adjacent rows share the adapter's loads.
  * rank: a multiple of 8, 8 .. 256.  0 <= batch <= 65535 (0: no-op);
  *    0 <= n_adapters <= 65536 (0: lora_* may be NULL).
- * ws: gptq_w4a16_lora_workspace_bytes(batch, d_out, d_in, rank) bytes, not
- *    shared with a call that may run at the same time.
+ * ws: gptq_w4a16_lora_workspace_bytes(...) bytes, not shared with a call that may run at the same time.
  * All sums are fp32; the result does not depend on timing (no atomics on y).
  */
-size_t gptq_w4a16_lora_workspace_bytes(int64_t batch, int64_t d_out, int64_t d_in, int rank);
+size_t gptq_w4a16_lora_workspace_bytes(int64_t batch, int64_t d_out, int64_t d_in,
+                                       int group_size, int rank);
 int gptq_w4a16_lora(const uint16_t* x, int64_t batch, const uint32_t* qweight,
                     const uint16_t* scales, const uint8_t* qzeros, const int32_t* perm,
                     int64_t d_out, int64_t d_in, int group_size, const uint16_t* lora_a,

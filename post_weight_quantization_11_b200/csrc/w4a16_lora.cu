@@ -3,19 +3,24 @@
 //
 //   y[b] = x[b] Q^T + scaling[a] (x[b] A_a^T) B_a^T,   a = adapter[b]
 //
-// Two kernels.  The first sweeps the packed rows (w4_rows.cuh) for chunks of up to
+// Up to LORA_SWEEP rows of x two kernels: the first sweeps the packed rows (w4_rows.cuh) for chunks of up to
 // 16 rows of x and slices of the columns, and computes t[b] = scaling A_a x[b]
-// beside it; the second joins the slices and adds B_a t.  Partial results go
-// through memory, not atomics: their order is fixed.
+// beside it; the second joins the slices and adds B_a t.  Beyond, the product is
+// the tcgen05 kernel's (w4a16_tc.cu), with t computed where the activations are put
+// in its order.  Partial results go through memory, not atomics: their order is
+// fixed.
 #include "common.cuh"
 #include "tc_common.cuh"
 #include "w4_rows.cuh"
+#include "w4a16_tc.cuh"
 
 namespace gptq {
 
 constexpr int LORA_KW = 8, LORA_ROWS = 32 * (W4_WARPS / LORA_KW);   // of w4_sweep
-constexpr int LORA_JOIN = 4;                     // rows of x per thread of the join
+constexpr int LORA_JOIN = 2, LORA_JOIN_THREADS = 128;   // rows of x per thread of the join
+constexpr int LORA_SWEEP = 16;                   // most rows of x of the row sweep
 constexpr int LORA_MAX_RANK = 256;
+constexpr int LORA_SMS = 148;                    // the plan does not depend on the device that is current
 
 struct LoraParams {
     const __half* x;
@@ -29,18 +34,19 @@ struct LoraParams {
     W4Layer lay;
     int chunk, chunks, slice, slices, groups;
     float* t;          // batch x rank
+    __half* xp;        // batch x d, reordered for the tcgen05 product
     float* part;       // slices x batch x m
     float* y;
 };
 
 // t[b][r] = scaling (A_a[r] . x[b]): one warp per (r, b), the warps of a CTA on
 // neighbouring rows b, which find a shared adapter's row in L1
-__device__ __forceinline__ void lora_shrink(const LoraParams& p)
+__device__ __forceinline__ void lora_shrink(const LoraParams& p, int warps)
 {
     const int lane = threadIdx.x & 31;
     const int64_t items = p.batch * p.rank;
-    for (int64_t it = int64_t(blockIdx.x) * W4_WARPS + (threadIdx.x >> 5); it < items;
-         it += int64_t(gridDim.x) * W4_WARPS) {
+    for (int64_t it = int64_t(blockIdx.x) * warps + (threadIdx.x >> 5); it < items;
+         it += int64_t(gridDim.x) * warps) {
         const int r = int(it / p.batch);
         const int64_t b = it - r * p.batch;
         int id = p.adapter[b];
@@ -117,7 +123,7 @@ lora_product_kernel(const __grid_constant__ CUtensorMap tm, const LoraParams p)
             [&]() {
                 w4_stage_half<NT, WIDE>(x, xs, [&](int n) { return p.x + (b0 + n) * p.d; }, p.perm,
                                         k0 * W4_STEP, steps, cols, int(p.d));
-                if (!shrunk) lora_shrink(p);               // beside the first copies
+                if (!shrunk) lora_shrink(p, W4_WARPS);               // beside the first copies
                 shrunk = true;
                 __syncthreads();
             },
@@ -127,15 +133,24 @@ lora_product_kernel(const __grid_constant__ CUtensorMap tm, const LoraParams p)
             });
         u += g1 - g0;
     }
-    if (!shrunk) lora_shrink(p);
+    if (!shrunk) lora_shrink(p, W4_WARPS);
+}
+
+// t, and the activations in the order of the tcgen05 product
+__global__ void __launch_bounds__(256) lora_front_kernel(const LoraParams p)
+{
+    lora_shrink(p, 8);
+    const int64_t total = p.batch * p.d;
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < total; i += int64_t(gridDim.x) * 256)
+        p.xp[i] = wq_gathered(p.x, p.perm, i, p.d);
 }
 
 // y[b][r] = sum of part over the slices + B_a[r] . t[b]; one row r and LORA_JOIN rows
 // of x per thread
-__global__ void __launch_bounds__(256) lora_join_kernel(const LoraParams p)
+__global__ void __launch_bounds__(LORA_JOIN_THREADS) lora_join_kernel(const LoraParams p)
 {
     __shared__ float4 ts[LORA_JOIN][LORA_MAX_RANK / 4];
-    const int64_t r = int64_t(blockIdx.x) * 256 + threadIdx.x;
+    const int64_t r = int64_t(blockIdx.x) * LORA_JOIN_THREADS + threadIdx.x;
     const int64_t b0 = int64_t(blockIdx.y) * LORA_JOIN;
     const int rows = int(min(int64_t(LORA_JOIN), p.batch - b0));
     int id[LORA_JOIN];
@@ -145,7 +160,7 @@ __global__ void __launch_bounds__(256) lora_join_kernel(const LoraParams p)
         if (id[i] >= p.n) id[i] = -1;
     }
     pdl_wait();
-    for (int i = threadIdx.x; i < rows * (p.rank / 4); i += 256)
+    for (int i = threadIdx.x; i < rows * (p.rank / 4); i += LORA_JOIN_THREADS)
         ts[i / (p.rank / 4)][i % (p.rank / 4)] =
             *reinterpret_cast<const float4*>(p.t + b0 * p.rank + int64_t(i) * 4);
     __syncthreads();
@@ -187,17 +202,32 @@ __global__ void __launch_bounds__(256) lora_join_kernel(const LoraParams p)
 }
 
 struct LoraPlan {
+    bool tc;                                     // the tcgen05 product
+    WqPlan wq;
     int nt, chunk, chunks, slice, slices, groups;
-    size_t at_part, bytes;
+    size_t at_xp, at_part, bytes;
 };
 
 // Rows of x that are staged together (one operand of 8, or two) and slices of the
 // columns: as few as fit beside the ring, or more where few row groups would leave
 // CTAs idle.  A group costs about 190 instructions a step and warp (two operands:
 // 260, bound by the matrix pipe) and 150 to join, and the slowest CTA counts.
-LoraPlan lora_plan(int64_t T, int64_t m, int64_t d, int rank)
+// More than 16 rows: the tcgen05 product, which needs groups of a multiple of 64 (14336
+// x 4096, groups of 128: 31 us against 43 at 16 rows, 56 against 44 at 32, 180 against
+// 75 at 128).
+LoraPlan lora_plan(int64_t T, int64_t m, int64_t d, int64_t g, int rank)
 {
     LoraPlan p{};
+    p.at_xp = align_up(size_t(T) * rank * 4, 256);
+    p.tc = T > LORA_SWEEP && g % 64 == 0;
+    if (p.tc) {
+        p.wq = wq_plan(T, m, d, g, LORA_SMS);
+        p.slices = p.wq.ksplit;
+        p.at_part = p.at_xp + align_up(size_t(T) * d * 2, 1024);
+        p.bytes = p.at_part + (p.slices > 1 ? align_up(size_t(p.slices) * T * m * 4, 256) : 0);
+        return p;
+    }
+    p.at_part = p.at_xp;
     p.nt = T > W4_COLS ? 2 : 1;
     p.chunk = int(std::min<int64_t>(T, W4_COLS * p.nt));
     p.chunks = int((T + p.chunk - 1) / p.chunk);
@@ -207,25 +237,27 @@ LoraPlan lora_plan(int64_t T, int64_t m, int64_t d, int rank)
     double best = 1e300;
     for (int s = (so + most - 1) / most; s <= std::min(so, 64); ++s) {
         const int steps = (so + s - 1) / s;
-        const int64_t rounds = ((int64_t(p.chunks) * s * p.groups) + 147) / 148;
+        const int64_t rounds = ((int64_t(p.chunks) * s * p.groups) + LORA_SMS - 1) / LORA_SMS;
         const double cost = double(rounds) * (((steps + LORA_KW - 1) / LORA_KW) * (p.nt == 1 ? 190 : 260) + 150);
         if (cost < best * 0.97) { best = cost; p.slice = steps; }
     }
     p.slices = (so + p.slice - 1) / p.slice;
-    p.at_part = align_up(size_t(T) * rank * 4, 256);
-    p.bytes = p.at_part + align_up(size_t(p.slices) * T * m * 4, 256);
+    p.bytes = p.at_part + (p.slices > 1 ? align_up(size_t(p.slices) * T * m * 4, 256) : 0);
     return p;
 }
 
 }  // namespace gptq
 
 extern "C" size_t gptq_w4a16_lora_workspace_bytes(int64_t batch, int64_t d_out, int64_t d_in,
-                                                  int rank)
+                                                  int group_size, int rank)
 {
-    if (batch <= 0 || d_out <= 0 || d_in <= 0 || rank <= 0) return 0;
-    if (batch > 65535 || d_out > gptq::kMaxRows || d_in > gptq::kMaxDim || d_in % 128 != 0 || rank > 256)
+    using namespace gptq;
+    const int64_t g = group_size == -1 ? d_in : group_size;
+    if (batch <= 0 || batch > 65535 || d_out <= 0 || d_out > kMaxRows || d_in <= 0 ||
+        d_in > kMaxDim || d_in % 128 != 0 || g < 32 || g % 32 != 0 || d_in % g != 0 || rank <= 0 ||
+        rank > LORA_MAX_RANK)
         return 0;
-    return gptq::lora_plan(batch, d_out, d_in, rank).bytes;
+    return lora_plan(batch, d_out, d_in, g, rank).bytes;
 }
 
 extern "C" int gptq_w4a16_lora(const uint16_t* x, int64_t batch, const uint32_t* qweight,
@@ -241,7 +273,7 @@ extern "C" int gptq_w4a16_lora(const uint16_t* x, int64_t batch, const uint32_t*
         return GPTQ_ERR_SHAPE;
     const int64_t g = (group_size == -1) ? d_in : group_size;
     if (g < 32 || g % 32 != 0 || d_in % g != 0) return GPTQ_ERR_UNSUPPORTED;
-    if (rank < 8 || rank > 256 || rank % 8 != 0) return GPTQ_ERR_UNSUPPORTED;
+    if (rank < 8 || rank > LORA_MAX_RANK || rank % 8 != 0) return GPTQ_ERR_UNSUPPORTED;
     if (batch == 0) return GPTQ_OK;
     if (!x || !qweight || !scales || !qzeros || !y || !ws || !adapter ||
         (n_adapters > 0 && (!lora_a || !lora_b || !lora_scaling)))
@@ -250,9 +282,8 @@ extern "C" int gptq_w4a16_lora(const uint16_t* x, int64_t batch, const uint32_t*
         !aligned16(y) || !aligned16(ws) || !aligned16(perm) || !aligned16(lora_a) ||
         !aligned16(lora_b) || !aligned(lora_scaling, 4) || !aligned(adapter, 4))
         return GPTQ_ERR_INVALID_ARG;
-    if (ws_bytes < gptq_w4a16_lora_workspace_bytes(batch, d_out, d_in, rank))
-        return GPTQ_ERR_INVALID_ARG;
-    const LoraPlan plan = lora_plan(batch, d_out, d_in, rank);
+    const LoraPlan plan = lora_plan(batch, d_out, d_in, g, rank);
+    if (ws_bytes < plan.bytes) return GPTQ_ERR_INVALID_ARG;
     LoraParams p{};
     p.x = reinterpret_cast<const __half*>(x);
     p.perm = perm;
@@ -264,27 +295,43 @@ extern "C" int gptq_w4a16_lora(const uint16_t* x, int64_t batch, const uint32_t*
     p.chunk = plan.chunk; p.chunks = plan.chunks; p.slice = plan.slice; p.slices = plan.slices;
     p.groups = plan.groups;
     p.t = static_cast<float*>(ws);
-    p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + plan.at_part);
+    p.xp = reinterpret_cast<__half*>(static_cast<uint8_t*>(ws) + plan.at_xp);
+    // one slice: in y, where the join finds it (each thread reads and writes its own elements)
+    p.part = plan.slices > 1
+                 ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + plan.at_part) : y;
     p.y = y;
     cudaStream_t st = as_stream(stream);
     KernelTimer kt(kKLora, st);
-    CUtensorMap tm;
-    if (w4_tmap(&tm, qweight, d_out, d_in, 32) != GPTQ_OK) return GPTQ_ERR_CUDA;
-    const bool wide = g % W4_STEP == 0;
-    const size_t smem = w4_smem(plan.slice, plan.chunk, plan.nt, wide, false);
-    auto kern = plan.nt == 1 ? (wide ? lora_product_kernel<1, true> : lora_product_kernel<1, false>)
-                             : (wide ? lora_product_kernel<2, true> : lora_product_kernel<2, false>);
-    static std::atomic<bool> done[4][64];
-    if (smem > W4_MAX_SMEM) return GPTQ_ERR_SHAPE;
-    if (!smem_opt_in(reinterpret_cast<const void*>(kern), W4_MAX_SMEM,
-                     done[(plan.nt - 1) * 2 + (wide ? 1 : 0)]))
+    if (plan.tc) {
+        lora_front_kernel<<<(unsigned)(device_sm_count() * 8), 256, 0, st>>>(p);
+        count_launches();
+        if (launch_status() != GPTQ_OK) return GPTQ_ERR_CUDA;
+        const int rc = wq_run(plan.wq, p.xp, batch, qweight, p.lay.sc, qzeros, d_out, d_in, g, p.part,
+                              batch * d_out, st);
+        if (rc != GPTQ_OK) return rc;
+    } else {
+        CUtensorMap tm;
+        if (w4_tmap(&tm, qweight, d_out, d_in, 32) != GPTQ_OK) return GPTQ_ERR_CUDA;
+        const bool wide = g % W4_STEP == 0;
+        const size_t smem = w4_smem(plan.slice, plan.chunk, plan.nt, wide, false);
+        if (smem > W4_MAX_SMEM) return GPTQ_ERR_SHAPE;
+        auto kern = plan.nt == 1
+                        ? (wide ? lora_product_kernel<1, true> : lora_product_kernel<1, false>)
+                        : (wide ? lora_product_kernel<2, true> : lora_product_kernel<2, false>);
+        static std::atomic<bool> done[4][64];
+        if (!smem_opt_in(reinterpret_cast<const void*>(kern), W4_MAX_SMEM,
+                         done[(plan.nt - 1) * 2 + (wide ? 1 : 0)]))
+            return GPTQ_ERR_CUDA;
+        const int64_t units = int64_t(plan.chunks) * plan.slices * plan.groups;
+        kern<<<(unsigned)std::min<int64_t>(device_sm_count(), units), W4_THREADS, smem, st>>>(tm, p);
+        count_launches();
+        if (launch_status() != GPTQ_OK) return GPTQ_ERR_CUDA;
+    }
+    if (launch_after(lora_join_kernel,
+                     dim3((unsigned)ceil_div(d_out, LORA_JOIN_THREADS),
+                          (unsigned)ceil_div(batch, LORA_JOIN)),
+                     LORA_JOIN_THREADS, 0, st, p) != cudaSuccess)
         return GPTQ_ERR_CUDA;
-    const int64_t units = int64_t(plan.chunks) * plan.slices * plan.groups;
-    kern<<<(unsigned)std::min<int64_t>(device_sm_count(), units), W4_THREADS, smem, st>>>(tm, p);
-    if (launch_status() != GPTQ_OK ||
-        launch_after(lora_join_kernel, dim3((unsigned)ceil_div(d_out, 256), (unsigned)ceil_div(batch, LORA_JOIN)),
-                     256, 0, st, p) != cudaSuccess)
-        return GPTQ_ERR_CUDA;
-    count_launches(2);
+    count_launches();
     return launch_status();
 }

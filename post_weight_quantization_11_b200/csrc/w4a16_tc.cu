@@ -30,6 +30,7 @@
 // accumulates at most 512 products).  Every mbarrier wait is bounded.
 #include "common.cuh"
 #include "tc_common.cuh"
+#include "w4a16_tc.cuh"
 
 namespace gptq {
 
@@ -65,15 +66,17 @@ struct WqParams {
     int chunks_per_split;
     int items;
     int atomic;         // ksplit > 1: y += (zeroed first)
+    int64_t split_stride;   // or, not atomic: elements between the splits' own outputs
 };
 
-struct WqItem { int rt, nt, c0, c1; };     // chunk range [c0, c1)
+struct WqItem { int rt, nt, ks, c0, c1; }; // chunk range [c0, c1)
 
 __device__ __forceinline__ WqItem wq_item(const WqParams& p, int q)
 {
     WqItem it;
     const int per = p.n_rt * p.n_nt;
     const int ks = q / per, rem = q - ks * per;
+    it.ks = ks;
     it.nt = rem / p.n_rt;
     it.rt = rem - it.nt * p.n_rt;
     const int nch = (int)(p.d / p.chunk);
@@ -297,12 +300,13 @@ w4a16_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             }
             if (!ok || !live) continue;
             const int64_t b0 = int64_t(it.nt) * p.ntile;
+            float* y = p.y + it.ks * p.split_stride;
 #pragma unroll
             for (int u = 0; u < NMAX; ++u) {
                 const int64_t b = b0 + u;
                 if (u < p.ntile && b < p.batch) {
-                    if (p.atomic) atomicAdd(p.y + b * p.m + row, sum[u]);
-                    else p.y[b * p.m + row] = sum[u];
+                    if (p.atomic) atomicAdd(y + b * p.m + row, sum[u]);
+                    else y[b * p.m + row] = sum[u];
                 }
             }
         }
@@ -324,18 +328,86 @@ __global__ void gather_cols_kernel(const __half* __restrict__ x, const int32_t* 
 {
     const int64_t total = batch * d;
     for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
-         i += int64_t(gridDim.x) * blockDim.x) {
-        const int64_t b = i / d, k = i - b * d;
-        const int e = int(k & 7);
-        const int64_t ks = (k & ~int64_t(7)) + ((e & 1) ? 4 + (e >> 1) : (e >> 1));
-        const int32_t pk = perm ? perm[ks] : int32_t(ks);
-        if (pk >= 0 && pk < d) {
-            xp[i] = x[b * d + pk];
-        } else {                                   // not followed: zero and record
-            xp[i] = __ushort_as_half(0);
-            atomicCAS(&g_device_status, 0, kErrIndex);
+         i += int64_t(gridDim.x) * blockDim.x)
+        xp[i] = wq_gathered(x, perm, i, d);
+}
+
+WqPlan wq_plan(int64_t batch, int64_t m, int64_t d, int64_t gsz, int sms)
+{
+    WqPlan p{};
+    p.small = ceil_div(batch, 16) * 16 <= 32;                   // the decode shape
+    p.ntile = (int)std::min<int64_t>(p.small ? 32 : WQ_NBIG, ceil_div(batch, 16) * 16);
+    p.n_rt = (int)ceil_div(m, WQ_M);
+    p.n_nt = (int)ceil_div(batch, p.ntile);
+    // accumulation chunk: the largest multiple of 64 columns, at most 512,
+    // that divides the group (a chunk never spans two groups)
+    p.chunk = WQ_K;
+    for (int64_t c = WQ_K; c <= std::min<int64_t>(gsz, WQ_CH); c += WQ_K)
+        if (gsz % c == 0) p.chunk = (int)c;
+    const int nch = (int)(d / p.chunk);
+    const int64_t tiles = int64_t(p.n_rt) * p.n_nt;
+    // split K (in whole chunks) when the tiles alone leave SMs idle: the
+    // split count that minimizes rounds x chunks per item, i.e. the longest
+    // CTA's share, among 1 .. nch (fewer splits on ties: fewer atomics)
+    int ks = 1;
+    if (tiles < 2 * sms) {
+        double best = 1e300;
+        for (int k = 1; k <= nch; ++k) {
+            const int64_t cps = ceil_div(nch, k);
+            const int64_t kk = ceil_div(nch, cps);
+            const double cost = double(ceil_div(tiles * kk, sms)) * double(cps + 1);
+            if (cost < best - 1e-9) { best = cost; ks = (int)kk; }
         }
     }
+    p.chunks_per_split = (int)ceil_div(nch, ks);
+    p.ksplit = (int)ceil_div(nch, p.chunks_per_split);
+    return p;
+}
+
+int wq_run(const WqPlan& plan, const __half* xp, int64_t batch, const uint32_t* qweight,
+           const __half* scales, const uint8_t* qzeros, int64_t m, int64_t d, int64_t gsz, float* y,
+           int64_t split_stride, cudaStream_t st)
+{
+    WqParams p{};
+    p.y = y;
+    p.scales = scales;
+    p.qzeros = qzeros;
+    p.m = m;
+    p.d = d;
+    p.gsz = gsz;
+    p.batch = batch;
+    p.ntile = plan.ntile;
+    p.n_rt = plan.n_rt;
+    p.n_nt = plan.n_nt;
+    p.chunk = plan.chunk;
+    p.chunks_per_split = plan.chunks_per_split;
+    p.ksplit = plan.ksplit;
+    p.items = plan.n_rt * plan.n_nt * plan.ksplit;
+    p.split_stride = split_stride;
+    p.atomic = split_stride == 0 && p.ksplit > 1;
+    if (p.atomic &&
+        cudaMemsetAsync(y, 0, sizeof(float) * size_t(batch) * size_t(m), st) != cudaSuccess)
+        return GPTQ_ERR_CUDA;
+    CUtensorMap tq, tx;
+    if (encode_tmap_2d(&tq, CU_TENSOR_MAP_DATA_TYPE_UINT32, qweight, (uint64_t)(d / 8),
+                       (uint64_t)m, (uint64_t)(d / 8) * 4, WQ_K / 8, WQ_M,
+                       CU_TENSOR_MAP_SWIZZLE_NONE) != GPTQ_OK ||
+        encode_tmap_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, xp, (uint64_t)d, (uint64_t)batch,
+                       (uint64_t)d * 2, WQ_K, (uint32_t)p.ntile,
+                       CU_TENSOR_MAP_SWIZZLE_128B) != GPTQ_OK)
+        return GPTQ_ERR_CUDA;
+    const int grid = std::min(p.items, device_sm_count());
+    auto run = [&](auto kern, int threads, int smem) -> int {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+            cudaSuccess)
+            return GPTQ_ERR_CUDA;
+        kern<<<grid, threads, smem, st>>>(tq, tx, p);
+        count_launches();
+        return launch_status();
+    };
+    return plan.small ? run(w4a16_tc_kernel<32>, WqCfg<32>::THREADS, WqCfg<32>::SMEM)
+                      : run(w4a16_tc_kernel<WQ_NBIG>, WqCfg<WQ_NBIG>::THREADS,
+                            WqCfg<WQ_NBIG>::SMEM);
 }
 
 }  // namespace gptq
@@ -373,63 +445,6 @@ extern "C" int gptq_w4a16_matmul(const uint16_t* x, int64_t batch, const uint32_
                                            xp);
         count_launches();
     }
-    const bool small = ceil_div(batch, 16) * 16 <= 32;          // the decode shape
-    WqParams p{};
-    p.y = y;
-    p.scales = reinterpret_cast<const __half*>(scales);
-    p.qzeros = qzeros;
-    p.m = d_out;
-    p.d = d_in;
-    p.gsz = gsz;
-    p.batch = batch;
-    p.ntile = (int)std::min<int64_t>(small ? 32 : WQ_NBIG, ceil_div(batch, 16) * 16);
-    p.n_rt = (int)ceil_div(d_out, WQ_M);
-    p.n_nt = (int)ceil_div(batch, p.ntile);
-    // accumulation chunk: the largest multiple of 64 columns, at most 512,
-    // that divides the group (a chunk never spans two groups)
-    p.chunk = WQ_K;
-    for (int64_t c = WQ_K; c <= std::min<int64_t>(gsz, WQ_CH); c += WQ_K)
-        if (gsz % c == 0) p.chunk = (int)c;
-    const int nch = (int)(d_in / p.chunk);
-    const int sms = device_sm_count();
-    const int64_t tiles = int64_t(p.n_rt) * p.n_nt;
-    // split K (in whole chunks) when the tiles alone leave SMs idle: the
-    // split count that minimizes rounds x chunks per item, i.e. the longest
-    // CTA's share, among 1 .. nch (fewer splits on ties: fewer atomics)
-    int ks = 1;
-    if (tiles < 2 * sms) {
-        double best = 1e300;
-        for (int k = 1; k <= nch; ++k) {
-            const int64_t cps = ceil_div(nch, k);
-            const int64_t kk = ceil_div(nch, cps);
-            const double cost = double(ceil_div(tiles * kk, sms)) * double(cps + 1);
-            if (cost < best - 1e-9) { best = cost; ks = (int)kk; }
-        }
-    }
-    p.chunks_per_split = (int)ceil_div(nch, ks);
-    p.ksplit = (int)ceil_div(nch, p.chunks_per_split);
-    p.items = (int)(tiles * p.ksplit);
-    p.atomic = p.ksplit > 1;
-    if (p.atomic &&
-        cudaMemsetAsync(y, 0, sizeof(float) * size_t(batch) * size_t(d_out), st) != cudaSuccess)
-        return GPTQ_ERR_CUDA;
-    CUtensorMap tq, tx;
-    if (encode_tmap_2d(&tq, CU_TENSOR_MAP_DATA_TYPE_UINT32, qweight, (uint64_t)(d_in / 8),
-                       (uint64_t)d_out, (uint64_t)(d_in / 8) * 4, WQ_K / 8, WQ_M,
-                       CU_TENSOR_MAP_SWIZZLE_NONE) != GPTQ_OK ||
-        encode_tmap_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, xp, (uint64_t)d_in, (uint64_t)batch,
-                       (uint64_t)d_in * 2, WQ_K, (uint32_t)p.ntile,
-                       CU_TENSOR_MAP_SWIZZLE_128B) != GPTQ_OK)
-        return GPTQ_ERR_CUDA;
-    const int grid = std::min(p.items, sms);
-    auto run = [&](auto kern, int threads, int smem) -> int {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-            cudaSuccess)
-            return GPTQ_ERR_CUDA;
-        kern<<<grid, threads, smem, st>>>(tq, tx, p);
-        count_launches();
-        return launch_status();
-    };
-    return small ? run(w4a16_tc_kernel<32>, WqCfg<32>::THREADS, WqCfg<32>::SMEM)
-                 : run(w4a16_tc_kernel<WQ_NBIG>, WqCfg<WQ_NBIG>::THREADS, WqCfg<WQ_NBIG>::SMEM);
+    return wq_run(wq_plan(batch, d_out, d_in, gsz, device_sm_count()), xp, batch, qweight,
+                  reinterpret_cast<const __half*>(scales), qzeros, d_out, d_in, gsz, y, 0, st);
 }

@@ -98,7 +98,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "gptq_w4a16_gemm": ([P, I64, P, P, P, P, I64, I64, I32, P, P], I32),
         "gptq_w4a16_matmul_workspace_bytes": ([I64, I64], SZ),
         "gptq_w4a16_matmul": ([P, I64, P, P, P, P, I64, I64, I32, P, P, SZ, P], I32),
-        "gptq_w4a16_lora_workspace_bytes": ([I64, I64, I64, I32], SZ),
+        "gptq_w4a16_lora_workspace_bytes": ([I64, I64, I64, I32, I32], SZ),
         "gptq_w4a16_lora": ([P, I64, P, P, P, P, I64, I64, I32, P, P, P, P, I64, I32, P, P, SZ, P],
                             I32),
         "gptq_w4a16_moe_workspace_bytes": ([I64, I64, I32, I64, I64], SZ),
@@ -650,9 +650,10 @@ def _packed_layer(qweight, scales, qzeros, perm, lead, m, d, group_size, index, 
             raise ValueError(f"perm{tag} must be {(*lead, d)}, got {tuple(perm.shape)}")
 
 
-def gptq_w4a16_lora_workspace_bytes(batch: int, d_out: int, d_in: int, rank: int) -> int:
+def gptq_w4a16_lora_workspace_bytes(batch: int, d_out: int, d_in: int, group_size: int,
+                                    rank: int) -> int:
     return int(load_library().gptq_w4a16_lora_workspace_bytes(int(batch), int(d_out), int(d_in),
-                                                              int(rank)))
+                                                              int(group_size), int(rank)))
 
 
 def gptq_w4a16_lora(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor,
@@ -679,7 +680,7 @@ def gptq_w4a16_lora(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor
         raise ValueError("adapter must have one entry per row of x, lora_scaling one per adapter")
     y = _out(y, "y", (b, m), torch.float32, x)
     lib = _lib or load_library()
-    ws, nb = _workspace(ws, lib.gptq_w4a16_lora_workspace_bytes(b, m, d, r), x)
+    ws, nb = _workspace(ws, lib.gptq_w4a16_lora_workspace_bytes(b, m, d, group_size, r), x)
     _call("gptq_w4a16_lora", dev, x.data_ptr(), b, qweight.data_ptr(), scales.data_ptr(),
           qzeros.data_ptr(), _addr(perm), m, d, group_size, lora_a.data_ptr(), lora_b.data_ptr(),
           lora_scaling.data_ptr(), adapter.data_ptr(), n, r, y.data_ptr(), ws.data_ptr(), nb)

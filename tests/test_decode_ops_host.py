@@ -32,9 +32,9 @@ def _caller(fn, names, defaults):
 
 
 def test_lora(lib):
-    ws = G.gptq_w4a16_lora_workspace_bytes(4, 64, 256, 8)
-    assert ws > 0 and G.gptq_w4a16_lora_workspace_bytes(0, 64, 256, 8) == 0
-    assert G.gptq_w4a16_lora_workspace_bytes(400, 64, 256, 8) > ws
+    ws = G.gptq_w4a16_lora_workspace_bytes(4, 64, 256, 128, 8)
+    assert ws > 0 and G.gptq_w4a16_lora_workspace_bytes(0, 64, 256, 128, 8) == 0
+    assert G.gptq_w4a16_lora_workspace_bytes(400, 64, 256, 128, 8) > ws
     names = ("x batch qw sc qz perm m d g a b scaling adapter n rank y ws wsb stream").split()
     c = _caller(lib.gptq_w4a16_lora, names,
                 dict(x=FAKE, batch=4, qw=FAKE, sc=FAKE, qz=FAKE, perm=None, m=64, d=256, g=128,

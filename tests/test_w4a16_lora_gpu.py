@@ -120,7 +120,7 @@ def test_graph_replay_other_stream_and_given_buffers():
     lay = {k: _t(c[1][k]) for k in ("qw", "sc", "qz", "perm")}
     a, b, sc, ids = (_t(v) for v in (c[2], c[3], c[4], c[5]))
     y = torch.full((3, 500), 7.0, device=DEV)
-    ws = torch.full((G.gptq_w4a16_lora_workspace_bytes(3, 500, 1024, 16),), 255, dtype=torch.uint8,
+    ws = torch.full((G.gptq_w4a16_lora_workspace_bytes(3, 500, 1024, 64, 16),), 255, dtype=torch.uint8,
                     device=DEV)
     call = lambda: G.gptq_w4a16_lora(x, lay["qw"], lay["sc"], lay["qz"], a, b, ids, sc, 64,  # noqa
                                      lay["perm"], y, ws)
