@@ -3,9 +3,10 @@
 //
 //   y[b] = x[b] Q^T + scaling[a] (x[b] A_a^T) B_a^T,   a = adapter[b]
 //
-// Up to LORA_SWEEP rows of x two kernels: the first sweeps the packed rows (w4_rows.cuh) for chunks of up to
+// Up to LORA_SWEEP rows of x two kernels (three with an act-order permutation, which the
+// first applies): one sweeps the packed rows (w4_rows.cuh) for chunks of up to
 // 16 rows of x and slices of the columns, and computes t[b] = scaling A_a x[b]
-// beside it; the second joins the slices and adds B_a t.  Beyond, the product is
+// beside it; the other joins the slices and adds B_a t.  Beyond, the product is
 // the tcgen05 kernel's (w4a16_tc.cu), with t computed where the activations are put
 // in its order.  Partial results go through memory, not atomics: their order is
 // fixed.
@@ -34,19 +35,84 @@ struct LoraParams {
     W4Layer lay;
     int chunk, chunks, slice, slices, groups;
     float* t;          // batch x rank
-    __half* xp;        // batch x d, reordered for the tcgen05 product
+    __half* xp;        // batch x d: x in the order of the sweep or of the tcgen05 product, or null
+    int tc;
     float* part;       // slices x batch x m
     float* y;
 };
 
+// t[b][r] = scaling (A_a[r] . x[b]).  A unit is a tile of eight rows b, one of the
+// adapters among them and 16 rank rows: S = A x^T on m16n8k16 mma.sync, the columns
+// split over the CTA's 16 warps.  A lane's 16-byte load is eight neighbouring columns
+// of its row, for A and x alike: operands of two products, whose order of the columns
+// does not matter.  Rows of other adapters are computed along and dropped.  All
+// threads; red: 16 x 128 floats.
+__device__ __forceinline__ void lora_shrink(const LoraParams& p, float* red)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const int tiles = int((p.batch + 7) / 8), rts = (p.rank + 15) / 16;
+    const int units = tiles * 8 * rts;
+    const int k0 = int(p.d / 32) * warp / W4_WARPS, k1 = int(p.d / 32) * (warp + 1) / W4_WARPS;
+    for (int u = blockIdx.x; u < units; u += gridDim.x) {
+        // neighbouring CTAs take other rank rows and row tiles before another adapter
+        const int slot = u / (tiles * rts), rest = u - slot * (tiles * rts);
+        const int64_t b0 = int64_t(rest / rts) * 8;
+        const int r0 = rest % rts * 16;
+        if (b0 + slot >= p.batch) continue;
+        const int id = p.adapter[b0 + slot];
+        if (id < 0 || id >= p.n) {
+            if (id != -1 && threadIdx.x == 0) atomicCAS(&g_device_status, 0, kErrIndex);
+            continue;
+        }
+        bool first = true;                                 // of the tile's rows with this adapter
+        for (int j = 0; j < slot; ++j) first = first && p.adapter[b0 + j] != id;
+        if (!first) continue;
+        const __half* a0 = p.a + (int64_t(id) * p.rank + min(r0 + g, p.rank - 1)) * p.d + t * 8;
+        const __half* a1 = p.a + (int64_t(id) * p.rank + min(r0 + g + 8, p.rank - 1)) * p.d + t * 8;
+        const __half* x = p.x + min(b0 + g, p.batch - 1) * p.d + t * 8;
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int k = k0; k < k1; k += 4) {                 // four rounds of 32 columns in flight
+            uint4 av[4], bv[4], xv[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (k + i < k1) {
+                    av[i] = __ldg(reinterpret_cast<const uint4*>(a0 + (k + i) * 32));
+                    bv[i] = __ldg(reinterpret_cast<const uint4*>(a1 + (k + i) * 32));
+                    xv[i] = __ldg(reinterpret_cast<const uint4*>(x + (k + i) * 32));
+                }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (k + i < k1) {
+                    mma_16816(s, av[i].x, bv[i].x, av[i].y, bv[i].y, xv[i].x, xv[i].y);
+                    mma_16816(s, av[i].z, bv[i].z, av[i].w, bv[i].w, xv[i].z, xv[i].w);
+                }
+        }
+        __syncthreads();                                   // the last unit's sums have been read
+        *reinterpret_cast<float4*>(red + (warp * 32 + lane) * 4) = make_float4(s[0], s[1], s[2], s[3]);
+        __syncthreads();
+        if (threadIdx.x < 128) {                           // element e of lane l
+            const int l = threadIdx.x >> 2, e = threadIdx.x & 3;
+            float v = 0.f;
+#pragma unroll
+            for (int w = 0; w < W4_WARPS; ++w) v += red[w * 128 + threadIdx.x];
+            const int r = r0 + (l >> 2) + 8 * (e >> 1);
+            const int64_t b = b0 + 2 * (l & 3) + (e & 1);
+            if (r < p.rank && b < p.batch && p.adapter[b] == id)
+                p.t[b * p.rank + r] = v * p.scaling[id];
+        }
+    }
+}
+
 // t[b][r] = scaling (A_a[r] . x[b]): one warp per (r, b), the warps of a CTA on
-// neighbouring rows b, which find a shared adapter's row in L1
-__device__ __forceinline__ void lora_shrink(const LoraParams& p, int warps)
+// neighbouring rows b, which find a shared adapter's row in L1 (up to LORA_SWEEP rows:
+// 8 rows of rank 16 and 4096 columns leave the whole call 9 us faster than lora_shrink,
+// which has a CTA per unit)
+__device__ __forceinline__ void lora_shrink_few(const LoraParams& p)
 {
     const int lane = threadIdx.x & 31;
     const int64_t items = p.batch * p.rank;
-    for (int64_t it = int64_t(blockIdx.x) * warps + (threadIdx.x >> 5); it < items;
-         it += int64_t(gridDim.x) * warps) {
+    for (int64_t it = int64_t(blockIdx.x) * W4_WARPS + (threadIdx.x >> 5); it < items;
+         it += int64_t(gridDim.x) * W4_WARPS) {
         const int r = int(it / p.batch);
         const int64_t b = it - r * p.batch;
         int id = p.adapter[b];
@@ -121,10 +187,14 @@ lora_product_kernel(const __grid_constant__ CUtensorMap tm, const LoraParams p)
         w4_sweep<NT, LORA_KW, WIDE, false, false>(
             pipe, &tm, p.lay, int64_t(g0) * LORA_ROWS, p.m, 0u, st, g1 - g0, k0, steps,
             [&]() {
-                w4_stage_half<NT, WIDE>(x, xs, [&](int n) { return p.x + (b0 + n) * p.d; }, p.perm,
+                if (!shrunk) {                             // beside the first copies
+                    if (p.xp) pdl_wait();                  // what the front kernel wrote
+                    else lora_shrink_few(p);
+                    shrunk = true;
+                }
+                const __half* src = p.xp ? p.xp : p.x;
+                w4_stage_half<NT, WIDE>(x, xs, [&](int n) { return src + (b0 + n) * p.d; }, nullptr,
                                         k0 * W4_STEP, steps, cols, int(p.d));
-                if (!shrunk) lora_shrink(p, W4_WARPS);               // beside the first copies
-                shrunk = true;
                 __syncthreads();
             },
             [&](int grp, int r, int n, float v) {
@@ -133,16 +203,41 @@ lora_product_kernel(const __grid_constant__ CUtensorMap tm, const LoraParams p)
             });
         u += g1 - g0;
     }
-    if (!shrunk) lora_shrink(p, W4_WARPS);
+    if (!shrunk && p.xp) pdl_wait();
+    else if (!shrunk) lora_shrink_few(p);
 }
 
-// t, and the activations in the order of the tcgen05 product
-__global__ void __launch_bounds__(256) lora_front_kernel(const LoraParams p)
+// t, and the activations in the order of the product that follows, eight at a time
+__global__ void __launch_bounds__(W4_THREADS) lora_front_kernel(const LoraParams p)
 {
-    lora_shrink(p, 8);
+    __shared__ __align__(16) float red[W4_WARPS * 128];
     const int64_t total = p.batch * p.d;
-    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < total; i += int64_t(gridDim.x) * 256)
-        p.xp[i] = wq_gathered(p.x, p.perm, i, p.d);
+    for (int64_t i = (int64_t(blockIdx.x) * W4_THREADS + threadIdx.x) * 8; i < total;
+         i += int64_t(gridDim.x) * (W4_THREADS * 8)) {
+        alignas(16) __half h[8];
+        if (p.perm) {
+            const int64_t b = i / p.d;
+            const int k = int(i - b * p.d);
+            const int4 lo = *reinterpret_cast<const int4*>(p.perm + k);
+            const int4 hi = *reinterpret_cast<const int4*>(p.perm + k + 4);
+            const int at[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int c = p.tc ? at[(j & 1) ? 4 + (j >> 1) : (j >> 1)] : at[j];
+                const bool ok = c >= 0 && c < p.d;         // a bad index is not followed
+                if (!ok) atomicCAS(&g_device_status, 0, kErrIndex);
+                h[j] = ok ? p.x[b * p.d + c] : __ushort_as_half(0);
+            }
+        } else {                                           // (the tcgen05 product)
+            const uint4 v = *reinterpret_cast<const uint4*>(p.x + i);
+            const __half* s = reinterpret_cast<const __half*>(&v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) h[j] = s[(j & 1) ? 4 + (j >> 1) : (j >> 1)];
+        }
+        *reinterpret_cast<uint4*>(p.xp + i) = *reinterpret_cast<const uint4*>(h);
+    }
+    if (p.tc) lora_shrink(p, red);
+    else lora_shrink_few(p);
 }
 
 // y[b][r] = sum of part over the slices + B_a[r] . t[b]; one row r and LORA_JOIN rows
@@ -219,15 +314,14 @@ LoraPlan lora_plan(int64_t T, int64_t m, int64_t d, int64_t g, int rank)
 {
     LoraPlan p{};
     p.at_xp = align_up(size_t(T) * rank * 4, 256);
+    p.at_part = p.at_xp + align_up(size_t(T) * d * 2, 1024);
     p.tc = T > LORA_SWEEP && g % 64 == 0;
     if (p.tc) {
         p.wq = wq_plan(T, m, d, g, LORA_SMS);
         p.slices = p.wq.ksplit;
-        p.at_part = p.at_xp + align_up(size_t(T) * d * 2, 1024);
         p.bytes = p.at_part + (p.slices > 1 ? align_up(size_t(p.slices) * T * m * 4, 256) : 0);
         return p;
     }
-    p.at_part = p.at_xp;
     p.nt = T > W4_COLS ? 2 : 1;
     p.chunk = int(std::min<int64_t>(T, W4_COLS * p.nt));
     p.chunks = int((T + p.chunk - 1) / p.chunk);
@@ -295,17 +389,20 @@ extern "C" int gptq_w4a16_lora(const uint16_t* x, int64_t batch, const uint32_t*
     p.chunk = plan.chunk; p.chunks = plan.chunks; p.slice = plan.slice; p.slices = plan.slices;
     p.groups = plan.groups;
     p.t = static_cast<float*>(ws);
-    p.xp = reinterpret_cast<__half*>(static_cast<uint8_t*>(ws) + plan.at_xp);
+    p.tc = plan.tc;
+    p.xp = plan.tc || perm ? reinterpret_cast<__half*>(static_cast<uint8_t*>(ws) + plan.at_xp) : nullptr;
     // one slice: in y, where the join finds it (each thread reads and writes its own elements)
     p.part = plan.slices > 1
                  ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + plan.at_part) : y;
     p.y = y;
     cudaStream_t st = as_stream(stream);
     KernelTimer kt(kKLora, st);
-    if (plan.tc) {
-        lora_front_kernel<<<(unsigned)(device_sm_count() * 8), 256, 0, st>>>(p);
+    if (p.xp) {
+        lora_front_kernel<<<(unsigned)(device_sm_count() * (plan.tc ? 2 : 1)), W4_THREADS, 0, st>>>(p);
         count_launches();
         if (launch_status() != GPTQ_OK) return GPTQ_ERR_CUDA;
+    }
+    if (plan.tc) {
         const int rc = wq_run(plan.wq, p.xp, batch, qweight, p.lay.sc, qzeros, d_out, d_in, g, p.part,
                               batch * d_out, st);
         if (rc != GPTQ_OK) return rc;
@@ -323,7 +420,13 @@ extern "C" int gptq_w4a16_lora(const uint16_t* x, int64_t batch, const uint32_t*
                          done[(plan.nt - 1) * 2 + (wide ? 1 : 0)]))
             return GPTQ_ERR_CUDA;
         const int64_t units = int64_t(plan.chunks) * plan.slices * plan.groups;
-        kern<<<(unsigned)std::min<int64_t>(device_sm_count(), units), W4_THREADS, smem, st>>>(tm, p);
+        const unsigned grid = (unsigned)std::min<int64_t>(device_sm_count(), units);
+        if (p.xp) {
+            if (launch_after(kern, grid, W4_THREADS, smem, st, tm, p) != cudaSuccess)
+                return GPTQ_ERR_CUDA;
+        } else {
+            kern<<<grid, W4_THREADS, smem, st>>>(tm, p);
+        }
         count_launches();
         if (launch_status() != GPTQ_OK) return GPTQ_ERR_CUDA;
     }
