@@ -571,7 +571,7 @@ __device__ __forceinline__ void w4_sweep(W4Pipe& pipe, const CUtensorMap* tm, co
     issue();
     // scales and zero points: WIDE: of four steps at a time (lane t those of step
     // t), four steps ahead; else of block t of a step, one step ahead
-    const __half* sc = l.sc + row0 * l.G;
+    const uint8_t* sc = reinterpret_cast<const uint8_t*>(l.sc) + row0 * (l.G * 2);
     const uint8_t* qz = l.qz + row0 * l.Gb;
     const uint32_t last = uint32_t(end - row0 - 1);
     auto params = [&](W4Raw& p, int grp, int j) {
@@ -579,14 +579,16 @@ __device__ __forceinline__ void w4_sweep(W4Pipe& pipe, const CUtensorMap* tm, co
         const uint32_t at = (block * l.grp.mul) >> 22;
         const uint32_t first = (grp * RW + rw) * ROWS + w4_rho(g);
         p.shift = 4 * (at & 1);
+        // bytes from the sweep's first row on: a uniform base and one 32-bit register
+        const uint32_t gs = uint32_t(l.G) * 2, gz = uint32_t(l.Gb);
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const uint32_t r = PAIR ? first + m * 8 + i * pair
                                         : min(first + m * 16 + i * 8, last);
-                p.s[m][i] = ld_nc_u16(sc + (r * uint32_t(l.G) + at));
-                p.z[m][i] = ld_nc_u8(qz + (r * uint32_t(l.Gb) + (at >> 1)));
+                p.s[m][i] = ld_nc_u16(sc + (r * gs + at * 2));
+                p.z[m][i] = ld_nc_u8(qz + (r * gz + (at >> 1)));
             }
     };
     constexpr int EVERY = WIDE ? 4 : 1;
@@ -612,22 +614,25 @@ __device__ __forceinline__ void w4_sweep(W4Pipe& pipe, const CUtensorMap* tm, co
             if (!w4_try_wait(pipe.bar + pipe.get * 8, pipe.phase))
                 w4_wait_long(pipe.bar + pipe.get * 8, pipe.phase, pipe.abort);
             const uint32_t slot = from + pipe.get * W4_SLOT;
+            auto next_params = [&](int jj) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                if (j + u < n) {
-                    if ((j + u) % EVERY == 0) {
+                for (int m = 0; m < 2; ++m)
 #pragma unroll
-                        for (int m = 0; m < 2; ++m)
-#pragma unroll
-                            for (int i = 0; i < 2; ++i)
-                                par[m][i] = w4_param(ahead.s[m][i], ahead.z[m][i], ahead.shift);
-                        if (j + u + EVERY < n) params(ahead, grp, j + u + EVERY);
-                        else params(ahead, min(grp + 1, groups - 1), 0);
-                    }
-                    w4_step<NT, WIDE, SPLIT, PAIR>(y, WIDE ? slot ^ (64 * u) : slot, u, par,
-                                                   (j & 2) + u, x, xs, xw, st.plane);
-                    xs += (WIDE ? 1 : 4) * W4_COLS * NT * 4;
-                }
+                    for (int i = 0; i < 2; ++i)
+                        par[m][i] = w4_param(ahead.s[m][i], ahead.z[m][i], ahead.shift);
+                if (jj + EVERY < n) params(ahead, grp, jj + EVERY);
+                else params(ahead, min(grp + 1, groups - 1), 0);
+            };
+            auto step = [&](int u) {
+                w4_step<NT, WIDE, SPLIT, PAIR>(y, WIDE ? slot ^ (64 * u) : slot, u, par, (j & 2) + u, x,
+                                               xs, xw, st.plane);
+                xs += (WIDE ? 1 : 4) * W4_COLS * NT * 4;
+            };
+            if (!WIDE || (j & 2) == 0) next_params(j);
+            step(0);
+            if (j + 1 < n) {
+                if (!WIDE) next_params(j + 1);
+                step(1);
             }
             pipe.phase ^= pipe.get;
             pipe.get ^= 1u;

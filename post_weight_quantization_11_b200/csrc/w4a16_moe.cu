@@ -19,7 +19,7 @@ constexpr int kMoeTokens = 64, kMoeExperts = 256, kMoeTopK = 8;
 constexpr int64_t kMoeMaxModel = 20480;     // a row of x has to fit beside the ring
 // Of w4_sweep: more column shares make finer row groups, fewer make longer ones
 constexpr int MOE_MAX_SMEM = W4_MAX_SMEM - 11 * 1024;     // beside the routes
-constexpr int MOE_IN_KW = 8, MOE_IN_ROWS = 16 * (W4_WARPS / MOE_IN_KW);
+template <int KW> constexpr int kMoeInRows = 16 * (W4_WARPS / KW);
 constexpr int MOE_OUT_KW = 4, MOE_OUT_ROWS = 32 * (W4_WARPS / MOE_OUT_KW);
 constexpr int kMoeSms = 148;               // the plan does not depend on the device that is current
 constexpr int kMoePairs = kMoeTokens * kMoeTopK;
@@ -167,7 +167,7 @@ __device__ __forceinline__ void moe_routes(const MoeParams& p, MoeRoutes& r, int
 // h = silu(G x) (U x) of every pair.  A row tile is 8 gate rows and the same 8
 // up rows, so that a lane holds both of an element of h.  The CTAs share the
 // row tiles of all chunks evenly; a CTA stages a chunk's tokens once.
-template <bool WIDE>
+template <int KW, bool WIDE>
 __global__ void __launch_bounds__(W4_THREADS, 1) moe_in_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p)
 {
     extern __shared__ uint8_t smem_raw[];
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(W4_THREADS, 1) moe_in_kernel(const __grid_cons
     __shared__ int cnt[kMoeExperts], off[kMoeExperts], coff[kMoeExperts];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const int steps = int(p.d / W4_STEP), groups = int(p.f / MOE_IN_ROWS);
+    const int steps = int(p.d / W4_STEP), groups = int(p.f / kMoeInRows<KW>);
     uint4* x = reinterpret_cast<uint4*>(smem + w4_at_x(1));
     float* xs = reinterpret_cast<float*>(smem + w4_at_x(1) + w4_x_bytes(steps, p.chunk, false));
     W4Pipe pipe = w4_pipe<1>(smem, &abort);
@@ -196,8 +196,8 @@ __global__ void __launch_bounds__(W4_THREADS, 1) moe_in_kernel(const __grid_cons
         const int16_t* list = r.list + r.start[c];
         const int64_t row0 = int64_t(e) * 2 * p.f;
         const W4Stage st{smem_u32(x), smem_u32(xs), cols, 0};
-        w4_sweep<1, MOE_IN_KW, WIDE, false, true>(
-            pipe, &tm, p.in, row0 + int64_t(g0) * MOE_IN_ROWS, row0 + 2 * p.f, uint32_t(p.f), st,
+        w4_sweep<1, KW, WIDE, false, true>(
+            pipe, &tm, p.in, row0 + int64_t(g0) * kMoeInRows<KW>, row0 + 2 * p.f, uint32_t(p.f), st,
             g1 - g0, 0, steps,
             [&]() {
                 w4_stage_half<1, WIDE>(
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(W4_THREADS, 1) moe_in_kernel(const __grid_cons
             },
             [&](int grp, int r, int n, float gate, float up) {
                 if (n < cols)
-                    p.h[int64_t(list[n]) * p.f + int64_t(g0 + grp) * MOE_IN_ROWS + r] =
+                    p.h[int64_t(list[n]) * p.f + int64_t(g0 + grp) * kMoeInRows<KW> + r] =
                         gate / (1.f + expf(-gate)) * up;
             });
         u += g1 - g0;
@@ -378,19 +378,25 @@ extern "C" int gptq_w4a16_moe(const uint16_t* x, int64_t tokens, const float* lo
     KernelTimer kt(kKMoe, st);
     const int sms = device_sm_count();
     auto ctas = [&](int64_t units) { return (unsigned)std::min<int64_t>(sms, units); };
-    auto in = gi % W4_STEP == 0 ? moe_in_kernel<true> : moe_in_kernel<false>;
-    auto out = go % W4_STEP == 0 ? moe_out_kernel<true> : moe_out_kernel<false>;
-    static std::atomic<bool> done[4][64];
-    if (!smem_opt_in(reinterpret_cast<const void*>(in), MOE_MAX_SMEM, done[gi % W4_STEP == 0]) ||
-        !smem_opt_in(reinterpret_cast<const void*>(out), MOE_MAX_SMEM, done[2 + (go % W4_STEP == 0)]))
-        return GPTQ_ERR_CUDA;
+    // Four column shares (64 rows of h a group, half the joins) where every CTA has many
+    // groups, eight (32 rows) where few groups would leave the last round half empty
     const int64_t pairs = tokens * top_k;
+    const int64_t chunks = std::max(std::min(pairs, n_experts), ceil_div(pairs, plan.chunk));
+    const bool fine = chunks * (d_ff / kMoeInRows<4>) < 8 * sms;
+    const bool wi = gi % W4_STEP == 0;
+    auto in = fine ? (wi ? moe_in_kernel<8, true> : moe_in_kernel<8, false>)
+                   : (wi ? moe_in_kernel<4, true> : moe_in_kernel<4, false>);
+    auto out = go % W4_STEP == 0 ? moe_out_kernel<true> : moe_out_kernel<false>;
+    static std::atomic<bool> done[6][64];
+    if (!smem_opt_in(reinterpret_cast<const void*>(in), MOE_MAX_SMEM, done[2 * fine + wi]) ||
+        !smem_opt_in(reinterpret_cast<const void*>(out), MOE_MAX_SMEM, done[4 + (go % W4_STEP == 0)]))
+        return GPTQ_ERR_CUDA;
     CUtensorMap ti, to;
     if (w4_tmap(&ti, qweight_in, n_experts * 2 * d_ff, d_model, 16) != GPTQ_OK ||
         w4_tmap(&to, qweight_out, n_experts * d_model, d_ff, 32) != GPTQ_OK)
         return GPTQ_ERR_CUDA;
     if (plan.smem_in > MOE_MAX_SMEM || plan.smem_out > MOE_MAX_SMEM) return GPTQ_ERR_SHAPE;
-    in<<<ctas(pairs * (d_ff / MOE_IN_ROWS)), W4_THREADS, plan.smem_in, st>>>(ti, p);
+    in<<<ctas(pairs * (d_ff / (fine ? kMoeInRows<8> : kMoeInRows<4>))), W4_THREADS, plan.smem_in, st>>>(ti, p);
     // what follows reads what the kernel before it wrote: not launched without it
     if (launch_status() != GPTQ_OK ||
         launch_after(out, ctas(pairs * plan.slices * (d_model / MOE_OUT_ROWS)), W4_THREADS,
