@@ -33,7 +33,9 @@
 // ones fold every 32 columns, for which a lane takes words of a row that are 16
 // bytes apart, so that a product stays inside 32 columns.
 // SPLIT: x in two fp16 parts (22 bits) for fp32 activations, scaled by a power
-// of two per column.
+// of two per column: W4_TWICE: each read of the rows is multiplied with both;
+// W4_BESIDE: up to four columns, the second parts are operand columns 4 .. 7 (half
+// the products; 0.8 of the time of the experts' second product for one token).
 #pragma once
 
 #include <atomic>
@@ -49,6 +51,7 @@ constexpr int W4_SLOT = 4096;                     // bytes of one: two steps of 
 constexpr int W4_MAX_SMEM = 226 * 1024;           // dynamic shared memory of a CTA
 constexpr int W4_STEP = 128;                      // columns per step
 constexpr int W4_COLS = 8;                        // columns n of an operand
+enum W4Split : int { W4_WHOLE = 0, W4_TWICE = 1, W4_BESIDE = 2 };
 
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch()
@@ -201,7 +204,7 @@ template <bool PAIR> __host__ __device__ constexpr int w4_row(int m, int i)
 // the lane's rows, held by lane t of the quad for (WIDE) step src of four or
 // (otherwise) block t of this step.
 // x[c]: shared address of the lane's part of operand column 8 c + g.
-template <int NT, bool WIDE, bool SPLIT, bool PAIR>
+template <int NT, bool WIDE, int SPLIT, bool PAIR>
 __device__ __forceinline__ void w4_step(float (&y)[NT][2][4], uint32_t slot, int u,
                                         const uint32_t (&p)[2][2], int src, uint32_t (&x)[NT],
                                         uint32_t xs, uint32_t xw, uint32_t plane)
@@ -236,7 +239,7 @@ __device__ __forceinline__ void w4_step(float (&y)[NT][2][4], uint32_t slot, int
 #pragma unroll
         for (int c = 0; c < NT; ++c) {
 #pragma unroll
-            for (int h = 0; h < (SPLIT ? 2 : 1); ++h) {
+            for (int h = 0; h < (SPLIT == W4_TWICE ? 2 : 1); ++h) {
                 const uint4 f = lds16(h ? x[c] + plane : x[c]);
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
@@ -352,7 +355,7 @@ __device__ __forceinline__ void w4_stage_half(uint4* x, float* xs, Row row, cons
 template <int NT, bool WIDE, class Row>
 __device__ __forceinline__ void w4_stage_split(uint4* x, float* xs, float* undo, uint32_t* top,
                                                Row row, const int32_t* perm, int k0, int steps,
-                                               int cols, int d)
+                                               int cols, int d, bool beside)
 {
     constexpr int XS = W4_COLS * NT;
     for (int i = threadIdx.x; i < XS; i += blockDim.x) top[i] = 0u;
@@ -402,7 +405,7 @@ __device__ __forceinline__ void w4_stage_split(uint4* x, float* xs, float* undo,
         const int i = base + threadIdx.x;
         const bool on = i < total;
         const int n = on ? i / nch : 0, kc = on ? i - n * nch : 0;
-        float s = 0.f;
+        float s = 0.f, s2 = 0.f;                           // of the first and the second parts
         if (on) {
             float v[8];
             load(n, kc, v);
@@ -413,14 +416,20 @@ __device__ __forceinline__ void w4_stage_split(uint4* x, float* xs, float* undo,
                 const float a = v[j] * f;                  // exact
                 h[j] = __float2half_rn(a);
                 l[j] = __float2half_rn(a - __half2float(h[j]));
-                s += __half2float(h[j]) + __half2float(l[j]);
+                s += __half2float(h[j]);
+                s2 += __half2float(l[j]);
             }
             const int at = w4_chunk<WIDE>(kc, n, cols);
             x[at] = w4_order(h);
             x[at + cols * nch] = w4_order(l);
         }
         s = w4_join<WIDE>(s);
-        if (on && kc % (WIDE ? 16 : 4) == 0) xs[(kc / (WIDE ? 16 : 4)) * XS + n] = s * 0x1p-14f;
+        s2 = w4_join<WIDE>(s2);
+        if (on && kc % (WIDE ? 16 : 4) == 0) {
+            float* to = xs + (kc / (WIDE ? 16 : 4)) * XS + n;
+            to[0] = (beside ? s : s + s2) * 0x1p-14f;
+            if (beside) to[4] = s2 * 0x1p-14f;
+        }
     }
 }
 
@@ -529,7 +538,7 @@ static __device__ __noinline__ void w4_wait_long(uint32_t bar, uint32_t parity, 
 //   done(group, r, n, v): the joined result of row r of the group (PAIR: of the
 //            group's gate rows), column n; PAIR: done(group, r, n, v, v2) with the up
 //            row's.
-template <int NT, int KW, bool WIDE, bool SPLIT, bool PAIR, class StageF, class DoneF>
+template <int NT, int KW, bool WIDE, int SPLIT, bool PAIR, class StageF, class DoneF>
 __device__ __forceinline__ void w4_sweep(W4Pipe& pipe, const CUtensorMap* tm, const W4Layer& l,
                                          int64_t row0, int64_t end, uint32_t pair,
                                          const W4Stage& st, int groups, int k0, int steps,
@@ -600,7 +609,8 @@ __device__ __forceinline__ void w4_sweep(W4Pipe& pipe, const CUtensorMap* tm, co
     uint32_t x0[NT];
 #pragma unroll
     for (int c = 0; c < NT; ++c)
-        x0[c] = st.x + (min(c * 8 + g, st.cols - 1) * 4 + t) * 16 + s0 * 4 * xw;
+        x0[c] = st.x + (min(SPLIT == W4_BESIDE ? g & 3 : c * 8 + g, st.cols - 1) * 4 + t) * 16 +
+                s0 * 4 * xw + (SPLIT == W4_BESIDE && g >= 4 ? st.plane : 0u);
     const uint32_t xs0 = st.xs + s0 * (WIDE ? 1 : 4) * W4_COLS * NT * 4 + t * 8;
     const uint32_t from = pipe.ring + w4_rho(g) * 128 + (WIDE ? (t ^ w4_rho(g)) * 16 : t * 4);
     const uint32_t red = pipe.red + (warp * 32 + lane) * 4;
@@ -660,9 +670,11 @@ __device__ __forceinline__ void w4_sweep(W4Pipe& pipe, const CUtensorMap* tm, co
             }
             if constexpr (PAIR)
                 done(grp, w * 16 + m * 8 + w4_rho(g), c * 8 + 2 * t + j, v * 0x1p14f, v2 * 0x1p14f);
-            else
+            else {
+                if (SPLIT == W4_BESIDE) v += __shfl_xor_sync(0xffffffffu, v, 2);   // column n + 4
                 done(grp, w * 32 + m * 16 + (j >> 1) * 8 + w4_rho(g), c * 8 + 2 * t + (j & 1),
                      v * 0x1p14f);
+            }
         }
     }
     __syncthreads();                                       // x and red free again

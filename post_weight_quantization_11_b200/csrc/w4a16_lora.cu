@@ -184,7 +184,7 @@ lora_product_kernel(const __grid_constant__ CUtensorMap tm, const LoraParams p)
         const int64_t b0 = int64_t(c) * p.chunk;
         const int cols = int(min(int64_t(p.chunk), p.batch - b0));
         const W4Stage st{smem_u32(x), smem_u32(xs), cols, 0u};
-        w4_sweep<NT, LORA_KW, WIDE, false, false>(
+        w4_sweep<NT, LORA_KW, WIDE, W4_WHOLE, false>(
             pipe, &tm, p.lay, int64_t(g0) * LORA_ROWS, p.m, 0u, st, g1 - g0, k0, steps,
             [&]() {
                 if (!shrunk) {                             // beside the first copies

@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(W4_THREADS, 1) moe_in_kernel(const __grid_cons
         const int16_t* list = r.list + r.start[c];
         const int64_t row0 = int64_t(e) * 2 * p.f;
         const W4Stage st{smem_u32(x), smem_u32(xs), cols, 0};
-        w4_sweep<1, KW, WIDE, false, true>(
+        w4_sweep<1, KW, WIDE, W4_WHOLE, true>(
             pipe, &tm, p.in, row0 + int64_t(g0) * kMoeInRows<KW>, row0 + 2 * p.f, uint32_t(p.f), st,
             g1 - g0, 0, steps,
             [&]() {
@@ -245,19 +245,24 @@ __global__ void __launch_bounds__(W4_THREADS, 1) moe_out_kernel(const __grid_con
         const int16_t* list = r.list + r.start[c];
         const int64_t row0 = int64_t(e) * p.d;
         const W4Stage st{smem_u32(x), smem_u32(xs), cols, uint32_t(steps * 256 * cols)};
-        w4_sweep<1, MOE_OUT_KW, WIDE, true, false>(
-            pipe, &tm, p.out, row0 + int64_t(g0) * MOE_OUT_ROWS, row0 + p.d, 0u, st, g1 - g0, k0,
-            steps,
-            [&]() {
-                w4_stage_split<1, WIDE>(
-                    x, xs, undo, top, [&](int n) { return p.h + int64_t(list[n]) * p.f; },
-                    p.po ? p.po + e * p.f : nullptr, k0 * W4_STEP, steps, cols, int(p.f));
-                __syncthreads();
-            },
-            [&](int grp, int r, int n, float v) {
-                if (n < cols)
-                    p.part[(int64_t(sl) * p.T * p.k + list[n]) * p.d + int64_t(g0 + grp) * MOE_OUT_ROWS + r] = v * undo[n];
-            });
+        auto stage = [&]() {
+            w4_stage_split<1, WIDE>(
+                x, xs, undo, top, [&](int n) { return p.h + int64_t(list[n]) * p.f; },
+                p.po ? p.po + e * p.f : nullptr, k0 * W4_STEP, steps, cols, int(p.f), cols <= 4);
+            __syncthreads();
+        };
+        auto done = [&](int grp, int r, int n, float v) {
+            if (n < cols)
+                p.part[(int64_t(sl) * p.T * p.k + list[n]) * p.d + int64_t(g0 + grp) * MOE_OUT_ROWS +
+                       r] = v * undo[n];
+        };
+        const int64_t first = row0 + int64_t(g0) * MOE_OUT_ROWS;
+        if (cols <= 4)
+            w4_sweep<1, MOE_OUT_KW, WIDE, W4_BESIDE, false>(pipe, &tm, p.out, first, row0 + p.d, 0u, st,
+                                                            g1 - g0, k0, steps, stage, done);
+        else
+            w4_sweep<1, MOE_OUT_KW, WIDE, W4_TWICE, false>(pipe, &tm, p.out, first, row0 + p.d, 0u, st,
+                                                           g1 - g0, k0, steps, stage, done);
         u += g1 - g0;
     }
 }
