@@ -7,17 +7,21 @@
 //   mn = min(0, min x), mx = max(0, max x)  over a group of group_size elements
 //   s = fp16((mx - mn) / 15), z = clamp(rne(-mn / s)), c = clamp(rne(x / s) + z)
 //
-// One warp per row (a token's head of q, k or v): lane l holds the E =
-// head_dim / 32 consecutive elements from E l on.  A rotation partner is in the
-// same lane (interleaved) or rot_dim / 2 / E lanes away, a group is group_size
-// / E lanes, and a cache word is 8 / E lanes: shuffles, no shared memory.  Every
-// operation is an IEEE fp32 one with its own rounding (no contraction), so the
-// codes are a function of the inputs alone.
+// A row (a token's head of q, k or v) is head_dim / 8 lanes of eight consecutive
+// elements: a warp has 256 / head_dim rows at a time and a few rows of one token in
+// turn, whose position, cosines, sines and slot are read once; the next rows are
+// loaded while some are worked on.  A rotation partner is in the same lane
+// (interleaved) or rot_dim / 16 lanes away, a group is group_size / 8 lanes, and a
+// cache word is a lane's: shuffles, no shared memory.  Every operation is an IEEE
+// fp32 one with its own rounding (no contraction), so the codes are a function of
+// the inputs alone.
 #include "common.cuh"
 #include "quant_common.cuh"
 #include "tc_common.cuh"
 
 namespace gptq {
+
+constexpr int KVA_THREADS = 128;
 
 struct KvAppend {
     const void* q;
@@ -30,7 +34,8 @@ struct KvAppend {
     const int64_t* slots;
     const float* table;
     int64_t n_pos;
-    int rot, inter, g;
+    int rot, inter;
+    int lanes_shift, groups_shift;         // log2 of a group's lanes, of a row's groups
     int64_t pages;
     int page_shift;
     uint32_t* kc;
@@ -42,141 +47,182 @@ struct KvAppend {
     __half* v_val;
 };
 
-template <int N> struct alignas(N) Bytes { uint8_t b[N]; };
-
-// E consecutive elements as fp32
-template <int E> __device__ __forceinline__ void load_row(const float* p, float (&x)[E])
-{
-    using V = Bytes<(E * 4 < 16 ? E * 4 : 16)>;
-    constexpr int PER = sizeof(V) / 4;
+// Eight elements as loaded
+template <typename T> struct Raw8;
+template <> struct Raw8<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p)
+    {
+        a = __ldg(reinterpret_cast<const float4*>(p));
+        b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    }
+    __device__ __forceinline__ void get(float (&x)[8]) const
+    {
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    }
+};
+template <> struct Raw8<__half> {
+    uint4 a;
+    __device__ __forceinline__ void load(const __half* p) { a = __ldg(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void get(float (&x)[8]) const
+    {
+        const __half2* h = reinterpret_cast<const __half2*>(&a);
 #pragma unroll
-    for (int i = 0; i < E / PER; ++i)
-        *reinterpret_cast<V*>(&x[i * PER]) = reinterpret_cast<const V*>(p)[i];
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = __half22float2(h[i]);
+            x[2 * i] = f.x;
+            x[2 * i + 1] = f.y;
+        }
+    }
+};
+
+__device__ __forceinline__ void store8(__half* p, const float (&x)[8])
+{
+    uint4 v;
+    __half2* h = reinterpret_cast<__half2*>(&v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+    *reinterpret_cast<uint4*>(p) = v;
 }
 
-template <int E> __device__ __forceinline__ void load_row(const __half* p, float (&x)[E])
+// group_params for 4 bits without its divisions: the same values.  Both quotients are
+// rounded correctly by div_rn_recip where they decide anything: a range over 2^20 gives
+// the largest scale either way, one below 15 2^-25 the smallest.
+__device__ __forceinline__ GroupQ group_params4(float mn, float mx)
 {
-    alignas(16) __half h[E];
-    *reinterpret_cast<Bytes<E * 2>*>(h) = *reinterpret_cast<const Bytes<E * 2>*>(p);
-#pragma unroll
-    for (int i = 0; i < E; ++i) x[i] = __half2float(h[i]);
+    constexpr float K15 = 0x1.111112p-4f;                  // RN(1 / 15)
+    if (mn == mx) { mn = -1.f; mx = 1.f; }                 // all-zero group
+    const float s_pre = div_rn_recip(fminf(__fsub_rn(mx, mn), 1048576.f), 15.f, K15);
+    unsigned short hb = __half_as_ushort(__float2half_rn(s_pre));
+    hb = hb == 0 ? (unsigned short)0x0001u : hb >= 0x7c00u ? (unsigned short)0x7bffu : hb;
+    GroupQ g;
+    g.h = __ushort_as_half(hb);
+    g.s = __half2float(g.h);
+    g.r = __frcp_rn(g.s);
+    g.z = fminf(fmaxf(rne_for_clamp(div_rn_recip(-mn, g.s, g.r)), 0.f), 15.f);
+    return g;
 }
 
-template <int E> __device__ __forceinline__ void store_halves(__half* p, const float (&x)[E])
+template <typename T, int D, bool INTER>
+__global__ void __launch_bounds__(KVA_THREADS) kv4_append_kernel(const KvAppend p)
 {
-    alignas(16) __half h[E];
-#pragma unroll
-    for (int i = 0; i < E; ++i) h[i] = __float2half_rn(x[i]);
-    *reinterpret_cast<Bytes<E * 2>*>(p) = *reinterpret_cast<const Bytes<E * 2>*>(h);
-}
-
-template <typename T, int E>
-__global__ void __launch_bounds__(256) kv4_append_kernel(const KvAppend p)
-{
-    constexpr int D = 32 * E, NB = D / 32;
+    constexpr int NB = D / 32, LANES = D / 8, AT_ONCE = 32 / LANES;
     constexpr uint32_t ALL = 0xffffffffu;
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, l = lane % LANES;
+    const int64_t t = blockIdx.x;
     const int rows = p.hq + 2 * p.hkv;
-    const int64_t item = int64_t(blockIdx.x) * (blockDim.x / 32) + (threadIdx.x >> 5);
-    const int64_t t = item / rows;
-    if (t >= p.tokens) return;                             // whole warps
-    const int r = int(item - t * rows);
+    const int step = (KVA_THREADS / 32) * AT_ONCE * gridDim.y;
+    int first = (blockIdx.y * (KVA_THREADS / 32) + (threadIdx.x >> 5)) * AT_ONCE;   // of the warp's rows
+    if (first >= rows) return;                             // whole warps
     const int64_t slot = p.slots[t];
     const int32_t pos = p.rot ? p.pos[t] : 0;
+    const T* q = static_cast<const T*>(p.q) + t * p.qs + l * 8;
+    const T* k = static_cast<const T*>(p.k) + t * p.ks + l * 8;
+    const T* v = static_cast<const T*>(p.v) + t * p.vs + l * 8;
+    const int sub = lane / LANES;
+    auto row = [&](int i) {                                // (a row behind the last: the last)
+        i = min(i, rows - 1);
+        return i < p.hq ? q + i * D : i < p.hq + p.hkv ? k + (i - p.hq) * D : v + (i - p.hq - p.hkv) * D;
+    };
+    Raw8<T> next;
+    next.load(row(first + sub));
     if ((slot >> p.page_shift) >= p.pages || pos < 0 || (p.rot && pos >= p.n_pos)) {
         if (lane == 0) atomicCAS(&g_device_status, 0, kErrIndex);   // nothing of the token is written
         return;
     }
-    const bool is_q = r < p.hq, is_v = r >= p.hq + p.hkv;
-    const int h = is_q ? r : (is_v ? r - p.hq - p.hkv : r - p.hq);
-    const T* src = is_q ? static_cast<const T*>(p.q) + t * p.qs
-                        : (is_v ? static_cast<const T*>(p.v) + t * p.vs
-                                : static_cast<const T*>(p.k) + t * p.ks);
-    float x[E];
-    load_row<E>(src + int64_t(h) * D + lane * E, x);
-    if (!is_v && p.rot) {
-        const int half = p.rot / 2, sh = half / E;         // lanes between partners
-        const float* row = p.table + int64_t(pos) * p.rot;
-        const bool in = lane * E < p.rot;
-        if (p.inter) {
+    // the lane's cosines and sines, and the partner's lane
+    const int sh = p.rot / 16;                             // lanes between partners
+    const bool in = l * 8 < p.rot, low = l < sh;
+    const int mate = in ? (low ? lane + sh : lane - sh) : lane;
+    float c[INTER ? 4 : 8], s[INTER ? 4 : 8];
+    if (in) {
+        const float* tab = p.table + int64_t(pos) * p.rot + (INTER ? l * 4 : (low ? l : l - sh) * 8);
+        const float* tas = tab + p.rot / 2;
 #pragma unroll
-            for (int i = 0; i < E; i += 2) {
-                const int j = (lane * E + i) / 2;
-                const float c = in ? row[j] : 1.f, s = in ? row[half + j] : 0.f;
-                const float a = x[i], b = x[i + 1];
-                if (in) {
-                    x[i] = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
-                    x[i + 1] = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
+        for (int i = 0; i < (INTER ? 4 : 8); i += 4) {
+            const float4 a = __ldg(reinterpret_cast<const float4*>(tab + i));
+            const float4 b = __ldg(reinterpret_cast<const float4*>(tas + i));
+            c[i] = a.x; c[i + 1] = a.y; c[i + 2] = a.z; c[i + 3] = a.w;
+            s[i] = b.x; s[i + 1] = b.y; s[i + 2] = b.z; s[i + 3] = b.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < (INTER ? 4 : 8); ++i) { c[i] = 1.f; s[i] = 0.f; }
+    }
+    const int64_t page = slot >> p.page_shift, at = slot & ((1 << p.page_shift) - 1);
+    for (;;) {
+        float x[8];
+        next.get(x);
+        const int now = first + sub;
+        const bool live = now < rows, is_q = now < p.hq, is_v = now >= p.hq + p.hkv;
+        first += step;
+        if (first < rows) next.load(row(first + sub));
+        if (p.rot && first - step < p.hq + p.hkv) {        // (some row of the warp is not v)
+            const bool turn = in && !is_v;
+            if constexpr (INTER) {
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    const float a = x[i], b = x[i + 1];
+                    const float u = __fsub_rn(__fmul_rn(a, c[i / 2]), __fmul_rn(b, s[i / 2]));
+                    const float w = __fadd_rn(__fmul_rn(b, c[i / 2]), __fmul_rn(a, s[i / 2]));
+                    x[i] = turn ? u : a;
+                    x[i + 1] = turn ? w : b;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float o = __shfl_sync(ALL, x[i], mate);
+                    const float u = __fmul_rn(x[i], c[i]), w = __fmul_rn(o, s[i]);
+                    const float y = low ? __fsub_rn(u, w) : __fadd_rn(u, w);
+                    x[i] = turn ? y : x[i];
                 }
             }
-        } else {
-            const bool first = lane < sh;
-            const int mate = in ? (first ? lane + sh : lane - sh) : lane;
+        }
+        if (is_q) store8(p.q_out + (t * p.hq + now) * D + l * 8, x);
+        if (first - step + AT_ONCE > p.hq) {               // some row of the warp is k or v
+            const int h = now - p.hq - (is_v ? p.hkv : 0);
+            constexpr float BIG = 3.402823466e38f;
+            float mn = 0.f, mx = 0.f;
 #pragma unroll
-            for (int i = 0; i < E; ++i) {
-                const float o = __shfl_sync(ALL, x[i], mate);
-                const int j = (first ? lane : lane - sh) * E + i;
-                const float c = in ? row[j] : 1.f, s = in ? row[half + j] : 0.f;
-                if (in)
-                    x[i] = first ? __fsub_rn(__fmul_rn(x[i], c), __fmul_rn(o, s))
-                                 : __fadd_rn(__fmul_rn(x[i], c), __fmul_rn(o, s));
+            for (int i = 0; i < 8; ++i) {
+                x[i] = fminf(fmaxf(x[i], -BIG), BIG);      // NaN -> -BIG
+                mn = fminf(mn, x[i]);
+                mx = fmaxf(mx, x[i]);
+            }
+            const int lpg = 1 << p.lanes_shift;            // lanes per group
+            for (int o = 1; o < lpg; o <<= 1) {
+                mn = fminf(mn, __shfl_xor_sync(ALL, mn, o));
+                mx = fmaxf(mx, __shfl_xor_sync(ALL, mx, o));
+            }
+            if (live && !is_q) {
+                const GroupQ gq = group_params4(mn, mx);
+                uint32_t w = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float code = quant_code_fast(x[i], gq, 15.f);
+                    w |= code_byte(code) << (4 * i);
+                    x[i] = __fmul_rn(__fsub_rn(code, gq.z), gq.s);
+                }
+                __half* values = is_v ? p.v_val : p.k_val;
+                if (values) store8(values + (t * p.hkv + h) * D + l * 8, x);
+                if (slot >= 0) {                           // < 0: padding, the cache is left alone
+                    const int64_t rowi = ((page * p.hkv + h) << p.page_shift) + at;
+                    if ((l & (lpg - 1)) == 0)
+                        (is_v ? p.vp : p.kp)[(rowi << p.groups_shift) + (l >> p.lanes_shift)] =
+                            __halves2half2(gq.h, __float2half_rn(gq.z));
+                    const int i = l >> 2, u = l & 3;       // block of 32 elements, eighth of it
+                    if (is_v) {                            // half words: elements 32 i + 4 h' ..
+                        uint16_t* out = reinterpret_cast<uint16_t*>(p.vc + rowi * (D / 8));
+                        out[(2 * u) * NB + i] = uint16_t(w);
+                        out[(2 * u + 1) * NB + i] = uint16_t(w >> 16);
+                    } else {                               // words: elements 32 i + 8 t' ..
+                        p.kc[rowi * (D / 8) + u * NB + i] = w;
+                    }
+                }
             }
         }
-    }
-    if (is_q) {
-        store_halves<E>(p.q_out + (t * p.hq + h) * D + lane * E, x);
-        return;
-    }
-    constexpr float BIG = 3.402823466e38f;
-    float mn = 0.f, mx = 0.f;
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-        x[i] = fminf(fmaxf(x[i], -BIG), BIG);              // NaN -> -BIG
-        mn = fminf(mn, x[i]);
-        mx = fmaxf(mx, x[i]);
-    }
-    const int lpg = p.g / E;                               // lanes per group (a power of two)
-    for (int o = 1; o < lpg; o <<= 1) {
-        mn = fminf(mn, __shfl_xor_sync(ALL, mn, o));
-        mx = fmaxf(mx, __shfl_xor_sync(ALL, mx, o));
-    }
-    const GroupQ gq = group_params(mn, mx, 15.f);
-    uint32_t w = 0;
-    float val[E];
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-        const float c = quant_code_fast(x[i], gq, 15.f);
-        w |= code_byte(c) << (4 * i);
-        val[i] = __fmul_rn(__fsub_rn(c, gq.z), gq.s);
-    }
-    __half* values = is_v ? p.v_val : p.k_val;
-    if (values) store_halves<E>(values + (t * p.hkv + h) * D + lane * E, val);
-    if (slot < 0) return;                                  // padding: the cache is left alone
-    const int64_t page = slot >> p.page_shift, at = slot & ((1 << p.page_shift) - 1);
-    const int64_t rowi = (((page * p.hkv + h) << p.page_shift) + at);
-    if (lane % lpg == 0)
-        (is_v ? p.vp : p.kp)[rowi * (D / p.g) + lane / lpg] =
-            __halves2half2(gq.h, __float2half_rn(gq.z));
-    if (is_v) {                                            // half words: elements 32 i + 4 h' ..
-        uint16_t* out = reinterpret_cast<uint16_t*>(p.vc + rowi * (D / 8));
-        if constexpr (E == 2) {
-            w |= __shfl_xor_sync(ALL, w, 1) << 8;
-            if (!(lane & 1)) out[((lane >> 1) & 7) * NB + (lane >> 4)] = uint16_t(w);
-        } else if constexpr (E == 4) {
-            out[(lane & 7) * NB + (lane >> 3)] = uint16_t(w);
-        } else {
-            out[(2 * (lane & 3)) * NB + (lane >> 2)] = uint16_t(w);
-            out[(2 * (lane & 3) + 1) * NB + (lane >> 2)] = uint16_t(w >> 16);
-        }
-    } else {                                               // words: elements 32 i + 8 t' ..
-        uint32_t* out = p.kc + rowi * (D / 8);
-        if constexpr (E == 2) w |= __shfl_xor_sync(ALL, w, 1) << 8;
-        if constexpr (E == 2) w |= __shfl_xor_sync(ALL, w, 2) << 16;
-        if constexpr (E == 4) w |= __shfl_xor_sync(ALL, w, 1) << 16;
-        if (lane % (8 / E) == 0) {
-            const int word = lane * E / 8;                 // of the row, in element order
-            out[(word & 3) * NB + (word >> 2)] = w;
-        }
+        if (first >= rows) return;
     }
 }
 
@@ -229,7 +275,9 @@ extern "C" int gptq_kv4_append(const void* q, int64_t q_stride, const void* k, i
     p.hkv = kv_heads;
     p.pos = positions; p.slots = slots;
     p.table = cos_sin; p.n_pos = n_positions;
-    p.rot = rot_dim; p.inter = interleaved != 0; p.g = g;
+    p.rot = rot_dim; p.inter = interleaved != 0;
+    while ((8 << p.lanes_shift) < g) ++p.lanes_shift;
+    while ((g << p.groups_shift) < head_dim) ++p.groups_shift;
     p.pages = pages;
     while ((1 << p.page_shift) < page_size) ++p.page_shift;
     p.kc = k_codes; p.kp = reinterpret_cast<__half2*>(k_params);
@@ -237,19 +285,28 @@ extern "C" int gptq_kv4_append(const void* q, int64_t q_stride, const void* k, i
     p.q_out = reinterpret_cast<__half*>(q_out);
     p.k_val = reinterpret_cast<__half*>(k_values);
     p.v_val = reinterpret_cast<__half*>(v_values);
-    const int64_t items = tokens * (p.hq + 2 * p.hkv), blocks = ceil_div(items, 8);
-    if (blocks > 0x7fffffff) return GPTQ_ERR_SHAPE;
+    // CTAs per token: all rows at once while there are few tokens, six rounds a warp beyond
+    const int rows = p.hq + 2 * p.hkv, at_once = KVA_THREADS / 32 * (256 / head_dim);
+    const int64_t all = ceil_div(rows, at_once);
+    const int64_t split = std::max<int64_t>(
+        std::min<int64_t>(all, ceil_div(int64_t(device_sm_count()) * 8, tokens)), ceil_div(all, 6));
     cudaStream_t st = as_stream(stream);
     KernelTimer kt(kKKvAppend, st);
-    auto run = [&](auto kern) {
-        kern<<<(unsigned)blocks, 256, 0, st>>>(p);
+    auto run = [&](auto inter, auto plain) {
+        const dim3 grid((unsigned)tokens, (unsigned)split);
+        if (p.inter) inter<<<grid, KVA_THREADS, 0, st>>>(p);
+        else plain<<<grid, KVA_THREADS, 0, st>>>(p);
         count_launches();
         return launch_status();
     };
     const bool f32 = dtype == GPTQ_DTYPE_F32;
+#define KVA_RUN(D)                                                                        \
+    return f32 ? run(kv4_append_kernel<float, D, true>, kv4_append_kernel<float, D, false>)   \
+               : run(kv4_append_kernel<__half, D, true>, kv4_append_kernel<__half, D, false>);
     switch (head_dim) {
-        case 64: return f32 ? run(kv4_append_kernel<float, 2>) : run(kv4_append_kernel<__half, 2>);
-        case 128: return f32 ? run(kv4_append_kernel<float, 4>) : run(kv4_append_kernel<__half, 4>);
-        default: return f32 ? run(kv4_append_kernel<float, 8>) : run(kv4_append_kernel<__half, 8>);
+        case 64: KVA_RUN(64)
+        case 128: KVA_RUN(128)
+        default: KVA_RUN(256)
     }
+#undef KVA_RUN
 }
