@@ -38,6 +38,8 @@ namespace gptq {
 
 constexpr int KV_WARPS = 4, KV_TILE = 32, KV_RING = 3;
 constexpr float KV_LAZY = 7.f;
+constexpr float KV_NONE = -3e38f;          // the maximum of no scores: finite, so that no difference is NaN
+constexpr int KV_ALONE = 256;              // up to so many keys: one chunk, no second kernel
 
 struct KvAttn {
     const __half* q;
@@ -176,23 +178,24 @@ __global__ void __launch_bounds__(KV_WARPS * 32, KvShape<D, G>::CTAS) kv4_attent
     const uint32_t to0 = ring + (what < 2 ? what * Sh::CODES : 2 * Sh::CODES + (what - 2) * Sh::PARAMS) +
                          half * bytes;
     int ptile = warp, pslot = 0, pkey = c0 + warp * KV_TILE + half * 16;
-    uint32_t seen = 0;                                     // two bits a slot: halves with a valid page
+    bool stray = false;                                    // a page out of range was met
     uint32_t page = 0;
     auto look = [&]() { page = pkey < c1 ? uint32_t(table[pkey >> p.page_shift]) : 0u; };
     auto issue = [&]() {
         if (ptile >= tiles) return;
-        const bool in = pkey < c1 && lane < 8, go = in && page < uint32_t(p.pages);
-        if (in && !go) atomicCAS(&g_device_status, 0, kErrIndex);
-        const uint32_t who = __ballot_sync(ALL, go);
-        const uint32_t halves = (who & 1u) | ((who >> 3) & 2u);
-        seen = (seen & ~(3u << (2 * pslot))) | (halves << (2 * pslot));
+        const bool bad = page >= uint32_t(p.pages);
+        if (__any_sync(ALL, bad)) {                        // page 0 in its place; its keys are masked
+            if (bad) page = 0u;
+            if (lane == 0) atomicCAS(&g_device_status, 0, kErrIndex);
+            stray = true;
+        }
         const uint32_t bar = bar0 + pslot * 8;
         if (lane == 0)
             asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar),
-                         "r"(uint32_t(__popc(halves)) * (Sh::SLOT / 2))
+                         "r"(c0 + ptile * KV_TILE + 16 < c1 ? Sh::SLOT : Sh::SLOT / 2)
                          : "memory");
         __syncwarp();
-        if (go)
+        if (lane < 8 && pkey < c1)
             kv_bulk(to0 + pslot * Sh::SLOT, from0 + (uint64_t(page) * pageb + (uint32_t(pkey) & mask) * keyb),
                     bytes, bar);
         ptile += KV_WARPS;
@@ -248,7 +251,7 @@ __global__ void __launch_bounds__(KV_WARPS * 32, KvShape<D, G>::CTAS) kv4_attent
     const int last = sp.L - sp.n + (rt * 8 + min(sp.rows, 8) - 1) / grp + 1;
     const int all_from = p.window > 0 ? int(max(int64_t(last) - p.window, int64_t(0))) : 0;
 
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, zs[G][2] = {};
+    float m[2] = {KV_NONE, KV_NONE}, l[2] = {0.f, 0.f}, zs[G][2] = {};
     float o[NB][2][4] = {};                                // [block][nibbles 0, 2 | 1, 3]
     uint32_t top_exp = 0;                                  // biased fp16 exponent of the largest value scale
     float factor = 0x1p21f;                                // 2^(21 - top_exp): u < 2^(7 + KV_LAZY)
@@ -257,9 +260,8 @@ __global__ void __launch_bounds__(KV_WARPS * 32, KvShape<D, G>::CTAS) kv4_attent
     uint32_t phase = 0;
     for (int tile = warp; tile < tiles; tile += KV_WARPS) {
         const int k0 = c0 + tile * KV_TILE;
-        mbar_wait(&bars[warp * KV_RING + slot], phase, kErrWaitFull, &abort);
+        if (!w4_try_wait(bar0 + slot * 8, phase)) w4_wait_long(bar0 + slot * 8, phase, &abort);
         const uint8_t* base = smem + warp * (KV_RING * Sh::SLOT) + slot * Sh::SLOT;
-        const uint32_t halves = (seen >> (2 * slot)) & 3u;
         float sc[2][4];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {                      // scores of 16 keys
@@ -312,14 +314,21 @@ __global__ void __launch_bounds__(KV_WARPS * 32, KvShape<D, G>::CTAS) kv4_attent
                 }
             }
         }
-        const bool edge = k0 < all_from || k0 + KV_TILE > all_lim || halves != 3u;
+        const bool edge = k0 < all_from || k0 + KV_TILE > all_lim || stray;
+        uint32_t there = 3u;                               // halves with a valid page
         if (edge) {                                        // some keys are not seen by some row
+            if (stray)
+                for (int h = 0; h < 2; ++h) {
+                    const int key = k0 + h * 16;
+                    if (key < c1 && uint32_t(table[key >> p.page_shift]) >= uint32_t(p.pages))
+                        there &= ~(1u << h);
+                }
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int key = k0 + h * 16 + (e >> 1) * 8 + kv_key(g);
-                    if (key >= lim[e & 1] || key < from[e & 1] || !((halves >> h) & 1u))
+                    if (key >= lim[e & 1] || key < from[e & 1] || !((there >> h) & 1u))
                         sc[h][e] = -INFINITY;
                 }
         }
@@ -340,7 +349,7 @@ __global__ void __launch_bounds__(KV_WARPS * 32, KvShape<D, G>::CTAS) kv4_attent
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int key = k0 + h * 16 + i * 8 + kv_key(g);
-                    if (key < sp.lo || key >= c1 || !((halves >> h) & 1u))
+                    if (key < sp.lo || key >= c1 || !((there >> h) & 1u))
 #pragma unroll
                         for (int k = 0; k < G; ++k) vz[h][i][k] = 0u;
                 }
@@ -369,7 +378,7 @@ __global__ void __launch_bounds__(KV_WARPS * 32, KvShape<D, G>::CTAS) kv4_attent
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const float mn = fmaxf(m[j], mx[j]);
-                const float al = m[j] == -INFINITY ? 0.f : ex2(m[j] - mn), ad = al * down;
+                const float al = ex2(m[j] - mn), ad = al * down;
                 m[j] = mn;
                 l[j] *= al;
 #pragma unroll
@@ -383,12 +392,11 @@ __global__ void __launch_bounds__(KV_WARPS * 32, KvShape<D, G>::CTAS) kv4_attent
                     }
             }
         }
-        const float mu[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                sc[h][e] = ex2(sc[h][e] - mu[e & 1]);
+                sc[h][e] = ex2(sc[h][e] - m[e & 1]);
                 l[e & 1] += sc[h][e];
             }
 #pragma unroll
@@ -474,17 +482,14 @@ __global__ void __launch_bounds__(KV_WARPS * 32, KvShape<D, G>::CTAS) kv4_attent
     const int64_t unit = (int64_t(b) * gridDim.y + blockIdx.y) * p.splits + blockIdx.x;
     for (int e = threadIdx.x; e < rows * D; e += KV_WARPS * 32) {
         const int r = e / D, d = e - r * D;
-        float top = -INFINITY, sum = 0.f, v = 0.f;
+        float top = KV_NONE, sum = 0.f, v = 0.f;
 #pragma unroll
         for (int w = 0; w < KV_WARPS; ++w) top = fmaxf(top, wm[w][r]);
-        if (top > -INFINITY) {
 #pragma unroll
-            for (int w = 0; w < KV_WARPS; ++w) {
-                if (wm[w][r] == -INFINITY) continue;
-                const float c = ex2(wm[w][r] - top);
-                sum = fmaf(c, wl[w][r], sum);
-                v = fmaf(c, reinterpret_cast<const float*>(smem)[w * (8 * D) + e], v);
-            }
+        for (int w = 0; w < KV_WARPS; ++w) {
+            const float c = ex2(wm[w][r] - top);           // (a warp without keys: sum and v are 0)
+            sum = fmaf(c, wl[w][r], sum);
+            v = fmaf(c, reinterpret_cast<const float*>(smem)[w * (8 * D) + e], v);
         }
         if (p.splits == 1) {
             const int rr = rt * 8 + r;
@@ -510,26 +515,28 @@ template <int D> __global__ void __launch_bounds__(256) kv4_join_kernel(const Kv
     if (!sp.ok || r >= sp.rows) return;
     const int n = sp.hi > sp.base ? (sp.hi - sp.base + p.chunk - 1) / p.chunk : 0;
     const float* part = p.part + (int64_t(b) * gridDim.x + blockIdx.x) * p.splits * (8 * (D + 2));
-    float top = -INFINITY, sum = 0.f, v[E] = {};
+    float top = KV_NONE, sum = 0.f, v[E] = {};
     for (int s = lane; s < n; s += 32) top = fmaxf(top, part[int64_t(s) * (8 * (D + 2)) + 8 * D + r]);
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (top > -INFINITY)
-        for (int s = 0; s < n; ++s) {
-            const float* src = part + int64_t(s) * (8 * (D + 2));
-            const float c = ex2(src[8 * D + r] - top);   // 0 for a chunk this row does not see
-            sum = fmaf(c, src[8 * D + 8 + r], sum);
+#pragma unroll 4
+    for (int s = 0; s < n; ++s) {
+        const float* src = part + int64_t(s) * (8 * (D + 2));
+        const float c = ex2(src[8 * D + r] - top);         // (a chunk that this row does not see: 0s)
+        sum = fmaf(c, src[8 * D + 8 + r], sum);
 #pragma unroll
-            for (int e = 0; e < E; ++e) v[e] = fmaf(c, src[r * D + e * 32 + lane], v[e]);
-        }
+        for (int e = 0; e < E; ++e) v[e] = fmaf(c, src[r * D + e * 32 + lane], v[e]);
+    }
     const int rr = rt * 8 + r;
     __half* dst = p.out + ((sp.s0 + rr / grp) * p.hq + hk * grp + rr % grp) * D;
 #pragma unroll
     for (int e = 0; e < E; ++e) dst[e * 32 + lane] = __float2half_rn(sum > 0.f ? v[e] / sum : 0.f);
 }
 
-// Keys per chunk: a multiple of a CTA's round of tiles, and as few chunks as keep
-// eight CTAs (four at a time) on each SM when every sequence has the bound's length
+// Keys per chunk: a multiple of a CTA's round of tiles, and as few chunks as give each
+// SM eight CTAs (two rounds of four) when every sequence has the bound's length; twelve
+// from 8 sequences on, whose lengths may differ (32 ragged ones: 62 us against 67 with
+// eight; two of 131000: 95 us with eight, 105 with twelve)
 struct KvPlan { int chunk, splits, row_tiles; size_t bytes; };
 
 KvPlan kv_plan(int64_t seqs, int hq, int hkv, int D, int64_t max_q, int64_t max_len, int64_t window)
@@ -541,14 +548,16 @@ KvPlan kv_plan(int64_t seqs, int hq, int hkv, int D, int64_t max_q, int64_t max_
     span = std::max<int64_t>(span, 1);
     constexpr int ROUND = KV_WARPS * KV_TILE;
     const int64_t units = seqs * hkv * k.row_tiles;
-    int64_t chunk = (units * span + 148 * 8 - 1) / (148 * 8);
+    const int64_t aim = 148 * (seqs < 8 ? 8 : 12);
+    int64_t chunk = (units * span + aim - 1) / aim;
     chunk = std::max<int64_t>(ROUND, (chunk + ROUND - 1) / ROUND * ROUND);
+    if (span <= KV_ALONE) chunk = std::max<int64_t>(chunk, (span + ROUND - 1) / ROUND * ROUND);
     chunk = std::max<int64_t>(chunk, ((span + 4095) / 4096 + ROUND - 1) / ROUND * ROUND);
     k.chunk = int(std::min<int64_t>(chunk, int64_t(1) << 30));
     k.splits = int((span + k.chunk - 1) / k.chunk);
-    // splits <= ceil(1184 / units) by the choice of chunk; this bound grows with every
+    // splits <= ceil(aim / units) by the choice of chunk; this bound grows with every
     // argument, so a workspace for the bounds serves every smaller call
-    const int64_t most = std::min(units * ((max_len + ROUND - 1) / ROUND + 1), units + 148 * 8);
+    const int64_t most = std::min(units * ((max_len + ROUND - 1) / ROUND + 1), units + 148 * 12);
     k.bytes = align_up(size_t(most) * 8 * (D + 2) * 4, 256);
     return k;
 }

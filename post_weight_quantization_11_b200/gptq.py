@@ -819,7 +819,8 @@ def gptq_kv4_append(k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
         pos_ptr, table_ptr = positions.data_ptr(), cos_sin.data_ptr()
     kval = vval = None
     if values:
-        kval, vval = k.new_empty((2, T, hkv, D), dtype=torch.float16).unbind(0)
+        kval = k.new_empty((T, hkv, D), dtype=torch.float16)
+        vval = torch.empty_like(kval)
     _call("gptq_kv4_append", dev, _addr(q), qs, k.data_ptr(), ks, v.data_ptr(), vs, dt, T, hq, hkv,
           D, pos_ptr, slots.data_ptr(), table_ptr, n_pos, rot, bool(interleaved),
           cache.group_size, cache.pages, cache.page_size, cache.k_codes.data_ptr(),
