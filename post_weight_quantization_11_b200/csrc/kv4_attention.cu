@@ -54,6 +54,8 @@ struct KvAttn {
     const int32_t* start;
     float scale;                           // times log2(e)
     int chunk, splits, row_tiles;
+    int grp;                               // query heads per key head
+    uint32_t grp_mul;                      // ceil(2^32 / grp): r / grp = r grp_mul >> 32 for r grp < 2^32
     float* part;                           // unit x 8 rows x (D, then maximum and sum)
     __half* out;
 };
@@ -94,6 +96,19 @@ __device__ __forceinline__ void kv_bulk(uint32_t dst, const void* src, uint32_t 
         : "memory");
 }
 
+// Query of a row, whose head is the rest (rows are at most 8 x 65535)
+__device__ __forceinline__ int kv_query(const KvAttn& p, int r)
+{
+    return p.grp == 1 ? r : int(__umulhi(uint32_t(r), p.grp_mul));
+}
+
+// Place of row r of a sequence in q and out: elements from the sequence's first row on
+__device__ __forceinline__ int64_t kv_row(const KvAttn& p, int64_t s0, int hk, int r)
+{
+    const int i = kv_query(p, r);
+    return (s0 + i) * p.hq + hk * p.grp + (r - i * p.grp);
+}
+
 // What a row tile of a sequence sees
 struct KvSpan {
     bool ok;                               // the sequence's range and length are valid
@@ -109,10 +124,9 @@ __device__ __forceinline__ KvSpan kv_span(const KvAttn& p, int b, int rt)
     s.s0 = s0;
     s.n = int(s1 - s0);
     s.L = int(L);
-    const int grp = p.hq / p.hkv;
-    s.rows = s.n * grp - rt * 8;           // from the tile's first row on
+    s.rows = s.n * p.grp - rt * 8;         // from the tile's first row on
     if (!s.ok || s.rows <= 0) { s.rows = s.lo = s.base = s.hi = 0; return s; }
-    const int i0 = rt * 8 / grp, i1 = (rt * 8 + min(s.rows, 8) - 1) / grp;
+    const int i0 = kv_query(p, rt * 8), i1 = kv_query(p, rt * 8 + min(s.rows, 8) - 1);
     s.hi = max(0, s.L - s.n + i1 + 1);
     const int64_t lo = p.window > 0 ? int64_t(s.L) - s.n + i0 + 1 - p.window : 0;
     s.lo = int(max(lo, int64_t(0)));
@@ -144,7 +158,6 @@ __global__ void __launch_bounds__(KV_WARPS * 32, KvShape<D, G>::CTAS) kv4_attent
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int warp = __shfl_sync(ALL, threadIdx.x >> 5, 0);
     const int b = blockIdx.z, hk = blockIdx.y / p.row_tiles, rt = blockIdx.y - hk * p.row_tiles;
-    const int grp = p.hq / p.hkv;
     const KvSpan sp = kv_span(p, b, rt);
     if (!sp.ok) {
         if (threadIdx.x == 0) atomicCAS(&g_device_status, 0, kErrIndex);
@@ -211,9 +224,8 @@ __global__ void __launch_bounds__(KV_WARPS * 32, KvShape<D, G>::CTAS) kv4_attent
     // order of a word's nibbles) and the sums over each group
     uint32_t qf[NB][4];
     {
-        const int r = rt * 8 + g;
         const bool on = g < sp.rows;
-        const __half* src = p.q + ((sp.s0 + (on ? r / grp : 0)) * p.hq + hk * grp + (on ? r % grp : 0)) * D;
+        const __half* src = p.q + kv_row(p, sp.s0, hk, rt * 8 + (on ? g : 0)) * D;
         float qs[G] = {};
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
@@ -243,12 +255,12 @@ __global__ void __launch_bounds__(KV_WARPS * 32, KvShape<D, G>::CTAS) kv4_attent
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const int r = rt * 8 + min(2 * t + j, sp.rows - 1);
-        lim[j] = sp.L - sp.n + r / grp + 1;
+        lim[j] = sp.L - sp.n + kv_query(p, r) + 1;
         const int64_t lo = p.window > 0 ? int64_t(lim[j]) - p.window : 0;
         from[j] = int(max(lo, int64_t(0)));
     }
-    const int all_lim = sp.L - sp.n + rt * 8 / grp + 1;    // keys [all_from, all_lim): seen by every row
-    const int last = sp.L - sp.n + (rt * 8 + min(sp.rows, 8) - 1) / grp + 1;
+    const int all_lim = sp.L - sp.n + kv_query(p, rt * 8) + 1;    // keys [all_from, all_lim): seen by every row
+    const int last = sp.L - sp.n + kv_query(p, rt * 8 + min(sp.rows, 8) - 1) + 1;
     const int all_from = p.window > 0 ? int(max(int64_t(last) - p.window, int64_t(0))) : 0;
 
     float m[2] = {KV_NONE, KV_NONE}, l[2] = {0.f, 0.f}, zs[G][2] = {};
@@ -480,25 +492,40 @@ __global__ void __launch_bounds__(KV_WARPS * 32, KvShape<D, G>::CTAS) kv4_attent
     __syncthreads();
     const int rows = min(sp.rows, 8);
     const int64_t unit = (int64_t(b) * gridDim.y + blockIdx.y) * p.splits + blockIdx.x;
-    for (int e = threadIdx.x; e < rows * D; e += KV_WARPS * 32) {
-        const int r = e / D, d = e - r * D;
-        float top = KV_NONE, sum = 0.f, v = 0.f;
+    float* dst = p.part + unit * (8 * (D + 2));
+    if (threadIdx.x < rows) {                              // the warps' weights in row r
+        const int r = threadIdx.x;
+        float top = KV_NONE, sum = 0.f, c[KV_WARPS];
 #pragma unroll
         for (int w = 0; w < KV_WARPS; ++w) top = fmaxf(top, wm[w][r]);
 #pragma unroll
+        for (int w = 0; w < KV_WARPS; ++w) {               // (a warp without keys: its sums are 0)
+            c[w] = ex2(wm[w][r] - top);
+            sum = fmaf(c[w], wl[w][r], sum);
+        }
+        if (p.splits > 1) { dst[8 * D + r] = top; dst[8 * D + 8 + r] = sum; }
+        const float scale = p.splits > 1 ? 1.f : sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+        for (int w = 0; w < KV_WARPS; ++w) wm[w][r] = c[w] * scale;
+    }
+    __syncthreads();
+    for (int e = threadIdx.x * 4; e < rows * D; e += KV_WARPS * 32 * 4) {
+        const int r = e / D, d = e - r * D;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
         for (int w = 0; w < KV_WARPS; ++w) {
-            const float c = ex2(wm[w][r] - top);           // (a warp without keys: sum and v are 0)
-            sum = fmaf(c, wl[w][r], sum);
-            v = fmaf(c, reinterpret_cast<const float*>(smem)[w * (8 * D) + e], v);
+            const float c = wm[w][r];
+            const float4 u = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem) +
+                                                              w * (8 * D) + e);
+            v.x = fmaf(c, u.x, v.x); v.y = fmaf(c, u.y, v.y);
+            v.z = fmaf(c, u.z, v.z); v.w = fmaf(c, u.w, v.w);
         }
         if (p.splits == 1) {
-            const int rr = rt * 8 + r;
-            p.out[((sp.s0 + rr / grp) * p.hq + hk * grp + rr % grp) * D + d] =
-                __float2half_rn(sum > 0.f ? v / sum : 0.f);
+            alignas(8) const __half2 h[2] = {__floats2half2_rn(v.x, v.y), __floats2half2_rn(v.z, v.w)};
+            *reinterpret_cast<uint2*>(p.out + kv_row(p, sp.s0, hk, rt * 8 + r) * D + d) =
+                *reinterpret_cast<const uint2*>(h);
         } else {
-            float* dst = p.part + unit * (8 * (D + 2));
-            dst[e] = v;
-            if (d == 0) { dst[8 * D + r] = top; dst[8 * D + 8 + r] = sum; }
+            *reinterpret_cast<float4*>(dst + e) = v;
         }
     }
 }
@@ -510,7 +537,6 @@ template <int D> __global__ void __launch_bounds__(256) kv4_join_kernel(const Kv
     pdl_wait();
     const int lane = threadIdx.x & 31, r = threadIdx.x >> 5;
     const int b = blockIdx.y, hk = blockIdx.x / p.row_tiles, rt = blockIdx.x - hk * p.row_tiles;
-    const int grp = p.hq / p.hkv;
     const KvSpan sp = kv_span(p, b, rt);
     if (!sp.ok || r >= sp.rows) return;
     const int n = sp.hi > sp.base ? (sp.hi - sp.base + p.chunk - 1) / p.chunk : 0;
@@ -527,8 +553,7 @@ template <int D> __global__ void __launch_bounds__(256) kv4_join_kernel(const Kv
 #pragma unroll
         for (int e = 0; e < E; ++e) v[e] = fmaf(c, src[r * D + e * 32 + lane], v[e]);
     }
-    const int rr = rt * 8 + r;
-    __half* dst = p.out + ((sp.s0 + rr / grp) * p.hq + hk * grp + rr % grp) * D;
+    __half* dst = p.out + kv_row(p, sp.s0, hk, rt * 8 + r) * D;
 #pragma unroll
     for (int e = 0; e < E; ++e) dst[e * 32 + lane] = __float2half_rn(sum > 0.f ? v[e] / sum : 0.f);
 }
@@ -621,6 +646,8 @@ extern "C" int gptq_kv4_attention(const uint16_t* q, int64_t tokens, int64_t seq
     p.tokens = tokens; p.seqs = seqs; p.pages = pages; p.width = table_width;
     p.window = window; p.max_q = (int)max_q; p.max_len = (int)max_seq_len;
     p.hq = q_heads; p.hkv = kv_heads;
+    p.grp = q_heads / kv_heads;
+    p.grp_mul = uint32_t(((uint64_t(1) << 32) + p.grp - 1) / p.grp);
     while ((1 << p.page_shift) < page_size) ++p.page_shift;
     p.kc = k_codes; p.kp = reinterpret_cast<const __half2*>(k_params);
     p.vc = v_codes; p.vp = reinterpret_cast<const __half2*>(v_params);
