@@ -29,9 +29,9 @@
 //  * x is staged once per CTA in operand order: 16 bytes hold the eight columns
 //    of one packed word for one n, so one LDS.128 feeds two products; the order
 //    within the eight is the nibbles' pairing above.
-// Groups that are a multiple of 128 columns (WIDE) fold once a step; smaller
-// ones fold every 32 columns, for which a lane takes words of a row that are 16
-// bytes apart, so that a product stays inside 32 columns.
+// The scales are applied every 32 FOLD columns: once a step for groups that are a
+// multiple of 128 columns (FOLD = 4); for a multiple of 64 or 32 (2, 1) a lane takes
+// words of a row that are 16 bytes apart, so that a product stays inside 32 columns.
 // SPLIT: x in two fp16 parts (22 bits) for fp32 activations, scaled by a power
 // of two per column: W4_TWICE: each read of the rows is multiplied with both;
 // W4_BESIDE: up to four columns, the second parts are operand columns 4 .. 7 (half
@@ -126,6 +126,9 @@ inline W4Group w4_group(int64_t g)
     return W4Group{((1u << 22) + n - 1) / n};
 }
 
+// Blocks of 32 columns that share a scale, at most a step
+inline int w4_fold(int64_t g) { return g % 128 == 0 ? 4 : g % 64 == 0 ? 2 : 1; }
+
 // One packed layer
 struct W4Layer {
     const uint32_t* qw;
@@ -179,9 +182,9 @@ __device__ __forceinline__ uint32_t w4_param(uint32_t s, uint32_t z, uint32_t sh
 }
 
 // Staged activations: chunk ((step 4 + w) cols + n) 4 + t of 16 bytes holds, for
-// column n, the columns 128 step + 32 t + 8 w .. (WIDE) or 128 step + 32 w + 8 t ..
+// column n, the columns 128 step + 32 t + 8 w .. (FOLD 4) or 128 step + 32 w + 8 t ..
 // in the order 0 4 2 6 1 5 3 7; SPLIT: a second plane behind the first.  xs: 2^-14
-// times the sums of a step's 128 (WIDE) or 32 columns, 8 NT floats each.  Lanes of
+// times the sums of 32 FOLD columns each, 8 NT floats.  Lanes of
 // columns behind cols read another column; their results are not used.
 struct W4Stage {
     uint32_t x, xs;        // shared addresses
@@ -199,12 +202,12 @@ template <bool PAIR> __host__ __device__ constexpr int w4_row(int m, int i)
     return PAIR ? i * 16 + m * 8 : m * 16 + i * 8;
 }
 
-// y += 2^-14 times the step's product.  slot: shared address of the lane's row; WIDE:
+// y += 2^-14 times the step's product.  slot: shared address of the lane's row; FOLD 4:
 // of its part t of the step, else of word t of the row.  u: the step of the slot.  p: w4_param of
 // the lane's rows, held by lane t of the quad for (WIDE) step src of four or
 // (otherwise) block t of this step.
 // x[c]: shared address of the lane's part of operand column 8 c + g.
-template <int NT, bool WIDE, int SPLIT, bool PAIR>
+template <int NT, int FOLD, int SPLIT, bool PAIR>
 __device__ __forceinline__ void w4_step(float (&y)[NT][2][4], uint32_t slot, int u,
                                         const uint32_t (&p)[2][2], int src, uint32_t (&x)[NT],
                                         uint32_t xs, uint32_t xw, uint32_t plane)
@@ -216,7 +219,7 @@ __device__ __forceinline__ void w4_step(float (&y)[NT][2][4], uint32_t slot, int
     for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            if constexpr (WIDE) {
+            if constexpr (FOLD == 4) {
                 const uint4 v = lds16(slot + w4_row<PAIR>(m, i) * 128);
                 q[m][i][0] = v.x; q[m][i][1] = v.y; q[m][i][2] = v.z; q[m][i][3] = v.w;
             } else {
@@ -243,7 +246,7 @@ __device__ __forceinline__ void w4_step(float (&y)[NT][2][4], uint32_t slot, int
                 const uint4 f = lds16(h ? x[c] + plane : x[c]);
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
-                    if (h == 0 && (!WIDE || w == 0)) {
+                    if (h == 0 && w % FOLD == 0) {
                         mma_16816_first(lo[c][m], a[m][0], a[m][1], a[m][2], a[m][3], f.x, f.y);
                         mma_16816_first(hi[c][m], b[m][0], b[m][1], b[m][2], b[m][3], f.z, f.w);
                     } else {
@@ -254,18 +257,18 @@ __device__ __forceinline__ void w4_step(float (&y)[NT][2][4], uint32_t slot, int
             }
             x[c] += xw;
         }
-        if (!WIDE || w == 3) {
+        if (w % FOLD == FOLD - 1) {
             float2 sz[2][2];
 #pragma unroll
             for (int m = 0; m < 2; ++m)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const uint32_t v = __shfl_sync(0xffffffffu, p[m][i], WIDE ? src : w, 4);
+                    const uint32_t v = __shfl_sync(0xffffffffu, p[m][i], src + w / FOLD, 4);
                     sz[m][i] = __half22float2(*reinterpret_cast<const __half2*>(&v));
                 }
 #pragma unroll
             for (int c = 0; c < NT; ++c) {
-                const float2 k = lds_f2(xs + ((WIDE ? 0 : w) * NT + c) * (W4_COLS * 4));
+                const float2 k = lds_f2(xs + (w / FOLD * NT + c) * (W4_COLS * 4));
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -280,10 +283,10 @@ __device__ __forceinline__ void w4_step(float (&y)[NT][2][4], uint32_t slot, int
 }
 
 // Where the chunk of the columns 8 kc .. of column n goes
-template <bool WIDE> __device__ __forceinline__ int w4_chunk(int kc, int n, int cols)
+template <int FOLD> __device__ __forceinline__ int w4_chunk(int kc, int n, int cols)
 {
     const int step = kc >> 4, hi = (kc >> 2) & 3, lo = kc & 3;
-    const int w = WIDE ? lo : hi, t = WIDE ? hi : lo;
+    const int w = FOLD == 4 ? lo : hi, t = FOLD == 4 ? hi : lo;
     return ((step * 4 + w) * cols + n) * 4 + t;
 }
 
@@ -297,22 +300,18 @@ __device__ __forceinline__ uint4 w4_order(const __half (&h)[8])
     return make_uint4(pack2(h[0], h[4]), pack2(h[2], h[6]), pack2(h[1], h[5]), pack2(h[3], h[7]));
 }
 
-// The sums of x over 32 (or 128, WIDE) columns from each lane's sum over 8; lanes
+// The sums of x over 32 FOLD columns from each lane's sum over 8; lanes
 // hold consecutive chunks, 16 to a step
-template <bool WIDE> __device__ __forceinline__ float w4_join(float s)
+template <int FOLD> __device__ __forceinline__ float w4_join(float s)
 {
-    s += __shfl_xor_sync(0xffffffffu, s, 1);
-    s += __shfl_xor_sync(0xffffffffu, s, 2);
-    if constexpr (WIDE) {
-        s += __shfl_xor_sync(0xffffffffu, s, 4);
-        s += __shfl_xor_sync(0xffffffffu, s, 8);
-    }
+#pragma unroll
+    for (int o = 1; o < 4 * FOLD; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     return s;
 }
 
 // Stages columns [k0, k0 + 128 steps) of `cols` fp16 rows (row(n): its first
 // element), through perm when given.  All threads; ends without a barrier.
-template <int NT, bool WIDE, class Row>
+template <int NT, int FOLD, class Row>
 __device__ __forceinline__ void w4_stage_half(uint4* x, float* xs, Row row, const int32_t* perm,
                                               int k0, int steps, int cols, int d)
 {
@@ -341,10 +340,10 @@ __device__ __forceinline__ void w4_stage_half(uint4* x, float* xs, Row row, cons
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) s += __half2float(h[j]);
-            x[w4_chunk<WIDE>(kc, n, cols)] = w4_order(h);
+            x[w4_chunk<FOLD>(kc, n, cols)] = w4_order(h);
         }
-        s = w4_join<WIDE>(s);
-        if (on && kc % (WIDE ? 16 : 4) == 0) xs[(kc / (WIDE ? 16 : 4)) * XS + n] = s * 0x1p-14f;
+        s = w4_join<FOLD>(s);
+        if (on && kc % (4 * FOLD) == 0) xs[(kc / (4 * FOLD)) * XS + n] = s * 0x1p-14f;
     }
 }
 
@@ -352,7 +351,7 @@ __device__ __forceinline__ void w4_stage_half(uint4* x, float* xs, Row row, cons
 // brings its largest magnitude to 2^14 .. 2^15 (undo[n]: its inverse; a column
 // with an infinity or NaN is not scaled).  top: 8 NT words of scratch.  Holds
 // barriers; ends without one.
-template <int NT, bool WIDE, class Row>
+template <int NT, int FOLD, class Row>
 __device__ __forceinline__ void w4_stage_split(uint4* x, float* xs, float* undo, uint32_t* top,
                                                Row row, const int32_t* perm, int k0, int steps,
                                                int cols, int d, bool beside)
@@ -419,14 +418,14 @@ __device__ __forceinline__ void w4_stage_split(uint4* x, float* xs, float* undo,
                 s += __half2float(h[j]);
                 s2 += __half2float(l[j]);
             }
-            const int at = w4_chunk<WIDE>(kc, n, cols);
+            const int at = w4_chunk<FOLD>(kc, n, cols);
             x[at] = w4_order(h);
             x[at + cols * nch] = w4_order(l);
         }
-        s = w4_join<WIDE>(s);
-        s2 = w4_join<WIDE>(s2);
-        if (on && kc % (WIDE ? 16 : 4) == 0) {
-            float* to = xs + (kc / (WIDE ? 16 : 4)) * XS + n;
+        s = w4_join<FOLD>(s);
+        s2 = w4_join<FOLD>(s2);
+        if (on && kc % (4 * FOLD) == 0) {
+            float* to = xs + (kc / (4 * FOLD)) * XS + n;
             to[0] = (beside ? s : s + s2) * 0x1p-14f;
             if (beside) to[4] = s2 * 0x1p-14f;
         }
@@ -444,14 +443,14 @@ inline __host__ __device__ size_t w4_x_bytes(int steps, int cols, bool split)
 {
     return size_t(steps) * 256 * cols * (split ? 2 : 1);
 }
-inline __host__ __device__ size_t w4_xs_bytes(int steps, int nt, bool wide)
+inline __host__ __device__ size_t w4_xs_bytes(int steps, int nt, int fold)
 {
-    return size_t(steps) * (wide ? 1 : 4) * W4_COLS * nt * 4;
+    return size_t(steps) * (4 / fold) * W4_COLS * nt * 4;
 }
 // (and up to 1023 bytes in front, for the alignment of the ring)
-inline size_t w4_smem(int steps, int cols, int nt, bool wide, bool split)
+inline size_t w4_smem(int steps, int cols, int nt, int fold, bool split)
 {
-    return 1024 + w4_at_x(nt) + w4_x_bytes(steps, cols, split) + w4_xs_bytes(steps, nt, wide);
+    return 1024 + w4_at_x(nt) + w4_x_bytes(steps, cols, split) + w4_xs_bytes(steps, nt, fold);
 }
 
 // The packed rows as a TMA tensor, in boxes of `rows` rows and two steps
@@ -538,7 +537,7 @@ static __device__ __noinline__ void w4_wait_long(uint32_t bar, uint32_t parity, 
 //   done(group, r, n, v): the joined result of row r of the group (PAIR: of the
 //            group's gate rows), column n; PAIR: done(group, r, n, v, v2) with the up
 //            row's.
-template <int NT, int KW, bool WIDE, int SPLIT, bool PAIR, class StageF, class DoneF>
+template <int NT, int KW, int FOLD, int SPLIT, bool PAIR, class StageF, class DoneF>
 __device__ __forceinline__ void w4_sweep(W4Pipe& pipe, const CUtensorMap* tm, const W4Layer& l,
                                          int64_t row0, int64_t end, uint32_t pair,
                                          const W4Stage& st, int groups, int k0, int steps,
@@ -578,13 +577,14 @@ __device__ __forceinline__ void w4_sweep(W4Pipe& pipe, const CUtensorMap* tm, co
     static_assert(W4_RING == 2, "pipe.put and get");
     issue();
     issue();
-    // scales and zero points: WIDE: of four steps at a time (lane t those of step
-    // t), four steps ahead; else of block t of a step, one step ahead
+    // scales and zero points of FOLD steps at a time, as many steps ahead: PER groups a
+    // step, lane t of a quad those of group t % PER of step t / PER
+    constexpr int PER = 4 / FOLD;
     const uint8_t* sc = reinterpret_cast<const uint8_t*>(l.sc) + row0 * (l.G * 2);
     const uint8_t* qz = l.qz + row0 * l.Gb;
     const uint32_t last = uint32_t(end - row0 - 1);
     auto params = [&](W4Raw& p, int grp, int j) {
-        const uint32_t block = (first_step + min(j + (WIDE ? t : 0), n - 1)) * 4 + (WIDE ? 0 : t);
+        const uint32_t block = (first_step + min(j + t / PER, n - 1)) * 4 + (t % PER) * FOLD;
         const uint32_t at = (block * l.grp.mul) >> 22;
         const uint32_t first = (grp * RW + rw) * ROWS + w4_rho(g);
         p.shift = 4 * (at & 1);
@@ -600,7 +600,6 @@ __device__ __forceinline__ void w4_sweep(W4Pipe& pipe, const CUtensorMap* tm, co
                 p.z[m][i] = ld_nc_u8(qz + (r * gz + (at >> 1)));
             }
     };
-    constexpr int EVERY = WIDE ? 4 : 1;
     uint32_t par[2][2] = {};
     W4Raw ahead{};
     if (n) params(ahead, 0, 0);
@@ -611,8 +610,8 @@ __device__ __forceinline__ void w4_sweep(W4Pipe& pipe, const CUtensorMap* tm, co
     for (int c = 0; c < NT; ++c)
         x0[c] = st.x + (min(SPLIT == W4_BESIDE ? g & 3 : c * 8 + g, st.cols - 1) * 4 + t) * 16 +
                 s0 * 4 * xw + (SPLIT == W4_BESIDE && g >= 4 ? st.plane : 0u);
-    const uint32_t xs0 = st.xs + s0 * (WIDE ? 1 : 4) * W4_COLS * NT * 4 + t * 8;
-    const uint32_t from = pipe.ring + w4_rho(g) * 128 + (WIDE ? (t ^ w4_rho(g)) * 16 : t * 4);
+    const uint32_t xs0 = st.xs + s0 * PER * W4_COLS * NT * 4 + t * 8;
+    const uint32_t from = pipe.ring + w4_rho(g) * 128 + (FOLD == 4 ? (t ^ w4_rho(g)) * 16 : t * 4);
     const uint32_t red = pipe.red + (warp * 32 + lane) * 4;
     for (int grp = 0; grp < groups; ++grp) {
         float y[NT][2][4] = {};
@@ -630,18 +629,18 @@ __device__ __forceinline__ void w4_sweep(W4Pipe& pipe, const CUtensorMap* tm, co
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
                         par[m][i] = w4_param(ahead.s[m][i], ahead.z[m][i], ahead.shift);
-                if (jj + EVERY < n) params(ahead, grp, jj + EVERY);
+                if (jj + FOLD < n) params(ahead, grp, jj + FOLD);
                 else params(ahead, min(grp + 1, groups - 1), 0);
             };
             auto step = [&](int u) {
-                w4_step<NT, WIDE, SPLIT, PAIR>(y, WIDE ? slot ^ (64 * u) : slot, u, par, (j & 2) + u, x,
-                                               xs, xw, st.plane);
-                xs += (WIDE ? 1 : 4) * W4_COLS * NT * 4;
+                w4_step<NT, FOLD, SPLIT, PAIR>(y, FOLD == 4 ? slot ^ (64 * u) : slot, u, par,
+                                               (((j & 2) + u) % FOLD) * PER, x, xs, xw, st.plane);
+                xs += PER * W4_COLS * NT * 4;
             };
-            if (!WIDE || (j & 2) == 0) next_params(j);
+            if (FOLD < 4 || (j & 2) == 0) next_params(j);
             step(0);
             if (j + 1 < n) {
-                if (!WIDE) next_params(j + 1);
+                if (FOLD == 1) next_params(j + 1);
                 step(1);
             }
             pipe.phase ^= pipe.get;

@@ -157,7 +157,7 @@ __device__ __forceinline__ void lora_shrink_few(const LoraParams& p)
     }
 }
 
-template <int NT, bool WIDE>
+template <int NT, int FOLD>
 __global__ void __launch_bounds__(W4_THREADS, 1)
 lora_product_kernel(const __grid_constant__ CUtensorMap tm, const LoraParams p)
 {
@@ -184,7 +184,7 @@ lora_product_kernel(const __grid_constant__ CUtensorMap tm, const LoraParams p)
         const int64_t b0 = int64_t(c) * p.chunk;
         const int cols = int(min(int64_t(p.chunk), p.batch - b0));
         const W4Stage st{smem_u32(x), smem_u32(xs), cols, 0u};
-        w4_sweep<NT, LORA_KW, WIDE, W4_WHOLE, false>(
+        w4_sweep<NT, LORA_KW, FOLD, W4_WHOLE, false>(
             pipe, &tm, p.lay, int64_t(g0) * LORA_ROWS, p.m, 0u, st, g1 - g0, k0, steps,
             [&]() {
                 if (!shrunk) {                             // beside the first copies
@@ -193,7 +193,7 @@ lora_product_kernel(const __grid_constant__ CUtensorMap tm, const LoraParams p)
                     shrunk = true;
                 }
                 const __half* src = p.xp ? p.xp : p.x;
-                w4_stage_half<NT, WIDE>(x, xs, [&](int n) { return src + (b0 + n) * p.d; }, nullptr,
+                w4_stage_half<NT, FOLD>(x, xs, [&](int n) { return src + (b0 + n) * p.d; }, nullptr,
                                         k0 * W4_STEP, steps, cols, int(p.d));
                 __syncthreads();
             },
@@ -409,15 +409,18 @@ extern "C" int gptq_w4a16_lora(const uint16_t* x, int64_t batch, const uint32_t*
     } else {
         CUtensorMap tm;
         if (w4_tmap(&tm, qweight, d_out, d_in, 32) != GPTQ_OK) return GPTQ_ERR_CUDA;
-        const bool wide = g % W4_STEP == 0;
-        const size_t smem = w4_smem(plan.slice, plan.chunk, plan.nt, wide, false);
+        const int fold = w4_fold(g);
+        const size_t smem = w4_smem(plan.slice, plan.chunk, plan.nt, fold, false);
         if (smem > W4_MAX_SMEM) return GPTQ_ERR_SHAPE;
-        auto kern = plan.nt == 1
-                        ? (wide ? lora_product_kernel<1, true> : lora_product_kernel<1, false>)
-                        : (wide ? lora_product_kernel<2, true> : lora_product_kernel<2, false>);
-        static std::atomic<bool> done[4][64];
+        auto kern = plan.nt == 1 ? (fold == 4   ? lora_product_kernel<1, 4>
+                                    : fold == 2 ? lora_product_kernel<1, 2>
+                                                : lora_product_kernel<1, 1>)
+                                 : (fold == 4   ? lora_product_kernel<2, 4>
+                                    : fold == 2 ? lora_product_kernel<2, 2>
+                                                : lora_product_kernel<2, 1>);
+        static std::atomic<bool> done[10][64];
         if (!smem_opt_in(reinterpret_cast<const void*>(kern), W4_MAX_SMEM,
-                         done[(plan.nt - 1) * 2 + (wide ? 1 : 0)]))
+                         done[(plan.nt - 1) * 5 + fold]))
             return GPTQ_ERR_CUDA;
         const int64_t units = int64_t(plan.chunks) * plan.slices * plan.groups;
         const unsigned grid = (unsigned)std::min<int64_t>(device_sm_count(), units);

@@ -167,7 +167,7 @@ __device__ __forceinline__ void moe_routes(const MoeParams& p, MoeRoutes& r, int
 // h = silu(G x) (U x) of every pair.  A row tile is 8 gate rows and the same 8
 // up rows, so that a lane holds both of an element of h.  The CTAs share the
 // row tiles of all chunks evenly; a CTA stages a chunk's tokens once.
-template <int KW, bool WIDE>
+template <int KW, int FOLD>
 __global__ void __launch_bounds__(W4_THREADS, 1) moe_in_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p)
 {
     extern __shared__ uint8_t smem_raw[];
@@ -196,11 +196,11 @@ __global__ void __launch_bounds__(W4_THREADS, 1) moe_in_kernel(const __grid_cons
         const int16_t* list = r.list + r.start[c];
         const int64_t row0 = int64_t(e) * 2 * p.f;
         const W4Stage st{smem_u32(x), smem_u32(xs), cols, 0};
-        w4_sweep<1, KW, WIDE, W4_WHOLE, true>(
+        w4_sweep<1, KW, FOLD, W4_WHOLE, true>(
             pipe, &tm, p.in, row0 + int64_t(g0) * kMoeInRows<KW>, row0 + 2 * p.f, uint32_t(p.f), st,
             g1 - g0, 0, steps,
             [&]() {
-                w4_stage_half<1, WIDE>(
+                w4_stage_half<1, FOLD>(
                     x, xs, [&](int n) { return p.x + int64_t(list[n] / p.k) * p.d; },
                     p.pi ? p.pi + e * p.d : nullptr, 0, steps, cols, int(p.d));
                 __syncthreads();
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(W4_THREADS, 1) moe_in_kernel(const __grid_cons
 }
 
 // part[slice][pair] = D h over a slice of the columns
-template <bool WIDE>
+template <int FOLD>
 __global__ void __launch_bounds__(W4_THREADS, 1) moe_out_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p)
 {
     extern __shared__ uint8_t smem_raw[];
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(W4_THREADS, 1) moe_out_kernel(const __grid_con
         const int64_t row0 = int64_t(e) * p.d;
         const W4Stage st{smem_u32(x), smem_u32(xs), cols, uint32_t(steps * 256 * cols)};
         auto stage = [&]() {
-            w4_stage_split<1, WIDE>(
+            w4_stage_split<1, FOLD>(
                 x, xs, undo, top, [&](int n) { return p.h + int64_t(list[n]) * p.f; },
                 p.po ? p.po + e * p.f : nullptr, k0 * W4_STEP, steps, cols, int(p.f), cols <= 4);
             __syncthreads();
@@ -258,10 +258,10 @@ __global__ void __launch_bounds__(W4_THREADS, 1) moe_out_kernel(const __grid_con
         };
         const int64_t first = row0 + int64_t(g0) * MOE_OUT_ROWS;
         if (cols <= 4)
-            w4_sweep<1, MOE_OUT_KW, WIDE, W4_BESIDE, false>(pipe, &tm, p.out, first, row0 + p.d, 0u, st,
+            w4_sweep<1, MOE_OUT_KW, FOLD, W4_BESIDE, false>(pipe, &tm, p.out, first, row0 + p.d, 0u, st,
                                                             g1 - g0, k0, steps, stage, done);
         else
-            w4_sweep<1, MOE_OUT_KW, WIDE, W4_TWICE, false>(pipe, &tm, p.out, first, row0 + p.d, 0u, st,
+            w4_sweep<1, MOE_OUT_KW, FOLD, W4_TWICE, false>(pipe, &tm, p.out, first, row0 + p.d, 0u, st,
                                                            g1 - g0, k0, steps, stage, done);
         u += g1 - g0;
     }
@@ -313,8 +313,8 @@ MoePlan moe_plan(int64_t T, int64_t E, int k, int64_t d, int64_t f)
         if (cost < best * 0.97) { best = cost; m.slice = steps; }
     }
     m.slices = (so + m.slice - 1) / m.slice;
-    m.smem_in = w4_smem(si, m.chunk, 1, false, false);
-    m.smem_out = w4_smem(m.slice, m.chunk, 1, false, true);
+    m.smem_in = w4_smem(si, m.chunk, 1, 1, false);
+    m.smem_out = w4_smem(m.slice, m.chunk, 1, 1, true);
     const size_t pairs = size_t(T) * k;
     m.at_h = align_up(sizeof(MoeRoutes), 256);
     m.at_part = m.at_h + align_up(pairs * f * 4, 256);
@@ -388,13 +388,13 @@ extern "C" int gptq_w4a16_moe(const uint16_t* x, int64_t tokens, const float* lo
     const int64_t pairs = tokens * top_k;
     const int64_t chunks = std::max(std::min(pairs, n_experts), ceil_div(pairs, plan.chunk));
     const bool fine = chunks * (d_ff / kMoeInRows<4>) < 8 * sms;
-    const bool wi = gi % W4_STEP == 0;
-    auto in = fine ? (wi ? moe_in_kernel<8, true> : moe_in_kernel<8, false>)
-                   : (wi ? moe_in_kernel<4, true> : moe_in_kernel<4, false>);
-    auto out = go % W4_STEP == 0 ? moe_out_kernel<true> : moe_out_kernel<false>;
-    static std::atomic<bool> done[6][64];
-    if (!smem_opt_in(reinterpret_cast<const void*>(in), MOE_MAX_SMEM, done[2 * fine + wi]) ||
-        !smem_opt_in(reinterpret_cast<const void*>(out), MOE_MAX_SMEM, done[4 + (go % W4_STEP == 0)]))
+    const int fi = w4_fold(gi), fo = w4_fold(go);
+    auto in = fine ? (fi == 4 ? moe_in_kernel<8, 4> : fi == 2 ? moe_in_kernel<8, 2> : moe_in_kernel<8, 1>)
+                   : (fi == 4 ? moe_in_kernel<4, 4> : fi == 2 ? moe_in_kernel<4, 2> : moe_in_kernel<4, 1>);
+    auto out = fo == 4 ? moe_out_kernel<4> : fo == 2 ? moe_out_kernel<2> : moe_out_kernel<1>;
+    static std::atomic<bool> done[15][64];
+    if (!smem_opt_in(reinterpret_cast<const void*>(in), MOE_MAX_SMEM, done[5 * fine + fi]) ||
+        !smem_opt_in(reinterpret_cast<const void*>(out), MOE_MAX_SMEM, done[10 + fo]))
         return GPTQ_ERR_CUDA;
     CUtensorMap ti, to;
     if (w4_tmap(&ti, qweight_in, n_experts * 2 * d_ff, d_model, 16) != GPTQ_OK ||
