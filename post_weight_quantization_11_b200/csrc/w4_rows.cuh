@@ -204,8 +204,7 @@ template <bool PAIR> __host__ __device__ constexpr int w4_row(int m, int i)
 
 // y += 2^-14 times the step's product.  slot: shared address of the lane's row; FOLD 4:
 // of its part t of the step, else of word t of the row.  u: the step of the slot.  p: w4_param of
-// the lane's rows, held by lane t of the quad for (WIDE) step src of four or
-// (otherwise) block t of this step.
+// the lane's rows, of the groups of the step, held by lanes src on of the quad.
 // x[c]: shared address of the lane's part of operand column 8 c + g.
 template <int NT, int FOLD, int SPLIT, bool PAIR>
 __device__ __forceinline__ void w4_step(float (&y)[NT][2][4], uint32_t slot, int u,

@@ -18,7 +18,7 @@
 namespace gptq {
 
 constexpr int LORA_KW = 8, LORA_ROWS = 32 * (W4_WARPS / LORA_KW);   // of w4_sweep
-constexpr int LORA_JOIN = 2, LORA_JOIN_THREADS = 128;   // rows of x per thread of the join
+constexpr int LORA_JOIN = 4, LORA_JOIN_ROWS = 128;      // rows of x and of the layer per CTA of the join
 constexpr int LORA_SWEEP = 16;                   // most rows of x of the row sweep
 constexpr int LORA_MAX_RANK = 256;
 constexpr int LORA_SMS = 148;                    // the plan does not depend on the device that is current
@@ -240,28 +240,30 @@ __global__ void __launch_bounds__(W4_THREADS) lora_front_kernel(const LoraParams
     else lora_shrink_few(p);
 }
 
-// y[b][r] = sum of part over the slices + B_a[r] . t[b]; one row r and LORA_JOIN rows
-// of x per thread
-__global__ void __launch_bounds__(LORA_JOIN_THREADS) lora_join_kernel(const LoraParams p)
+// y[b][r] = sum of part over the slices + B_a[r] . t[b].  A CTA has 128 rows r and
+// LORA_JOIN rows b.  B_a is read whole lines at a time: a row's 16-byte chunks lie in
+// neighbouring lanes (LANES of them, a power of two), whose sums are joined by shuffles
+// and meet the slices' sums, one row r a thread, in shared memory (one thread per row of
+// B: 32 lines a load, 20 us against 8 for 93 rows of rank 64).
+template <int LANES> __global__ void __launch_bounds__(LORA_JOIN_ROWS) lora_join_kernel(const LoraParams p)
 {
     __shared__ float4 ts[LORA_JOIN][LORA_MAX_RANK / 4];
-    const int64_t r = int64_t(blockIdx.x) * LORA_JOIN_THREADS + threadIdx.x;
+    __shared__ float low[LORA_JOIN][LORA_JOIN_ROWS];
+    const int tid = threadIdx.x;
+    const int64_t r0 = int64_t(blockIdx.x) * LORA_JOIN_ROWS, r = r0 + tid;
     const int64_t b0 = int64_t(blockIdx.y) * LORA_JOIN;
-    const int rows = int(min(int64_t(LORA_JOIN), p.batch - b0));
+    const int rows = int(min(int64_t(LORA_JOIN), p.batch - b0)), chunks = p.rank / 8;
     int id[LORA_JOIN];
+    bool any = false;
 #pragma unroll
     for (int i = 0; i < LORA_JOIN; ++i) {
         id[i] = i < rows ? p.adapter[b0 + i] : -1;
         if (id[i] >= p.n) id[i] = -1;
+        any = any || id[i] >= 0;
     }
     pdl_wait();
-    for (int i = threadIdx.x; i < rows * (p.rank / 4); i += LORA_JOIN_THREADS)
-        ts[i / (p.rank / 4)][i % (p.rank / 4)] =
-            *reinterpret_cast<const float4*>(p.t + b0 * p.rank + int64_t(i) * 4);
-    __syncthreads();
-    if (r >= p.m) return;
     float y[LORA_JOIN] = {};
-    {
+    if (r < p.m) {
         const float* src = p.part + b0 * p.m + r;
         const int64_t slice = p.batch * p.m;
 #pragma unroll 4
@@ -270,30 +272,54 @@ __global__ void __launch_bounds__(LORA_JOIN_THREADS) lora_join_kernel(const Lora
             for (int i = 0; i < LORA_JOIN; ++i)
                 if (i < rows) y[i] += src[i * p.m];
     }
-#pragma unroll 2
-    for (int k = 0; k < p.rank; k += 8) {
-        uint4 bv[LORA_JOIN];
+    if (any) {                                             // (of the CTA)
+        for (int i = tid; i < rows * (p.rank / 4); i += LORA_JOIN_ROWS)
+            ts[i / (p.rank / 4)][i % (p.rank / 4)] =
+                *reinterpret_cast<const float4*>(p.t + b0 * p.rank + int64_t(i) * 4);
+        __syncthreads();
+        const int c0 = tid % LANES;
+#pragma unroll 4
+        for (int pass = 0; pass < LANES; ++pass) {
+            const int row = pass * (LORA_JOIN_ROWS / LANES) + tid / LANES;
+            const int64_t at = min(r0 + row, p.m - 1);
+            float v[LORA_JOIN] = {};
+            for (int c = c0; c < chunks; c += LANES) {
+                uint4 bv[LORA_JOIN];
+#pragma unroll
+                for (int i = 0; i < LORA_JOIN; ++i)        // all on their way before the first is used
+                    if (id[i] >= 0 && (i == 0 || id[i] != id[i - 1]))
+                        bv[i] = __ldg(reinterpret_cast<const uint4*>(
+                            p.b + (int64_t(id[i]) * p.m + at) * p.rank + c * 8));
+#pragma unroll
+                for (int i = 0; i < LORA_JOIN; ++i) {
+                    if (id[i] < 0) continue;
+                    if (i > 0 && id[i] == id[i - 1]) bv[i] = bv[i - 1];   // neighbours share the load
+                    const float4 t0 = ts[i][2 * c], t1 = ts[i][2 * c + 1];
+                    const __half2* h = reinterpret_cast<const __half2*>(&bv[i]);
+                    const float2 v0 = __half22float2(h[0]), v1 = __half22float2(h[1]);
+                    const float2 v2 = __half22float2(h[2]), v3 = __half22float2(h[3]);
+                    v[i] = fmaf(v0.x, t0.x, v[i]); v[i] = fmaf(v0.y, t0.y, v[i]);
+                    v[i] = fmaf(v1.x, t0.z, v[i]); v[i] = fmaf(v1.y, t0.w, v[i]);
+                    v[i] = fmaf(v2.x, t1.x, v[i]); v[i] = fmaf(v2.y, t1.y, v[i]);
+                    v[i] = fmaf(v3.x, t1.z, v[i]); v[i] = fmaf(v3.y, t1.w, v[i]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < LORA_JOIN; ++i) {
+#pragma unroll
+                for (int o = 1; o < LANES; o <<= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+                if (c0 == 0) low[i][row] = v[i];
+            }
+        }
+        __syncthreads();
 #pragma unroll
         for (int i = 0; i < LORA_JOIN; ++i)
-            bv[i] = id[i] < 0 ? make_uint4(0u, 0u, 0u, 0u)
-                              : __ldg(reinterpret_cast<const uint4*>(
-                                    p.b + (int64_t(id[i]) * p.m + r) * p.rank + k));
-#pragma unroll
-        for (int i = 0; i < LORA_JOIN; ++i) {
-            if (id[i] < 0) continue;
-            const float4 t0 = ts[i][k / 4], t1 = ts[i][k / 4 + 1];
-            const __half2* h = reinterpret_cast<const __half2*>(&bv[i]);
-            const float2 v0 = __half22float2(h[0]), v1 = __half22float2(h[1]);
-            const float2 v2 = __half22float2(h[2]), v3 = __half22float2(h[3]);
-            y[i] = fmaf(v0.x, t0.x, y[i]); y[i] = fmaf(v0.y, t0.y, y[i]);
-            y[i] = fmaf(v1.x, t0.z, y[i]); y[i] = fmaf(v1.y, t0.w, y[i]);
-            y[i] = fmaf(v2.x, t1.x, y[i]); y[i] = fmaf(v2.y, t1.y, y[i]);
-            y[i] = fmaf(v3.x, t1.z, y[i]); y[i] = fmaf(v3.y, t1.w, y[i]);
-        }
+            if (id[i] >= 0) y[i] += low[i][tid];
     }
+    if (r < p.m)
 #pragma unroll
-    for (int i = 0; i < LORA_JOIN; ++i)
-        if (i < rows) p.y[(b0 + i) * p.m + r] = y[i];
+        for (int i = 0; i < LORA_JOIN; ++i)
+            if (i < rows) p.y[(b0 + i) * p.m + r] = y[i];
 }
 
 struct LoraPlan {
@@ -433,10 +459,12 @@ extern "C" int gptq_w4a16_lora(const uint16_t* x, int64_t batch, const uint32_t*
         count_launches();
         if (launch_status() != GPTQ_OK) return GPTQ_ERR_CUDA;
     }
-    if (launch_after(lora_join_kernel,
-                     dim3((unsigned)ceil_div(d_out, LORA_JOIN_THREADS),
+    auto join = rank >= 64 ? lora_join_kernel<8> : rank >= 32 ? lora_join_kernel<4>
+              : rank >= 16 ? lora_join_kernel<2> : lora_join_kernel<1>;
+    if (launch_after(join,
+                     dim3((unsigned)ceil_div(d_out, LORA_JOIN_ROWS),
                           (unsigned)ceil_div(batch, LORA_JOIN)),
-                     LORA_JOIN_THREADS, 0, st, p) != cudaSuccess)
+                     LORA_JOIN_ROWS, 0, st, p) != cudaSuccess)
         return GPTQ_ERR_CUDA;
     count_launches();
     return launch_status();
