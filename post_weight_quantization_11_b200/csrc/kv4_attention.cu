@@ -594,7 +594,7 @@ extern "C" size_t gptq_kv4_attention_workspace_bytes(int64_t seqs, int q_heads, 
                                                      int64_t max_seq_len)
 {
     if (seqs <= 0 || q_heads <= 0 || kv_heads <= 0 || head_dim <= 0 || max_q_len <= 0 ||
-        max_seq_len <= 0)
+        max_seq_len < 0)
         return 0;
     if (seqs > 65535 || q_heads > 1024 || kv_heads > 1024 || q_heads % kv_heads != 0 || head_dim > 256 ||
         max_q_len > (int64_t(1) << 24) || max_seq_len > (int64_t(1) << 30))

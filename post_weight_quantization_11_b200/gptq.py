@@ -587,7 +587,8 @@ def _bad(t, name: str, dtype, index):
 
 def _on(t, name: str, dtype, index: int):
     """_need, and on the device with this index"""
-    if not (t.dtype is dtype and t.get_device() == index and t.is_contiguous()):
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and
+            t.is_contiguous()):
         _bad(t, name, dtype, index)
 
 
@@ -670,6 +671,7 @@ def gptq_w4a16_lora(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor
     _on(lora_b, "lora_b", torch.float16, dev)
     _on(adapter, "adapter", torch.int32, dev)
     _on(lora_scaling, "lora_scaling", torch.float32, dev)
+    _tensor(qweight, "qweight")
     b, d = x.shape
     m = qweight.shape[0]
     n, r = lora_a.shape[0], lora_a.shape[1]
@@ -707,6 +709,7 @@ def gptq_w4a16_moe(x: torch.Tensor, logits: torch.Tensor, qweight_in: torch.Tens
     dev = _tensor(x, "x")
     _on(x, "x", torch.float16, dev)
     _on(logits, "logits", torch.float32, dev)
+    _tensor(qweight_out, "qweight_out")
     T, d = x.shape
     E = logits.shape[1]
     f = qweight_out.shape[-1] * 8
@@ -766,8 +769,8 @@ class KV4Cache:
 
 def _rows(t, name: str, tokens: int, heads, head_dim: int, dtype, index: int):
     """A tokens x heads x head_dim tensor or view with dense rows: its token stride."""
-    if t.dtype is not dtype or t.get_device() != index:
-        raise ValueError(f"{name} must be {dtype} on cuda:{index}, got {t.dtype} on {t.device}")
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != index:
+        raise ValueError(f"{name} must be a {dtype} tensor on cuda:{index}")
     shape = t.shape
     if len(shape) != 3 or shape[0] != tokens or shape[2] != head_dim or \
             (heads is not None and shape[1] != heads):

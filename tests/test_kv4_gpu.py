@@ -241,6 +241,34 @@ def test_attention_rows_that_see_nothing():
     _attn_check(c, 1)
 
 
+def test_attention_of_no_keys_at_all():
+    """A bound of 0 keys: the workspace and the call still agree, rows are zero."""
+    c = _attn_case(14, [0, 0], [1, 1], 4, 2, 64, 16, 32)
+    assert not _attn_run(c, max_seq_len=0).any()
+    c["table"] = np.zeros((2, 0), np.int32)
+    assert not _attn_run(c).any()
+
+
+@pytest.mark.parametrize("hq,hkv", [(5, 5), (6, 2), (7, 1), (33, 3), (64, 1)])
+def test_attention_head_groups(hq, hkv):
+    """Groups of 1 .. 64 heads: rows that fill no tile, several tiles, many queries."""
+    _attn_check(_attn_case(hq, [200, 77], [1, 13], hq, hkv, 64, 16, 64), 33)
+    _attn_check(_attn_case(hq + 1, [1500], [3], hq, hkv, 128, 32, 64))
+
+
+def test_attention_of_a_smaller_batch_fits_the_workspace_of_the_bounds():
+    """One workspace for the bounds serves every smaller call."""
+    W = G.gptq_kv4_attention_workspace_bytes
+    most = W(40, 32, 8, 128, 4, 5000)
+    for B in (1, 2, 7, 8, 39):
+        for nq in (1, 4):
+            for L in (0, 1, 255, 256, 257, 4999):
+                assert W(B, 32, 8, 128, nq, L) <= most
+    ws = torch.empty(most, dtype=torch.uint8, device=DEV)
+    for lens in ([5000], [300, 299], [1000] * 9):
+        _attn_check(_attn_case(len(lens), lens, [1] * len(lens), 32, 8, 128, 16, 128), ws=ws)
+
+
 def test_attention_window_of_one_is_the_value():
     c = _attn_case(2, [70, 16], [2, 1], 8, 2, 128, 16, 64)
     got = _attn_check(c, 1)
@@ -374,6 +402,13 @@ def test_attention_refusals():
         _attn_run(dict(c, q=c["q"][:, :3]))                   # 3 heads on 2
     with pytest.raises(G.GptqError):
         _attn_run(dict(c, scale=float("nan")))
+    with pytest.raises(ValueError):
+        G.gptq_kv4_attention(c["q"], c["cache"], _t(c["table"]), _t(c["lens"]), _t(c["start"]), 1.0)
+    with pytest.raises(ValueError):
+        G.gptq_kv4_attention(_t(c["q"]), c["cache"], _t(c["table"]), c["lens"], _t(c["start"]), 1.0)
+    with pytest.raises(ValueError):
+        G.gptq_kv4_attention(_t(c["q"]).cpu(), c["cache"], _t(c["table"]), _t(c["lens"]),
+                             _t(c["start"]), 1.0)
     with pytest.raises(ValueError):
         _attn_run(dict(c, q=c["q"].astype(np.float32)))
     with pytest.raises(ValueError):

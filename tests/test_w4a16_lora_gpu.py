@@ -49,7 +49,9 @@ SHAPES = [(1, 64, 128, 32, 8, 1, False), (1, 301, 256, 128, 16, 3, True),
           (8, 129, 14336, 128, 16, 8, True), (9, 50, 640, 32, 40, 3, False),
           (17, 260, 1024, 64, 8, 4, True), (33, 64, 4224, 128, 128, 3, False),
           (64, 100, 512, 512, 256, 2, False), (93, 143, 768, 128, 16, 30, True),
-          (200, 257, 896, 64, 16, 7, False), (300, 40, 256, 32, 8, 2, True)]
+          (200, 257, 896, 64, 16, 7, False), (300, 40, 256, 32, 8, 2, True),
+          (16, 200, 5632, 64, 16, 5, True), (12, 65, 32768, 128, 8, 2, False),
+          (40, 63, 960 * 2, 96, 24, 4, True), (20, 4100, 256, 64, 48, 3, True)]
 
 
 @pytest.mark.parametrize("T,m,d,g,r,n,act", SHAPES)
@@ -159,6 +161,10 @@ def test_refusals():
         _run(x, lay, a, b, sc, ids[:1])
     with pytest.raises(ValueError):
         _run(x, dict(lay, g=32), a, b, sc, ids)               # scales of other groups
+    with pytest.raises(ValueError):
+        G.gptq_w4a16_lora(_t(x), None, _t(lay["sc"]), _t(lay["qz"]), _t(a), _t(b), _t(ids), _t(sc), 64)
+    with pytest.raises(ValueError):
+        G.gptq_w4a16_lora(x, _t(lay["qw"]), _t(lay["sc"]), _t(lay["qz"]), _t(a), _t(b), _t(ids), _t(sc), 64)
     with pytest.raises(G.GptqError):
         _run(x, lay, a[:, :4], b[:, :, :4], sc, ids)          # rank 4
     with pytest.raises(G.GptqError):

@@ -48,7 +48,9 @@ def _check(c):
     (8, 3, 2, 4096, 256, 128, False, True), (9, 2, 2, 256, 4352, 32, False, True),
     (16, 6, 2, 640, 512, 128, True, True), (24, 8, 2, 512, 768, 128, False, True),
     (33, 2, 1, 256, 256, 64, False, True), (41, 64, 8, 256, 128, 32, False, True),
-    (64, 4, 3, 384, 512, 128, True, False), (64, 256, 8, 128, 128, 128, False, True)])
+    (64, 4, 3, 384, 512, 128, True, False), (64, 256, 8, 128, 128, 128, False, True),
+    (5, 3, 2, 640, 384, 32, True, True), (4, 2, 2, 256, 640, 64, False, False),
+    (1, 2, 1, 20480, 128, 32, False, True), (8, 1, 1, 12288, 256, 128, False, True)])
 def test_against_the_definition(T, E, k, d, f, g, act, renorm):
     _check(_case(300 + T + d, T, E, k, d, f, g, act, renorm))
 
@@ -191,6 +193,9 @@ def test_refusals():
         _run(c[0][:, :128].copy(), *c[1:])
     with pytest.raises(G.GptqError):
         _run(*c, ws=torch.empty(64, dtype=torch.uint8, device=DEV))
+    with pytest.raises(ValueError):
+        G.gptq_w4a16_moe(
+            _t(c[0]), None, *[_t(c[i][k]) for i in (4, 5) for k in ("qw", "sc", "qz")], 2, 64)
     big = _case(13, 65, 2, 1, 128, 128, 32, False)
     with pytest.raises(G.GptqError):
         _run(*big)
