@@ -8,8 +8,9 @@
 //  * Work: (chunk of keys, key head and row tile, sequence).  Chunks have one size,
 //    so ragged batches balance; CTAs whose chunk lies behind a sequence's end leave
 //    at once.  The four warps of a CTA take tiles of 32 keys in turn, each with its
-//    own running maximum, sum and output, joined at the end; chunks are joined by a
-//    second kernel in a fixed order.
+//    own running maximum, sum and output, joined at the end.  Up to eight chunks that
+//    fit the GPU at once are a cluster, whose CTAs join them out of each other's
+//    shared memory; otherwise a second kernel joins them, in a fixed order.
 //  * A tile's 16-key halves are contiguous in the cache (a page is a multiple of
 //    16): eight bulk copies (codes and parameters of keys and values, two halves),
 //    one instruction of eight lanes, KV_RING tiles ahead on one mbarrier a tile.
@@ -39,6 +40,7 @@ namespace gptq {
 constexpr int KV_WARPS = 4, KV_TILE = 32, KV_RING = 3;
 constexpr float KV_LAZY = 7.f;
 constexpr float KV_NONE = -3e38f;          // the maximum of no scores: finite, so that no difference is NaN
+constexpr int KV_CLUSTER = 1024;           // most keys of a cluster's chunk
 constexpr int KV_ALONE = 256;              // up to so many keys: one chunk, no second kernel
 
 struct KvAttn {
@@ -144,7 +146,39 @@ template <int D, int G> struct KvShape {
     static constexpr int CTAS = D == 64 ? 4 : D == 128 && G < 4 ? 4 : 2;   // per SM, by registers
 };
 
-template <int D, int G>
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
+                 ::: "memory");
+}
+
+// The address of shared memory `a` in CTA `rank` of the cluster
+__device__ __forceinline__ uint32_t peer_addr(uint32_t a, uint32_t rank)
+{
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+    return r;
+}
+
+__device__ __forceinline__ float peer_f(uint32_t a)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float4 peer_f4(uint32_t a)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(a)
+                 : "memory");
+    return v;
+}
+
+// CLUSTER: the chunks of a row tile are the CTAs of one cluster
+template <int D, int G, bool CLUSTER>
 __global__ void __launch_bounds__(KV_WARPS * 32, KvShape<D, G>::CTAS) kv4_attention_kernel(const KvAttn p)
 {
     using Sh = KvShape<D, G>;
@@ -152,7 +186,7 @@ __global__ void __launch_bounds__(KV_WARPS * 32, KvShape<D, G>::CTAS) kv4_attent
     constexpr uint32_t LO = 0x000F000Fu, HI = 0x00F000F0u, ALL = 0xffffffffu;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(16) float qsum[G][8];             // read in pairs
-    __shared__ float wm[KV_WARPS][8], wl[KV_WARPS][8];
+    __shared__ float wm[KV_WARPS][8], wl[KV_WARPS][8], cm[8], cl[8];
     __shared__ __align__(8) uint64_t bars[KV_WARPS * KV_RING];
     __shared__ int abort;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -165,7 +199,7 @@ __global__ void __launch_bounds__(KV_WARPS * 32, KvShape<D, G>::CTAS) kv4_attent
     }
     if (sp.rows <= 0) return;
     const int c0 = sp.base + int(blockIdx.x) * p.chunk, c1 = min(sp.hi, c0 + p.chunk);
-    if (c0 >= sp.hi && (blockIdx.x > 0 || p.splits > 1)) return;
+    if (!CLUSTER && c0 >= sp.hi && (blockIdx.x > 0 || p.splits > 1)) return;
     const int tiles = c1 > c0 ? (c1 - c0 + KV_TILE - 1) / KV_TILE : 0;
 
     if (lane == 0)
@@ -503,12 +537,18 @@ __global__ void __launch_bounds__(KV_WARPS * 32, KvShape<D, G>::CTAS) kv4_attent
             c[w] = ex2(wm[w][r] - top);
             sum = fmaf(c[w], wl[w][r], sum);
         }
-        if (p.splits > 1) { dst[8 * D + r] = top; dst[8 * D + 8 + r] = sum; }
-        const float scale = p.splits > 1 ? 1.f : sum > 0.f ? 1.f / sum : 0.f;
+        if (CLUSTER) { cm[r] = top; cl[r] = sum; }
+        else if (p.splits > 1) { dst[8 * D + r] = top; dst[8 * D + 8 + r] = sum; }
+        const float scale = CLUSTER || p.splits > 1 ? 1.f : sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
         for (int w = 0; w < KV_WARPS; ++w) wm[w][r] = c[w] * scale;
     }
     __syncthreads();
+    auto put = [&](int r, int d, float4 v) {
+        alignas(8) const __half2 h[2] = {__floats2half2_rn(v.x, v.y), __floats2half2_rn(v.z, v.w)};
+        *reinterpret_cast<uint2*>(p.out + kv_row(p, sp.s0, hk, rt * 8 + r) * D + d) =
+            *reinterpret_cast<const uint2*>(h);
+    };
     for (int e = threadIdx.x * 4; e < rows * D; e += KV_WARPS * 32 * 4) {
         const int r = e / D, d = e - r * D;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -520,13 +560,30 @@ __global__ void __launch_bounds__(KV_WARPS * 32, KvShape<D, G>::CTAS) kv4_attent
             v.x = fmaf(c, u.x, v.x); v.y = fmaf(c, u.y, v.y);
             v.z = fmaf(c, u.z, v.z); v.w = fmaf(c, u.w, v.w);
         }
-        if (p.splits == 1) {
-            alignas(8) const __half2 h[2] = {__floats2half2_rn(v.x, v.y), __floats2half2_rn(v.z, v.w)};
-            *reinterpret_cast<uint2*>(p.out + kv_row(p, sp.s0, hk, rt * 8 + r) * D + d) =
-                *reinterpret_cast<const uint2*>(h);
-        } else {
-            *reinterpret_cast<float4*>(dst + e) = v;
+        if (CLUSTER) *reinterpret_cast<float4*>(reinterpret_cast<float*>(smem) + e) = v;
+        else if (p.splits == 1) put(r, d, v);
+        else *reinterpret_cast<float4*>(dst + e) = v;
+    }
+    if constexpr (CLUSTER) {                               // each CTA joins its share of the elements
+        cluster_sync();
+        const uint32_t am = smem_u32(cm), al = smem_u32(cl), ao = smem_u32(smem);
+        for (int e = (blockIdx.x * (KV_WARPS * 32) + threadIdx.x) * 4; e < rows * D;
+             e += p.splits * (KV_WARPS * 32 * 4)) {
+            const int r = e / D;
+            float top = KV_NONE, sum = 0.f;
+            for (int s = 0; s < p.splits; ++s) top = fmaxf(top, peer_f(peer_addr(am + r * 4, s)));
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int s = 0; s < p.splits; ++s) {
+                const float c = ex2(peer_f(peer_addr(am + r * 4, s)) - top);
+                sum = fmaf(c, peer_f(peer_addr(al + r * 4, s)), sum);
+                const float4 u = peer_f4(peer_addr(ao + e * 4, s));
+                v.x = fmaf(c, u.x, v.x); v.y = fmaf(c, u.y, v.y);
+                v.z = fmaf(c, u.z, v.z); v.w = fmaf(c, u.w, v.w);
+            }
+            const float inv = sum > 0.f ? 1.f / sum : 0.f;
+            put(r, e - r * D, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
         }
+        cluster_sync();                                    // the others have read this CTA's memory
     }
 }
 
@@ -562,7 +619,7 @@ template <int D> __global__ void __launch_bounds__(256) kv4_join_kernel(const Kv
 // SM eight CTAs (two rounds of four) when every sequence has the bound's length; twelve
 // from 8 sequences on, whose lengths may differ (32 ragged ones: 62 us against 67 with
 // eight; two of 131000: 95 us with eight, 105 with twelve)
-struct KvPlan { int chunk, splits, row_tiles; size_t bytes; };
+struct KvPlan { int chunk, splits, row_tiles; bool cluster; size_t bytes; };
 
 KvPlan kv_plan(int64_t seqs, int hq, int hkv, int D, int64_t max_q, int64_t max_len, int64_t window)
 {
@@ -574,16 +631,28 @@ KvPlan kv_plan(int64_t seqs, int hq, int hkv, int D, int64_t max_q, int64_t max_
     constexpr int ROUND = KV_WARPS * KV_TILE;
     const int64_t units = seqs * hkv * k.row_tiles;
     const int64_t aim = 148 * (seqs < 8 ? 8 : 12);
-    int64_t chunk = (units * span + aim - 1) / aim;
-    chunk = std::max<int64_t>(ROUND, (chunk + ROUND - 1) / ROUND * ROUND);
-    if (span <= KV_ALONE) chunk = std::max<int64_t>(chunk, (span + ROUND - 1) / ROUND * ROUND);
-    chunk = std::max<int64_t>(chunk, ((span + 4095) / 4096 + ROUND - 1) / ROUND * ROUND);
+    auto rounded = [&](int64_t keys) {
+        return std::max<int64_t>(ROUND, (keys + ROUND - 1) / ROUND * ROUND);
+    };
+    // clusters of two to eight chunks where all of them fit the GPU at once (four CTAs an
+    // SM) with at most KV_CLUSTER keys each: one sequence of 777 keys in one launch
+    const int64_t most = std::min<int64_t>(8, 148 * 4 / std::max<int64_t>(units, 1));
+    int64_t chunk = rounded((units * span + aim - 1) / aim);
+    if (span <= KV_ALONE) {
+        chunk = std::max(chunk, rounded(span));
+    } else if (most >= 2 && rounded((span + most - 1) / most) <= KV_CLUSTER) {
+        chunk = rounded((span + most - 1) / most);
+        k.cluster = true;
+    } else {
+        chunk = std::max(chunk, rounded((span + 4095) / 4096));
+    }
     k.chunk = int(std::min<int64_t>(chunk, int64_t(1) << 30));
     k.splits = int((span + k.chunk - 1) / k.chunk);
+    k.cluster = k.cluster && k.splits > 1;
     // splits <= ceil(aim / units) by the choice of chunk; this bound grows with every
     // argument, so a workspace for the bounds serves every smaller call
-    const int64_t most = std::min(units * ((max_len + ROUND - 1) / ROUND + 1), units + 148 * 12);
-    k.bytes = align_up(size_t(most) * 8 * (D + 2) * 4, 256);
+    const int64_t parts = std::min(units * ((max_len + ROUND - 1) / ROUND + 1), units + 148 * 12);
+    k.bytes = align_up(size_t(parts) * 8 * (D + 2) * 4, 256);
     return k;
 }
 
@@ -658,10 +727,28 @@ extern "C" int gptq_kv4_attention(const uint16_t* q, int64_t tokens, int64_t seq
     p.out = reinterpret_cast<__half*>(out);
     cudaStream_t st = as_stream(stream);
     KernelTimer kt(kKKvAttention, st);
-    auto run = [&](auto kern, auto join, int smem, std::atomic<bool> (&done)[64]) -> int {
-        if (!smem_opt_in(reinterpret_cast<const void*>(kern), smem, done)) return GPTQ_ERR_CUDA;
-        kern<<<dim3((unsigned)p.splits, (unsigned)(kv_heads * p.row_tiles), (unsigned)seqs),
-               KV_WARPS * 32, smem, st>>>(p);
+    const dim3 grid((unsigned)p.splits, (unsigned)(kv_heads * p.row_tiles), (unsigned)seqs);
+    auto run = [&](auto kern, auto ckern, auto join, int smem, std::atomic<bool> (&done)[2][64]) -> int {
+        if (!smem_opt_in(plan.cluster ? reinterpret_cast<const void*>(ckern)
+                                      : reinterpret_cast<const void*>(kern), smem, done[plan.cluster]))
+            return GPTQ_ERR_CUDA;
+        if (plan.cluster) {
+            cudaLaunchConfig_t cfg{};
+            cfg.gridDim = grid;
+            cfg.blockDim = KV_WARPS * 32;
+            cfg.dynamicSmemBytes = smem;
+            cfg.stream = st;
+            cudaLaunchAttribute at{};
+            at.id = cudaLaunchAttributeClusterDimension;
+            at.val.clusterDim.x = grid.x;
+            at.val.clusterDim.y = at.val.clusterDim.z = 1;
+            cfg.attrs = &at;
+            cfg.numAttrs = 1;
+            if (cudaLaunchKernelEx(&cfg, ckern, p) != cudaSuccess) return GPTQ_ERR_CUDA;
+            count_launches();
+            return launch_status();
+        }
+        kern<<<grid, KV_WARPS * 32, smem, st>>>(p);
         if (launch_status() != GPTQ_OK) return GPTQ_ERR_CUDA;
         count_launches();
         if (p.splits > 1) {
@@ -674,8 +761,9 @@ extern "C" int gptq_kv4_attention(const uint16_t* q, int64_t tokens, int64_t seq
     };
 #define KV_RUN(D, G)                                                                            \
     if (head_dim == D && g * G == D) {                                                          \
-        static std::atomic<bool> done[64];                                                      \
-        return run(kv4_attention_kernel<D, G>, kv4_join_kernel<D>, KvShape<D, G>::SMEM, done);  \
+        static std::atomic<bool> done[2][64];                                                   \
+        return run(kv4_attention_kernel<D, G, false>, kv4_attention_kernel<D, G, true>,         \
+                   kv4_join_kernel<D>, KvShape<D, G>::SMEM, done);                              \
     }
     KV_RUN(64, 1) KV_RUN(64, 2)
     KV_RUN(128, 1) KV_RUN(128, 2) KV_RUN(128, 4)
