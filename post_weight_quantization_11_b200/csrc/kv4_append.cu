@@ -15,6 +15,9 @@
 // cache word is a lane's: shuffles, no shared memory.  Every operation is an IEEE
 // fp32 one with its own rounding (no contraction), so the codes are a function of
 // the inputs alone.
+// Measured (B200, 32 + 2 x 8 heads of 128, fp16, groups of 32): 32 us for 4001 tokens
+// (104 MB: 3.3 TB/s, 0.50 of the measured copy rate; bound by the latency of the row
+// loads, one round ahead, and by 190 instructions a round of two rows), 2.2 us for 16.
 #include "common.cuh"
 #include "quant_common.cuh"
 #include "tc_common.cuh"

@@ -28,7 +28,10 @@
 //  * The rows of an operand are the keys kv_key(g) of its eight: the same keys are
 //    then two neighbouring columns of the other product's operand, and the reads of
 //    shared memory hit every bank as often (keys) or twice (values).
-
+// Measured (B200, 32 heads on 8 of 128): 59 us for 32 ragged sequences of up to 8000 keys
+// (178 MB: 3.0 TB/s), 92 us for two of 131000 in groups of 64 (2.7 TB/s), 6 us for one of
+// 777; bound by about 670 instructions a tile and warp (176 unpack, 48 multiply), issued in
+// half of the cycles by four warps a scheduler, and by the uneven last round of chunks.
 #include <cmath>
 
 #include "common.cuh"

@@ -32,10 +32,14 @@
 // The scales are applied every 32 FOLD columns: once a step for groups that are a
 // multiple of 128 columns (FOLD = 4); for a multiple of 64 or 32 (2, 1) a lane takes
 // words of a row that are 16 bytes apart, so that a product stays inside 32 columns.
+// What it reaches: a pass over 32 KB (a step of every warp) takes 0.55 us from shared
+// memory alone, 8.8 TB/s on 148 SMs; in a sweep of 14336 x 4096 rows 4.3 TB/s (0.65 of the
+// measured copy rate) with 270 instructions a step and warp (of which 128 unpack and
+// multiply), issued in half of the cycles; four warps a scheduler do not hide more.
 // SPLIT: x in two fp16 parts (22 bits) for fp32 activations, scaled by a power
 // of two per column: W4_TWICE: each read of the rows is multiplied with both;
 // W4_BESIDE: up to four columns, the second parts are operand columns 4 .. 7 (half
-// the products; 0.8 of the time of the experts' second product for one token).
+// the products; one token of 8 experts of 14336 x 4096: 59 us against 63 in all).
 #pragma once
 
 #include <atomic>
@@ -54,10 +58,6 @@ constexpr int W4_COLS = 8;                        // columns n of an operand
 enum W4Split : int { W4_WHOLE = 0, W4_TWICE = 1, W4_BESIDE = 2 };
 
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void pdl_launch()
-{
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
 
 // D (16x8 fp32) += A (16x16 fp16, row) B (16x8 fp16, col)
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,

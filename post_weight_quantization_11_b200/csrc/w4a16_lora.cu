@@ -10,6 +10,10 @@
 // the tcgen05 kernel's (w4a16_tc.cu), with t computed where the activations are put
 // in its order.  Partial results go through memory, not atomics: their order is
 // fixed.
+// Measured (B200): 11 us for one row and rank 16 of 4096 x 4096 (8.9 MB; gptq_w4a16_gemm
+// without adapters 11.7), 26 us for 8 requests of 14336 x 4096 with act-order (35 MB: two
+// rounds of row groups where 1.5 would do, the gather 3), 78 us for 93 rows of rank 64 of
+// 4096 x 11008 (45 of them the tcgen05 product).
 #include "common.cuh"
 #include "tc_common.cuh"
 #include "w4_rows.cuh"
