@@ -58,7 +58,7 @@ struct KvAttn {
     const int32_t* lens;
     const int32_t* start;
     float scale;                           // times log2(e)
-    int chunk, splits, row_tiles;
+    int chunk, splits, row_tiles, cluster; // cluster: the chunks of a row tile are one
     int grp;                               // query heads per key head
     uint32_t grp_mul;                      // ceil(2^32 / grp): r / grp = r grp_mul >> 32 for r grp < 2^32
     float* part;                           // unit x 8 rows x (D, then maximum and sum)
@@ -180,8 +180,10 @@ __device__ __forceinline__ float4 peer_f4(uint32_t a)
     return v;
 }
 
-// CLUSTER: the chunks of a row tile are the CTAs of one cluster
-template <int D, int G, bool CLUSTER>
+// HALF: at most four rows, whose second parts of u take the other four columns of the
+// operand (16 products a tile instead of 32 for the values, each of which holds the
+// scheduler up for six cycles)
+template <int D, int G, bool HALF>
 __global__ void __launch_bounds__(KV_WARPS * 32, KvShape<D, G>::CTAS) kv4_attention_kernel(const KvAttn p)
 {
     using Sh = KvShape<D, G>;
@@ -202,7 +204,7 @@ __global__ void __launch_bounds__(KV_WARPS * 32, KvShape<D, G>::CTAS) kv4_attent
     }
     if (sp.rows <= 0) return;
     const int c0 = sp.base + int(blockIdx.x) * p.chunk, c1 = min(sp.hi, c0 + p.chunk);
-    if (!CLUSTER && c0 >= sp.hi && (blockIdx.x > 0 || p.splits > 1)) return;
+    if (!p.cluster && c0 >= sp.hi && (blockIdx.x > 0 || p.splits > 1)) return;
     const int tiles = c1 > c0 ? (c1 - c0 + KV_TILE - 1) / KV_TILE : 0;
 
     if (lane == 0)
@@ -261,8 +263,9 @@ __global__ void __launch_bounds__(KV_WARPS * 32, KvShape<D, G>::CTAS) kv4_attent
     // order of a word's nibbles) and the sums over each group
     uint32_t qf[NB][4];
     {
-        const bool on = g < sp.rows;
-        const __half* src = p.q + kv_row(p, sp.s0, hk, rt * 8 + (on ? g : 0)) * D;
+        const int r = HALF ? g & 3 : g;
+        const bool on = r < sp.rows;
+        const __half* src = p.q + kv_row(p, sp.s0, hk, rt * 8 + (on ? r : 0)) * D;
         float qs[G] = {};
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
@@ -291,7 +294,7 @@ __global__ void __launch_bounds__(KV_WARPS * 32, KvShape<D, G>::CTAS) kv4_attent
     int lim[2], from[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        const int r = rt * 8 + min(2 * t + j, sp.rows - 1);
+        const int r = rt * 8 + min((2 * t + j) & (HALF ? 3 : 7), sp.rows - 1);
         lim[j] = sp.L - sp.n + kv_query(p, r) + 1;
         const int64_t lo = p.window > 0 ? int64_t(lim[j]) - p.window : 0;
         from[j] = int(max(lo, int64_t(0)));
@@ -354,12 +357,13 @@ __global__ void __launch_bounds__(KV_WARPS * 32, KvShape<D, G>::CTAS) kv4_attent
                     float2 sz = __half22float2(*reinterpret_cast<const __half2*>(
                         base + 2 * Sh::CODES + ((h * 16 + i * 8 + kv_key(g)) * G + k) * 4));
                     sz.x *= up;
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float v = fmaf(hi[2 * i + e], 0.0625f, lo[2 * i + e]);
-                        sc[h][2 * i + e] =
-                            fmaf(sz.x, fmaf(-sz.y, e ? qs.y : qs.x, v), sc[h][2 * i + e]);
-                    }
+                    float2 v = fma2(make_float2(hi[2 * i], hi[2 * i + 1]), make_float2(0.0625f, 0.0625f),
+                                    make_float2(lo[2 * i], lo[2 * i + 1]));
+                    v = fma2(make_float2(-sz.y, -sz.y), qs, v);
+                    v = fma2(make_float2(sz.x, sz.x), v,
+                             make_float2(sc[h][2 * i], sc[h][2 * i + 1]));
+                    sc[h][2 * i] = v.x;
+                    sc[h][2 * i + 1] = v.y;
                 }
             }
         }
@@ -479,8 +483,10 @@ __global__ void __launch_bounds__(KV_WARPS * 32, KvShape<D, G>::CTAS) kv4_attent
                     const __half2 uh = __floats2half2_rn(u0, u1);
                     const float2 f = __half22float2(uh);
                     const __half2 ul = __floats2half2_rn(u0 - f.x, u1 - f.y);
-                    bh[i] = movmatrix(*reinterpret_cast<const uint32_t*>(&uh));
-                    bl[i] = movmatrix(*reinterpret_cast<const uint32_t*>(&ul));
+                    const uint32_t wh = *reinterpret_cast<const uint32_t*>(&uh);
+                    const uint32_t wl = *reinterpret_cast<const uint32_t*>(&ul);
+                    bh[i] = movmatrix(HALF && t >= 2 ? wl : wh);
+                    if (!HALF) bl[i] = movmatrix(wl);
                 }
 #pragma unroll
                 for (int i = k * GB; i < (k + 1) * GB; ++i) {
@@ -494,8 +500,10 @@ __global__ void __launch_bounds__(KV_WARPS * 32, KvShape<D, G>::CTAS) kv4_attent
                     const uint32_t h2 = kv_center(c & HI, 64.f), h3 = kv_center(c8 & HI, 64.f);
                     mma_16816(o[i][0], n0, n1, n2, n3, bh[0], bh[1]);
                     mma_16816(o[i][1], h0, h1, h2, h3, bh[0], bh[1]);
-                    mma_16816(o[i][0], n0, n1, n2, n3, bl[0], bl[1]);
-                    mma_16816(o[i][1], h0, h1, h2, h3, bl[0], bl[1]);
+                    if (!HALF) {
+                        mma_16816(o[i][0], n0, n1, n2, n3, bl[0], bl[1]);
+                        mma_16816(o[i][1], h0, h1, h2, h3, bl[0], bl[1]);
+                    }
                 }
             }
         }
@@ -512,11 +520,18 @@ __global__ void __launch_bounds__(KV_WARPS * 32, KvShape<D, G>::CTAS) kv4_attent
 #pragma unroll
             for (int k = 0; k < G; ++k) zs[k][j] += __shfl_xor_sync(ALL, zs[k][j], s);
         }
+    if (HALF)
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                o[i][e >> 2][e & 3] += __shfl_xor_sync(ALL, o[i][e >> 2][e & 3], 2);
     __syncthreads();                                       // every warp is done with its ring
     const float undo = 1.f / factor;
     float* mine = reinterpret_cast<float*>(smem) + warp * (8 * D);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
+        if (HALF && t >= 2) break;
         if (g == 0) { wm[warp][2 * t + j] = m[j]; wl[warp][2 * t + j] = l[j]; }
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
@@ -540,9 +555,9 @@ __global__ void __launch_bounds__(KV_WARPS * 32, KvShape<D, G>::CTAS) kv4_attent
             c[w] = ex2(wm[w][r] - top);
             sum = fmaf(c[w], wl[w][r], sum);
         }
-        if (CLUSTER) { cm[r] = top; cl[r] = sum; }
+        if (p.cluster) { cm[r] = top; cl[r] = sum; }
         else if (p.splits > 1) { dst[8 * D + r] = top; dst[8 * D + 8 + r] = sum; }
-        const float scale = CLUSTER || p.splits > 1 ? 1.f : sum > 0.f ? 1.f / sum : 0.f;
+        const float scale = p.splits > 1 ? 1.f : sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
         for (int w = 0; w < KV_WARPS; ++w) wm[w][r] = c[w] * scale;
     }
@@ -563,11 +578,11 @@ __global__ void __launch_bounds__(KV_WARPS * 32, KvShape<D, G>::CTAS) kv4_attent
             v.x = fmaf(c, u.x, v.x); v.y = fmaf(c, u.y, v.y);
             v.z = fmaf(c, u.z, v.z); v.w = fmaf(c, u.w, v.w);
         }
-        if (CLUSTER) *reinterpret_cast<float4*>(reinterpret_cast<float*>(smem) + e) = v;
+        if (p.cluster) *reinterpret_cast<float4*>(reinterpret_cast<float*>(smem) + e) = v;
         else if (p.splits == 1) put(r, d, v);
         else *reinterpret_cast<float4*>(dst + e) = v;
     }
-    if constexpr (CLUSTER) {                               // each CTA joins its share of the elements
+    if (p.cluster) {                               // each CTA joins its share of the elements
         cluster_sync();
         const uint32_t am = smem_u32(cm), al = smem_u32(cl), ao = smem_u32(smem);
         for (int e = (blockIdx.x * (KV_WARPS * 32) + threadIdx.x) * 4; e < rows * D;
@@ -725,16 +740,17 @@ extern "C" int gptq_kv4_attention(const uint16_t* q, int64_t tokens, int64_t seq
     p.vc = v_codes; p.vp = reinterpret_cast<const __half2*>(v_params);
     p.table = block_table; p.lens = seq_lens; p.start = q_start;
     p.scale = scale * 1.4426950408889634f;
+    p.cluster = plan.cluster;
     p.chunk = plan.chunk; p.splits = plan.splits; p.row_tiles = plan.row_tiles;
     p.part = static_cast<float*>(ws);
     p.out = reinterpret_cast<__half*>(out);
     cudaStream_t st = as_stream(stream);
     KernelTimer kt(kKKvAttention, st);
     const dim3 grid((unsigned)p.splits, (unsigned)(kv_heads * p.row_tiles), (unsigned)seqs);
-    auto run = [&](auto kern, auto ckern, auto join, int smem, std::atomic<bool> (&done)[2][64]) -> int {
-        if (!smem_opt_in(plan.cluster ? reinterpret_cast<const void*>(ckern)
-                                      : reinterpret_cast<const void*>(kern), smem, done[plan.cluster]))
-            return GPTQ_ERR_CUDA;
+    const bool few = max_q * p.grp <= 4;
+    auto run = [&](auto kern, auto kern4, auto join, int smem, std::atomic<bool> (&done)[2][64]) -> int {
+        if (few) kern = kern4;
+        if (!smem_opt_in(reinterpret_cast<const void*>(kern), smem, done[few])) return GPTQ_ERR_CUDA;
         if (plan.cluster) {
             cudaLaunchConfig_t cfg{};
             cfg.gridDim = grid;
@@ -747,7 +763,7 @@ extern "C" int gptq_kv4_attention(const uint16_t* q, int64_t tokens, int64_t seq
             at.val.clusterDim.y = at.val.clusterDim.z = 1;
             cfg.attrs = &at;
             cfg.numAttrs = 1;
-            if (cudaLaunchKernelEx(&cfg, ckern, p) != cudaSuccess) return GPTQ_ERR_CUDA;
+            if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) return GPTQ_ERR_CUDA;
             count_launches();
             return launch_status();
         }

@@ -59,6 +59,17 @@ enum W4Split : int { W4_WHOLE = 0, W4_TWICE = 1, W4_BESIDE = 2 };
 
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Two fp32 FMAs in one instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<unsigned long long&>(d))
+        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
+          "l"(reinterpret_cast<unsigned long long&>(c)));
+    return d;
+}
+
 // D (16x8 fp32) += A (16x16 fp16, row) B (16x8 fp16, col)
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                           uint32_t a3, uint32_t b0, uint32_t b1)
@@ -271,10 +282,15 @@ __device__ __forceinline__ void w4_step(float (&y)[NT][2][4], uint32_t slot, int
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float v = fmaf(hi[c][m][e], 64.f, lo[c][m][e]);   // 2^-14 sum c x
-                        y[c][m][e] = fmaf(sz[m][e >> 1].x,
-                                          fmaf(sz[m][e >> 1].y, (e & 1) ? k.y : k.x, v), y[c][m][e]);
+                    for (int i = 0; i < 2; ++i) {
+                        const float2 h = make_float2(hi[c][m][2 * i], hi[c][m][2 * i + 1]);
+                        const float2 o = make_float2(lo[c][m][2 * i], lo[c][m][2 * i + 1]);
+                        float2 v = fma2(h, make_float2(64.f, 64.f), o);      // 2^-14 sum c x
+                        v = fma2(make_float2(sz[m][i].y, sz[m][i].y), k, v);
+                        v = fma2(make_float2(sz[m][i].x, sz[m][i].x), v,
+                                 make_float2(y[c][m][2 * i], y[c][m][2 * i + 1]));
+                        y[c][m][2 * i] = v.x;
+                        y[c][m][2 * i + 1] = v.y;
                     }
             }
         }
