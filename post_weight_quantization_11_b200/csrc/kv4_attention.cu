@@ -11,9 +11,9 @@
 //    own running maximum, sum and output, joined at the end.  Up to eight chunks that
 //    fit the GPU at once are a cluster, whose CTAs join them out of each other's
 //    shared memory; otherwise a second kernel joins them, in a fixed order.
-//  * A tile's 16-key halves are contiguous in the cache (a page is a multiple of
-//    16): eight bulk copies (codes and parameters of keys and values, two halves),
-//    one instruction of eight lanes, KV_RING tiles ahead on one mbarrier a tile.
+//  * A tile is contiguous in a page of 32 keys or more, its halves in one of 16: four or
+//    eight bulk copies (codes and parameters of keys and values), one instruction of as
+//    many lanes, KV_RING tiles ahead on one mbarrier a tile.
 //  * Scores: S^T = K q^T on m16n8k16 mma.sync, keys as rows.  A code alone in a half
 //    word is the fp16 subnormal c 2^-24 (low nibble) or c 2^-20 (high): one AND per
 //    operand register.  A key's scale and zero point are applied to the product:
@@ -217,9 +217,10 @@ __global__ void __launch_bounds__(KV_WARPS * 32, KvShape<D, G>::CTAS) kv4_attent
     const uint32_t ring = smem_u32(smem) + warp * (KV_RING * Sh::SLOT);
     const uint32_t bar0 = smem_u32(&bars[warp * KV_RING]);
     const int half = (lane >> 2) & 1, what = lane & 3;
+    const bool whole = p.page_shift >= 5, copies = lane < (whole ? 4 : 8);
     const int32_t* table = p.table + int64_t(b) * p.width;
     const uint32_t keyb = what < 2 ? D / 2 : G * 4;        // bytes of a key
-    const uint32_t bytes = keyb * 16, mask = (1u << p.page_shift) - 1u;
+    const uint32_t mask = (1u << p.page_shift) - 1u;
     const uint32_t pageb = (uint32_t(p.hkv) * keyb) << p.page_shift;
     const uint8_t* from0 =
         (what == 0 ? reinterpret_cast<const uint8_t*>(p.kc)
@@ -228,7 +229,7 @@ __global__ void __launch_bounds__(KV_WARPS * 32, KvShape<D, G>::CTAS) kv4_attent
                                            : reinterpret_cast<const uint8_t*>(p.vp)) +
         ((uint32_t(hk) * keyb) << p.page_shift);
     const uint32_t to0 = ring + (what < 2 ? what * Sh::CODES : 2 * Sh::CODES + (what - 2) * Sh::PARAMS) +
-                         half * bytes;
+                         half * keyb * 16;
     int ptile = warp, pslot = 0, pkey = c0 + warp * KV_TILE + half * 16;
     bool stray = false;                                    // a page out of range was met
     uint32_t page = 0;
@@ -242,14 +243,15 @@ __global__ void __launch_bounds__(KV_WARPS * 32, KvShape<D, G>::CTAS) kv4_attent
             stray = true;
         }
         const uint32_t bar = bar0 + pslot * 8;
+        const bool both = c0 + ptile * KV_TILE + 16 < c1;  // halves of the tile
         if (lane == 0)
             asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar),
-                         "r"(c0 + ptile * KV_TILE + 16 < c1 ? Sh::SLOT : Sh::SLOT / 2)
+                         "r"(both ? Sh::SLOT : Sh::SLOT / 2)
                          : "memory");
         __syncwarp();
-        if (lane < 8 && pkey < c1)
+        if (copies && pkey < c1)
             kv_bulk(to0 + pslot * Sh::SLOT, from0 + (uint64_t(page) * pageb + (uint32_t(pkey) & mask) * keyb),
-                    bytes, bar);
+                    keyb << (whole && both ? 5 : 4), bar);
         ptile += KV_WARPS;
         pkey += KV_WARPS * KV_TILE;
         pslot = pslot + 1 == KV_RING ? 0 : pslot + 1;
