@@ -557,8 +557,8 @@ int gptq_kv4_append(const void* q, int64_t q_stride, const void* k, int64_t k_st
  * rounded once.
  * head_dim, group_size, page_size and the cache: as gptq_kv4_append; q_heads a
  * multiple of kv_heads.  seqs == 0 or tokens == 0: no-op.
- * ws: gptq_kv4_attention_workspace_bytes(...) bytes, not shared with a call
- *    that may run at the same time.
+ * ws: gptq_kv4_attention_workspace_bytes(...) bytes (0 for few keys: ws may then
+ *    be NULL), not shared with a call that may run at the same time.
  */
 size_t gptq_kv4_attention_workspace_bytes(int64_t seqs, int q_heads, int kv_heads, int head_dim,
                                           int64_t max_q_len, int64_t max_seq_len);

@@ -669,8 +669,10 @@ KvPlan kv_plan(int64_t seqs, int hq, int hkv, int D, int64_t max_q, int64_t max_
     k.chunk = int(std::min<int64_t>(chunk, int64_t(1) << 30));
     k.splits = int((span + k.chunk - 1) / k.chunk);
     k.cluster = k.cluster && k.splits > 1;
-    // splits <= ceil(aim / units) by the choice of chunk; this bound grows with every
-    // argument, so a workspace for the bounds serves every smaller call
+    // None where the chunks are joined in a cluster or there is one: so is every smaller
+    // call then.  Otherwise splits <= ceil(aim / units) by the choice of chunk; this bound
+    // grows with every argument, so a workspace for the bounds serves every smaller call.
+    if (k.cluster || span <= KV_ALONE) return k;
     const int64_t parts = std::min(units * ((max_len + ROUND - 1) / ROUND + 1), units + 148 * 12);
     k.bytes = align_up(size_t(parts) * 8 * (D + 2) * 4, 256);
     return k;
@@ -717,18 +719,19 @@ extern "C" int gptq_kv4_attention(const uint16_t* q, int64_t tokens, int64_t seq
         return GPTQ_ERR_SHAPE;
     if (seqs == 0 || tokens == 0 || max_q_len == 0) return GPTQ_OK;
     if (!q || !k_codes || !k_params || !v_codes || !v_params || !seq_lens || !q_start || !out ||
-        !ws || (max_seq_len > 0 && !block_table))
+        (max_seq_len > 0 && !block_table))
         return GPTQ_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(k_codes) || !aligned16(k_params) || !aligned16(v_codes) ||
         !aligned16(v_params) || !aligned(block_table, 4) || !aligned(seq_lens, 4) ||
         !aligned(q_start, 4) || !aligned16(out) || !aligned16(ws))
         return GPTQ_ERR_INVALID_ARG;
+    if (max_q_len > (int64_t(1) << 24)) return GPTQ_ERR_SHAPE;
     if (ws_bytes < gptq_kv4_attention_workspace_bytes(seqs, q_heads, kv_heads, head_dim, max_q_len,
                                                       max_seq_len))
         return GPTQ_ERR_INVALID_ARG;
     const int64_t max_q = std::min(max_q_len, tokens);
     const KvPlan plan = kv_plan(seqs, q_heads, kv_heads, head_dim, max_q, max_seq_len, window);
-    if (plan.bytes > ws_bytes) return GPTQ_ERR_INVALID_ARG;
+    if (plan.bytes > ws_bytes || (plan.bytes && !ws)) return GPTQ_ERR_INVALID_ARG;
     if (int64_t(kv_heads) * plan.row_tiles > 65535) return GPTQ_ERR_SHAPE;
     KvAttn p{};
     p.q = reinterpret_cast<const __half*>(q);

@@ -627,7 +627,7 @@ def _out(t, name: str, shape, dtype, like):
 def _workspace(ws, nbytes: int, like):
     """(workspace, its bytes): the caller's, checked, or a new one."""
     if ws is None:
-        return like.new_empty(max(nbytes, 16), dtype=torch.uint8), max(nbytes, 16)
+        return (like.new_empty(nbytes, dtype=torch.uint8) if nbytes else None), nbytes
     if not isinstance(ws, torch.Tensor):
         raise ValueError("ws must be a CUDA tensor")
     _on(ws, "ws", ws.dtype, like.get_device())
@@ -685,7 +685,7 @@ def gptq_w4a16_lora(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor
     ws, nb = _workspace(ws, lib.gptq_w4a16_lora_workspace_bytes(b, m, d, group_size, r), x)
     _call("gptq_w4a16_lora", dev, x.data_ptr(), b, qweight.data_ptr(), scales.data_ptr(),
           qzeros.data_ptr(), _addr(perm), m, d, group_size, lora_a.data_ptr(), lora_b.data_ptr(),
-          lora_scaling.data_ptr(), adapter.data_ptr(), n, r, y.data_ptr(), ws.data_ptr(), nb)
+          lora_scaling.data_ptr(), adapter.data_ptr(), n, r, y.data_ptr(), _addr(ws), nb)
     return y
 
 
@@ -723,7 +723,7 @@ def gptq_w4a16_moe(x: torch.Tensor, logits: torch.Tensor, qweight_in: torch.Tens
     _call("gptq_w4a16_moe", dev, x.data_ptr(), T, logits.data_ptr(), E, top_k, bool(renormalize),
           qweight_in.data_ptr(), scales_in.data_ptr(), qzeros_in.data_ptr(), _addr(perm_in),
           qweight_out.data_ptr(), scales_out.data_ptr(), qzeros_out.data_ptr(), _addr(perm_out), d,
-          f, group_size, y.data_ptr(), ws.data_ptr(), nb)
+          f, group_size, y.data_ptr(), _addr(ws), nb)
     return y
 
 
@@ -873,7 +873,7 @@ def gptq_kv4_attention(q: torch.Tensor, cache: KV4Cache, block_table: torch.Tens
           cache.k_params.data_ptr(), cache.v_codes.data_ptr(), cache.v_params.data_ptr(),
           cache.pages, cache.page_size, cache.group_size, block_table.data_ptr(), width,
           seq_lens.data_ptr(), q_start.data_ptr(), scale, window, max_q_len, max_seq_len,
-          out.data_ptr(), ws.data_ptr(), nb)
+          out.data_ptr(), _addr(ws), nb)
     return out
 
 

@@ -104,23 +104,26 @@ def test_append(lib):
 
 def test_attention(lib):
     W = G.gptq_kv4_attention_workspace_bytes
-    ws = W(2, 8, 2, 64, 1, 64)
-    assert ws > 0 and W(0, 8, 2, 64, 1, 64) == 0
+    ws = W(2, 8, 2, 64, 1, 64000)
+    assert ws > 0 and W(0, 8, 2, 64, 1, 64000) == 0
+    assert W(2, 8, 2, 64, 1, 64) == 0                         # one chunk: nothing to join
     names = ("q T B hq hkv D kc kp vc vp pages page g table width lens start scale window maxq maxl out ws "
              "wsb stream").split()
     c = _caller(lib.gptq_kv4_attention, names,
                 dict(q=FAKE, T=2, B=2, hq=8, hkv=2, D=64, kc=FAKE, kp=FAKE, vc=FAKE, vp=FAKE, pages=9,
                      page=16, g=32, table=FAKE, width=4, lens=FAKE, start=FAKE, scale=0.125, window=0,
                      maxq=1, maxl=64, out=FAKE, ws=FAKE, wsb=ws, stream=None))
-    for p in ("q", "kc", "kp", "vc", "vp", "table", "lens", "start", "out", "ws"):
+    for p in ("q", "kc", "kp", "vc", "vp", "table", "lens", "start", "out"):
         assert c(**{p: None}) == 1
+    long = dict(maxl=64000, width=4000)
+    assert c(ws=None, **long) == 1 and c(wsb=ws - 1, **long) == 1
     for p in ("q", "kc", "kp", "vc", "vp", "out", "ws"):
         assert c(**{p: MIS}) == 1
     for p in ("table", "lens", "start"):
         assert c(**{p: ODD}) == 1
-    assert c(wsb=ws - 1) == 1 and c(scale=float("nan")) == 1 and c(scale=float("inf")) == 1
+    assert c(scale=float("nan")) == 1 and c(scale=float("inf")) == 1
     for bad in (dict(T=-1), dict(B=-1), dict(B=65536), dict(hq=7), dict(hq=0), dict(hkv=0), dict(pages=0),
-                dict(width=-1), dict(window=-1), dict(maxq=-1), dict(maxl=65), dict(maxl=-1)):
+                dict(width=-1), dict(window=-1), dict(maxq=-1), dict(maxq=(1 << 24) + 1), dict(maxl=65), dict(maxl=-1)):
         assert c(**bad) == 2
     for bad in (dict(D=96), dict(g=128), dict(g=16), dict(page=24), dict(page=8)):
         assert c(**bad) == 4

@@ -304,7 +304,7 @@ def test_attention_rows_behind_the_last_sequence_and_given_buffers():
     c = _attn_case(6, [33, 50], [1, 2], 4, 2, 64, 16, 32)
     c["q"] = np.concatenate([c["q"], c["q"][:2]])
     out = torch.full(c["q"].shape, 5.0, dtype=torch.float16, device=DEV)
-    ws = torch.full((G.gptq_kv4_attention_workspace_bytes(2, 4, 2, 64, 2, 64),), 255,
+    ws = torch.full((G.gptq_kv4_attention_workspace_bytes(2, 4, 2, 64, 2, 64) + 256,), 255,
                     dtype=torch.uint8, device=DEV)
     got = _attn_check(c, out=out, ws=ws)
     assert (got[3:] == 5).all()
