@@ -65,4 +65,26 @@ private:
 constexpr int64_t kMaxDim = 32768;
 constexpr int64_t kMaxRows = int64_t(1) << 24;
 
+// A kernel launched by launch_after waits here for its predecessors' results
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// A kernel on the stream that may start before its predecessor on it has ended
+// (it waits by pdl_wait)
+template <class... A>
+inline cudaError_t launch_after(void (*kern)(A...), dim3 grid, dim3 block, size_t smem,
+                                cudaStream_t st, A... args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 }  // namespace gptq

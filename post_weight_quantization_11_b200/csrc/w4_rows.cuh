@@ -57,8 +57,6 @@ constexpr int W4_STEP = 128;                      // columns per step
 constexpr int W4_COLS = 8;                        // columns n of an operand
 enum W4Split : int { W4_WHOLE = 0, W4_TWICE = 1, W4_BESIDE = 2 };
 
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // Two fp32 FMAs in one instruction
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
 {
@@ -705,25 +703,6 @@ inline bool smem_opt_in(const void* kern, int most, std::atomic<bool> (&done)[64
         return false;
     if (dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_release);
     return true;
-}
-
-// A kernel on the stream that may start before its predecessor on it has ended
-// (it waits by pdl_wait)
-template <class... A>
-inline cudaError_t launch_after(void (*kern)(A...), dim3 grid, dim3 block, size_t smem,
-                                cudaStream_t st, A... args)
-{
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 }  // namespace gptq

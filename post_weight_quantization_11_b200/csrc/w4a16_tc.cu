@@ -9,7 +9,7 @@
 //  * warp 0 loads the packed words by TMA (128 rows x 64 codes = 4 KB per
 //    stage, sixteen stages deep), warp 1 the activations (N x 64 fp16, 128-byte
 //    swizzle; columns in sweep order, gathered first when perm is given);
-//  * the dequantization warps (one or two threads per weight row) turn every
+//  * the dequantization warps (two threads per weight row) turn every
 //    packed word into one 16-byte chunk of exact fp16 values c - z: one mask
 //    and OR per pair of nibbles puts nibbles k and k + 4 into the mantissas
 //    of two 1024.0 halves, one subtraction of 1024 + z leaves c - z (small
@@ -21,11 +21,11 @@
 //  * warp 2 issues tcgen05.mma kind::f16 (M = 128 weight rows, N = the batch
 //    tile, K = 16), accumulating one scale chunk (a group, at most 512
 //    columns) per TMEM accumulator, two accumulators in turn;
-//  * four epilogue warps fold each chunk's accumulator into fp32 registers
+//  * the epilogue warps fold each chunk's accumulator into fp32 registers
 //    with the group's fp16 scale, then write y (atomically when K is split).
-// Two shapes: batch tiles up to 32 columns with eight dequantization warps
-// (decode: the dequantization sets the pace), and up to 128 columns with four
-// (the epilogue's 128 accumulators per thread need the registers).
+// Two shapes: batch tiles up to 32 columns with four epilogue warps, and up to 128
+// columns with eight, of 64 accumulators a thread; eight dequantization warps, which
+// set the pace of small tiles and of small groups.
 // Products (c - z) x are exact in fp32; sums are fp32 (each TMEM chunk
 // accumulates at most 512 products).  Every mbarrier wait is bounded.
 #include "common.cuh"
@@ -38,15 +38,16 @@ constexpr int WQ_M = 128, WQ_K = 64, WQ_NBIG = 128;
 constexpr int WQ_CH = 512;                                   // max K per accumulation chunk
 constexpr int WQ_A_BYTES = WQ_M * WQ_K * 2;                  // 16 KB
 constexpr int WQ_Q_BYTES = WQ_M * WQ_K / 2;                  // 4 KB
-constexpr int WQ_EPI_WARPS = 4;
 
 // The decode shape (batch tile <= 32) has a small activation tile, so it
 // keeps 8 operand stages (the MMAs' commits come back late relative to the
 // short dequantization of a stage); the large shape keeps 4 of 32 KB.
 template <int NMAX> struct WqCfg {
-    static constexpr int DEQ_WARPS = NMAX <= 32 ? 8 : 4;
+    static constexpr int DEQ_WARPS = 8;
     static constexpr int WORDS = 8 / (DEQ_WARPS / 4);          // packed words per thread and stage
-    static constexpr int THREADS = 32 * (3 + DEQ_WARPS + WQ_EPI_WARPS);
+    static constexpr int EPI_WARPS = NMAX <= 32 ? 4 : 8;
+    static constexpr int EPI_COLS = NMAX / (EPI_WARPS / 4);    // accumulators per epilogue thread
+    static constexpr int THREADS = 32 * (3 + DEQ_WARPS + EPI_WARPS);
     static constexpr uint32_t TMEM_COLS = 2 * NMAX < 32 ? 32 : 2 * NMAX;
     static constexpr int STAGES = NMAX <= 32 ? 8 : 4;
     static constexpr int QSTAGES = NMAX <= 32 ? 8 : 16;
@@ -117,7 +118,7 @@ w4a16_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     if (threadIdx.x == 0) {
         for (int s = 0; s < WQ_QSTAGES; ++s) { mbar_init(&qfull[s], 1); mbar_init(&qempty[s], WqCfg<NMAX>::DEQ_WARPS); }
         for (int s = 0; s < WQ_STAGES; ++s) { mbar_init(&afull[s], WqCfg<NMAX>::DEQ_WARPS + 1); mbar_init(&aempty[s], 1); }
-        for (int a = 0; a < 2; ++a) { mbar_init(&accf[a], 1); mbar_init(&acce[a], WQ_EPI_WARPS); }
+        for (int a = 0; a < 2; ++a) { mbar_init(&accf[a], 1); mbar_init(&acce[a], WqCfg<NMAX>::EPI_WARPS); }
         *abort = 0;
         fence_mbar_init();
     }
@@ -128,6 +129,7 @@ w4a16_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     const uint32_t tmem = *tmem_slot;
     const int P = gridDim.x;
     const int spc = p.chunk / WQ_K;                          // stages per chunk
+    const int spg = int(p.gsz / WQ_K), cpg = spg / spc;      // stages and chunks per group
     const int64_t G = p.d / p.gsz, Gz = (G + 1) / 2;
 
     if (warp == 0 || warp == 1) {
@@ -143,6 +145,7 @@ w4a16_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             int stage = 0;
             uint32_t phase = 0, armed = 0, armed_par = 0;
             bool ok = true;
+            if (!packed) pdl_wait();                         // for the gathered activations
             for (int q = blockIdx.x; q < p.items && ok; q += P) {
                 const WqItem it = wq_item(p, q);
                 for (int s = it.c0 * spc; s < it.c1 * spc; ++s) {
@@ -212,17 +215,18 @@ w4a16_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             const bool live = row < p.m;
             // zero points: the item's first group now, every next group one
             // group ahead (its load overlaps the current group's stages)
-            const int64_t s_begin = int64_t(it.c0) * spc, s_end = int64_t(it.c1) * spc;
-            int64_t gi_cur = (s_begin * WQ_K) / p.gsz;
-            const int64_t gi_last = ((s_end - 1) * WQ_K) / p.gsz;
-            uint32_t zb_cur = live ? uint32_t(p.qzeros[row * Gz + gi_cur / 2]) : 0u;
-            uint32_t zb_next = (live && gi_cur < gi_last) ? uint32_t(p.qzeros[row * Gz + (gi_cur + 1) / 2]) : 0u;
-            for (int64_t s = s_begin; s < s_end; ++s) {
-                const int64_t gi = (s * WQ_K) / p.gsz;
-                if (gi != gi_cur) {
-                    gi_cur = gi;
+            const uint8_t* zrow = p.qzeros + row * Gz;
+            const int s_begin = it.c0 * spc, s_end = it.c1 * spc;
+            int gi_cur = s_begin / spg, left = spg - (s_begin - gi_cur * spg);
+            const int gi_last = (s_end - 1) / spg;
+            uint32_t zb_cur = live ? uint32_t(zrow[gi_cur / 2]) : 0u;
+            uint32_t zb_next = (live && gi_cur < gi_last) ? uint32_t(zrow[(gi_cur + 1) / 2]) : 0u;
+            for (int s = s_begin; s < s_end; ++s, --left) {
+                if (left == 0) {
+                    left = spg;
+                    ++gi_cur;
                     zb_cur = zb_next;
-                    zb_next = (live && gi_cur < gi_last) ? uint32_t(p.qzeros[row * Gz + (gi_cur + 1) / 2]) : 0u;
+                    zb_next = (live && gi_cur < gi_last) ? uint32_t(zrow[(gi_cur + 1) / 2]) : 0u;
                 }
                 if (!mbar_wait(&qfull[qs], qph, kErrWaitFull, abort)) { ok = false; break; }
                 uint32_t words[W];
@@ -263,35 +267,38 @@ w4a16_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             }
         }
     } else {
-        // epilogue: TMEM lane quarter of the warp, one weight row per thread
-        const int qr = warp & 3;
+        // epilogue: TMEM lane quarter of the warp, one weight row and EC columns per thread
+        constexpr int EC = WqCfg<NMAX>::EPI_COLS;
+        const int qr = warp & 3, e0 = (warp - (3 + WqCfg<NMAX>::DEQ_WARPS)) / 4 * EC;
         const int r = qr * 32 + lane;
         int ch = 0;
         bool ok = true;
-        float sum[NMAX];
+        float sum[EC];
         for (int q = blockIdx.x; q < p.items && ok; q += P) {
             const WqItem it = wq_item(p, q);
             const int64_t row = int64_t(it.rt) * WQ_M + r;
             const bool live = row < p.m;
+            const __half* srow = p.scales + row * G;
+            int gi = it.c0 / cpg, left = cpg - (it.c0 - gi * cpg);
 #pragma unroll
-            for (int u = 0; u < NMAX; ++u) sum[u] = 0.f;
-            for (int c = it.c0; c < it.c1; ++c, ++ch) {
+            for (int u = 0; u < EC; ++u) sum[u] = 0.f;
+            for (int c = it.c0; c < it.c1; ++c, ++ch, --left) {
                 const int a = ch & 1;
                 const uint32_t aph = (ch >> 1) & 1;
+                if (left == 0) { left = cpg; ++gi; }
                 // the chunk's scale is requested before the wait, which hides its latency
-                const int64_t gi = (int64_t(c) * p.chunk) / p.gsz;
-                const float sc = live ? __half2float(p.scales[row * G + gi]) : 0.f;
+                const float sc = live ? __half2float(srow[gi]) : 0.f;
                 if (!mbar_wait(&accf[a], aph, kErrWaitAccFull, abort)) { ok = false; break; }
                 tc_fence_after();
-                const uint32_t base = tmem + uint32_t(a * NMAX) + (uint32_t(qr * 32) << 16);
+                const uint32_t base = tmem + uint32_t(a * NMAX + e0) + (uint32_t(qr * 32) << 16);
 #pragma unroll
-                for (int cb = 0; cb < (NMAX + 31) / 32; ++cb) {
-                    if (cb * 32 < p.ntile) {
-                        float v[32];
-                        tmem_ld32(base + uint32_t(cb * 32), v);
+                for (int cb = 0; cb < EC / 16; ++cb) {
+                    if (e0 + cb * 16 < p.ntile) {
+                        float v[16];
+                        tmem_ld16(base + uint32_t(cb * 16), v);
 #pragma unroll
-                        for (int u = 0; u < 32; ++u)
-                            if (cb * 32 + u < NMAX) sum[cb * 32 + u] = fmaf(sc, v[u], sum[cb * 32 + u]);
+                        for (int u = 0; u < 16; ++u)
+                            sum[cb * 16 + u] = fmaf(sc, v[u], sum[cb * 16 + u]);
                     }
                 }
                 tc_fence_before();
@@ -302,9 +309,9 @@ w4a16_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             const int64_t b0 = int64_t(it.nt) * p.ntile;
             float* y = p.y + it.ks * p.split_stride;
 #pragma unroll
-            for (int u = 0; u < NMAX; ++u) {
-                const int64_t b = b0 + u;
-                if (u < p.ntile && b < p.batch) {
+            for (int u = 0; u < EC; ++u) {
+                const int64_t b = b0 + e0 + u;
+                if (e0 + u < p.ntile && b < p.batch) {
                     if (p.atomic) atomicAdd(y + b * p.m + row, sum[u]);
                     else y[b * p.m + row] = sum[u];
                 }
@@ -401,7 +408,11 @@ int wq_run(const WqPlan& plan, const __half* xp, int64_t batch, const uint32_t* 
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
             cudaSuccess)
             return GPTQ_ERR_CUDA;
-        kern<<<grid, threads, smem, st>>>(tq, tx, p);
+        // (behind a memset, an ordinary launch)
+        if (p.atomic) kern<<<grid, threads, smem, st>>>(tq, tx, p);
+        else if (launch_after(kern, dim3(unsigned(grid)), dim3(unsigned(threads)), size_t(smem), st,
+                              tq, tx, p) != cudaSuccess)
+            return GPTQ_ERR_CUDA;
         count_launches();
         return launch_status();
     };
