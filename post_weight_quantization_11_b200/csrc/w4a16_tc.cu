@@ -6,10 +6,11 @@
 //
 // for any batch of activation rows.  The weights stream from HBM once, as
 // packed nibbles, and become tensor-core operands in shared memory:
-//  * warp 0 loads the packed words by TMA (128 rows x 64 codes = 4 KB per
-//    stage, sixteen stages deep), warp 1 the activations (N x 64 fp16, 128-byte
-//    swizzle; columns in sweep order, gathered first when perm is given);
-//  * the dequantization warps (two threads per weight row) turn every
+//  * warp 0 loads the packed words by TMA (128 rows x 256 codes = 16 KB, which
+//    four stages use, four such copies deep; rows of 32 bytes, a copy per stage,
+//    held the loads to a third of this), warp 1 the activations (N x 64 fp16,
+//    128-byte swizzle; columns in sweep order, gathered first when perm is given);
+//  * the dequantization warps (a thread per weight row, stages in turn) turn every
 //    packed word into one 16-byte chunk of exact fp16 values c - z: one mask
 //    and OR per pair of nibbles puts nibbles k and k + 4 into the mantissas
 //    of two 1024.0 halves, one subtraction of 1024 + z leaves c - z (small
@@ -37,20 +38,20 @@ namespace gptq {
 constexpr int WQ_M = 128, WQ_K = 64, WQ_NBIG = 128;
 constexpr int WQ_CH = 512;                                   // max K per accumulation chunk
 constexpr int WQ_A_BYTES = WQ_M * WQ_K * 2;                  // 16 KB
-constexpr int WQ_Q_BYTES = WQ_M * WQ_K / 2;                  // 4 KB
+constexpr int WQ_WIN = 4;                                    // stages per copy of packed words
+constexpr int WQ_Q_BYTES = WQ_WIN * WQ_M * WQ_K / 2;         // 16 KB
 
 // The decode shape (batch tile <= 32) has a small activation tile, so it
 // keeps 8 operand stages (the MMAs' commits come back late relative to the
 // short dequantization of a stage); the large shape keeps 4 of 32 KB.
 template <int NMAX> struct WqCfg {
     static constexpr int DEQ_WARPS = 8;
-    static constexpr int WORDS = 8 / (DEQ_WARPS / 4);          // packed words per thread and stage
     static constexpr int EPI_WARPS = NMAX <= 32 ? 4 : 8;
     static constexpr int EPI_COLS = NMAX / (EPI_WARPS / 4);    // accumulators per epilogue thread
     static constexpr int THREADS = 32 * (3 + DEQ_WARPS + EPI_WARPS);
     static constexpr uint32_t TMEM_COLS = 2 * NMAX < 32 ? 32 : 2 * NMAX;
     static constexpr int STAGES = NMAX <= 32 ? 8 : 4;
-    static constexpr int QSTAGES = NMAX <= 32 ? 8 : 16;
+    static constexpr int QSTAGES = 4;
     static constexpr int B_BYTES = NMAX * WQ_K * 2;            // 4 KB or 16 KB
     static constexpr int SMEM = STAGES * (WQ_A_BYTES + B_BYTES) + QSTAGES * WQ_Q_BYTES + 1024 + 512;
 };
@@ -104,7 +105,7 @@ w4a16_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     constexpr int WQ_B_BYTES = WqCfg<NMAX>::B_BYTES;
     uint8_t* sA = smem;                                          // stages x 16 KB
     uint8_t* sB = sA + WQ_STAGES * WQ_A_BYTES;                   // stages x (4 or 16 KB)
-    uint8_t* sQ = sB + WQ_STAGES * WQ_B_BYTES;                   // qstages x 4 KB
+    uint8_t* sQ = sB + WQ_STAGES * WQ_B_BYTES;                   // qstages x 16 KB
     uint64_t* qfull = reinterpret_cast<uint64_t*>(sQ + WQ_QSTAGES * WQ_Q_BYTES);
     uint64_t* qempty = qfull + WQ_QSTAGES;
     uint64_t* afull = qempty + WQ_QSTAGES;
@@ -117,7 +118,7 @@ w4a16_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < WQ_QSTAGES; ++s) { mbar_init(&qfull[s], 1); mbar_init(&qempty[s], WqCfg<NMAX>::DEQ_WARPS); }
-        for (int s = 0; s < WQ_STAGES; ++s) { mbar_init(&afull[s], WqCfg<NMAX>::DEQ_WARPS + 1); mbar_init(&aempty[s], 1); }
+        for (int s = 0; s < WQ_STAGES; ++s) { mbar_init(&afull[s], WqCfg<NMAX>::DEQ_WARPS / 2 + 1); mbar_init(&aempty[s], 1); }
         for (int a = 0; a < 2; ++a) { mbar_init(&accf[a], 1); mbar_init(&acce[a], WqCfg<NMAX>::EPI_WARPS); }
         *abort = 0;
         fence_mbar_init();
@@ -148,11 +149,13 @@ w4a16_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             if (!packed) pdl_wait();                         // for the gathered activations
             for (int q = blockIdx.x; q < p.items && ok; q += P) {
                 const WqItem it = wq_item(p, q);
-                for (int s = it.c0 * spc; s < it.c1 * spc; ++s) {
+                const int s0 = it.c0 * spc, s1 = it.c1 * spc;
+                for (int s = packed ? s0 / WQ_WIN : s0; s < (packed ? (s1 - 1) / WQ_WIN + 1 : s1);
+                     ++s) {
                     if (!mbar_wait(&empty[stage], phase ^ 1, kErrWaitEmpty, abort)) { ok = false; break; }
                     mbar_arrive_expect_tx(&full[stage], bytes);
                     if (packed)
-                        tma_load_2d(sQ + stage * WQ_Q_BYTES, map, &full[stage], s * (WQ_K / 8),
+                        tma_load_2d(sQ + stage * WQ_Q_BYTES, map, &full[stage], s * (WQ_WIN * WQ_K / 8),
                                     it.rt * WQ_M);
                     else
                         tma_load_2d(sB + stage * WQ_B_BYTES, map, &full[stage], s * WQ_K,
@@ -200,10 +203,9 @@ w4a16_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             }
         }
     } else if (warp < 3 + WqCfg<NMAX>::DEQ_WARPS) {
-        // dequantization: thread (h, r) = weight row r of the tile, words
-        // h W .. h W + W - 1 of the row's 8 packed words of a stage -> the
-        // same 16-byte chunks of its 128-byte row
-        constexpr int W = WqCfg<NMAX>::WORDS;
+        // dequantization: thread (h, r) = weight row r of the tile, the stages of parity h:
+        // the row's 8 packed words of a stage -> the 16-byte chunks of its 128-byte row
+        constexpr int W = WQ_K / 8;
         const int t = threadIdx.x - 96;
         const int r = t & (WQ_M - 1), h = t >> 7;
         int qs = 0, as = 0;
@@ -228,41 +230,51 @@ w4a16_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                     zb_cur = zb_next;
                     zb_next = (live && gi_cur < gi_last) ? uint32_t(zrow[(gi_cur + 1) / 2]) : 0u;
                 }
-                if (!mbar_wait(&qfull[qs], qph, kErrWaitFull, abort)) { ok = false; break; }
-                uint32_t words[W];
-                {
-                    const uint4* src = reinterpret_cast<const uint4*>(sQ + qs * WQ_Q_BYTES + r * 32 + h * W * 4);
-#pragma unroll
-                    for (int v = 0; v < W / 4; ++v) {
-                        const uint4 q4 = src[v];
-                        words[4 * v] = q4.x; words[4 * v + 1] = q4.y;
-                        words[4 * v + 2] = q4.z; words[4 * v + 3] = q4.w;
-                    }
+                const int sub = s & (WQ_WIN - 1);
+                if ((sub == 0 || s == s_begin) && !mbar_wait(&qfull[qs], qph, kErrWaitFull, abort)) {
+                    ok = false;
+                    break;
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&qempty[qs]);
-                if (++qs == WQ_QSTAGES) { qs = 0; qph ^= 1; }
-                const uint32_t z = (gi_cur & 1) ? (zb_cur >> 4) : (zb_cur & 0xFu);
-                const uint32_t zbits = 0x64006400u | (z << 16) | z;
-                const __half2 zz = *reinterpret_cast<const __half2*>(&zbits);
-                if (!mbar_wait(&aempty[as], aph ^ 1, kErrWaitEmpty, abort)) { ok = false; break; }
-                uint8_t* arow = sA + as * WQ_A_BYTES + r * 128;
+                if ((as & 1) == h) {                       // (an even number of stages)
+                    uint32_t words[W];
+                    {
+                        const uint8_t* src = sQ + qs * WQ_Q_BYTES + r * 128;
 #pragma unroll
-                for (int i = 0; i < W; ++i) {
-                    uint32_t o[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t bits = wq_pair_bits(words[i], j);
-                        const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&bits), zz);
-                        o[j] = *reinterpret_cast<const uint32_t*>(&v);
+                        for (int v = 0; v < W / 4; ++v) {      // (128-byte swizzle)
+                            const uint4 q4 = *reinterpret_cast<const uint4*>(
+                                src + (((sub * 2 + v) ^ (r & 7)) << 4));
+                            words[4 * v] = q4.x; words[4 * v + 1] = q4.y;
+                            words[4 * v + 2] = q4.z; words[4 * v + 3] = q4.w;
+                        }
                     }
-                    const int chunk = h * W + i;
-                    *reinterpret_cast<uint4*>(arow + ((chunk ^ (r & 7)) << 4)) =
-                        make_uint4(o[0], o[1], o[2], o[3]);
+                    const uint32_t z = (gi_cur & 1) ? (zb_cur >> 4) : (zb_cur & 0xFu);
+                    const uint32_t zbits = 0x64006400u | (z << 16) | z;
+                    const __half2 zz = *reinterpret_cast<const __half2*>(&zbits);
+                    if (!mbar_wait(&aempty[as], aph ^ 1, kErrWaitEmpty, abort)) { ok = false; break; }
+                    uint8_t* arow = sA + as * WQ_A_BYTES + r * 128;
+#pragma unroll
+                    for (int i = 0; i < W; ++i) {
+                        uint32_t o[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t bits = wq_pair_bits(words[i], j);
+                            const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&bits), zz);
+                            o[j] = *reinterpret_cast<const uint32_t*>(&v);
+                        }
+                        *reinterpret_cast<uint4*>(arow + ((i ^ (r & 7)) << 4)) =
+                            make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&afull[as]);
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&afull[as]);
+                // The words' slot is freed only here, where their values have been used: freed
+                // right behind their loads, the loads were moved past the arrival and read the
+                // slot's next words.
+                if (sub == WQ_WIN - 1 || s + 1 == s_end) {
+                    if (lane == 0) mbar_arrive(&qempty[qs]);
+                    if (++qs == WQ_QSTAGES) { qs = 0; qph ^= 1; }
+                }
                 if (++as == WQ_STAGES) { as = 0; aph ^= 1; }
             }
         }
@@ -289,6 +301,7 @@ w4a16_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 // the chunk's scale is requested before the wait, which hides its latency
                 const float sc = live ? __half2float(srow[gi]) : 0.f;
                 if (!mbar_wait(&accf[a], aph, kErrWaitAccFull, abort)) { ok = false; break; }
+                __syncwarp();                              // the loads below are the warp's
                 tc_fence_after();
                 const uint32_t base = tmem + uint32_t(a * NMAX + e0) + (uint32_t(qr * 32) << 16);
 #pragma unroll
@@ -354,15 +367,18 @@ WqPlan wq_plan(int64_t batch, int64_t m, int64_t d, int64_t gsz, int sms)
     const int nch = (int)(d / p.chunk);
     const int64_t tiles = int64_t(p.n_rt) * p.n_nt;
     // split K (in whole chunks) when the tiles alone leave SMs idle: the
-    // split count that minimizes rounds x chunks per item, i.e. the longest
-    // CTA's share, among 1 .. nch (fewer splits on ties: fewer atomics)
+    // split count that minimizes rounds x stages per item, i.e. the longest
+    // CTA's share, among 1 .. nch (fewer splits on ties: fewer partial sums).
+    // Beginning and ending an item costs about 8 stages (93 rows of 14336 x 4096: 44 us
+    // against 59 with one chunk in its place; 4 and 12 stages choose the same).
     int ks = 1;
     if (tiles < 2 * sms) {
         double best = 1e300;
         for (int k = 1; k <= nch; ++k) {
             const int64_t cps = ceil_div(nch, k);
             const int64_t kk = ceil_div(nch, cps);
-            const double cost = double(ceil_div(tiles * kk, sms)) * double(cps + 1);
+            const double cost =
+                double(ceil_div(tiles * kk, sms)) * double(cps * (p.chunk / WQ_K) + 8);
             if (cost < best - 1e-9) { best = cost; ks = (int)kk; }
         }
     }
@@ -397,8 +413,8 @@ int wq_run(const WqPlan& plan, const __half* xp, int64_t batch, const uint32_t* 
         return GPTQ_ERR_CUDA;
     CUtensorMap tq, tx;
     if (encode_tmap_2d(&tq, CU_TENSOR_MAP_DATA_TYPE_UINT32, qweight, (uint64_t)(d / 8),
-                       (uint64_t)m, (uint64_t)(d / 8) * 4, WQ_K / 8, WQ_M,
-                       CU_TENSOR_MAP_SWIZZLE_NONE) != GPTQ_OK ||
+                       (uint64_t)m, (uint64_t)(d / 8) * 4, WQ_WIN * WQ_K / 8, WQ_M,
+                       CU_TENSOR_MAP_SWIZZLE_128B) != GPTQ_OK ||
         encode_tmap_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, xp, (uint64_t)d, (uint64_t)batch,
                        (uint64_t)d * 2, WQ_K, (uint32_t)p.ntile,
                        CU_TENSOR_MAP_SWIZZLE_128B) != GPTQ_OK)
