@@ -12,8 +12,8 @@
 // fixed.
 // Measured (B200): 11 us for one row and rank 16 of 4096 x 4096 (8.9 MB; gptq_w4a16_gemm
 // without adapters 11.7), 26 us for 8 requests of 14336 x 4096 with act-order (35 MB: two
-// rounds of row groups where 1.5 would do, the gather 3), 78 us for 93 rows of rank 64 of
-// 4096 x 11008 (45 of them the tcgen05 product).
+// rounds of row groups where 1.5 would do, the gather 3), 53 us for 93 rows of rank 64 of
+// 4096 x 11008 (36 of them the tcgen05 product).
 #include "common.cuh"
 #include "tc_common.cuh"
 #include "w4_rows.cuh"
@@ -22,7 +22,9 @@
 namespace gptq {
 
 constexpr int LORA_KW = 8, LORA_ROWS = 32 * (W4_WARPS / LORA_KW);   // of w4_sweep
-constexpr int LORA_JOIN = 4, LORA_JOIN_ROWS = 128;      // rows of x and of the layer per CTA of the join
+constexpr int LORA_JOIN = 4, LORA_MANY = 8;      // rows of x per CTA of the join, few and many
+constexpr int LORA_JOIN_ROWS = 128;              // rows of the layer
+constexpr int LORA_TC_PARTS = 4;                 // slices of the columns of x A^T (tcgen05 product)
 constexpr int LORA_SWEEP = 16;                   // most rows of x of the row sweep
 constexpr int LORA_MAX_RANK = 256;
 constexpr int LORA_SMS = 148;                    // the plan does not depend on the device that is current
@@ -38,71 +40,77 @@ struct LoraParams {
     int rank;
     W4Layer lay;
     int chunk, chunks, slice, slices, groups;
-    float* t;          // batch x rank
+    float* t;          // batch x rank (the tcgen05 product: LORA_TC_PARTS of them)
     __half* xp;        // batch x d: x in the order of the sweep or of the tcgen05 product, or null
     int tc;
     float* part;       // slices x batch x m
     float* y;
 };
 
-// t[b][r] = scaling (A_a[r] . x[b]).  A unit is a tile of eight rows b, one of the
-// adapters among them and 16 rank rows: S = A x^T on m16n8k16 mma.sync, the columns
-// split over the CTA's 16 warps.  A lane's 16-byte load is eight neighbouring columns
-// of its row, for A and x alike: operands of two products, whose order of the columns
-// does not matter.  Rows of other adapters are computed along and dropped.  All
-// threads; red: 16 x 128 floats.
-__device__ __forceinline__ void lora_shrink(const LoraParams& p, float* red)
+// t[b][r] = scaling (A_a[r] . x[b]).  A unit is a tile of eight rows b, 16 rank rows and
+// a slice of the columns, whose sums stay apart in t; for each adapter among the rows
+// S = A x^T on m16n8k16 mma.sync, the slice split over the CTA's 16 warps.  A lane's
+// 16-byte load is eight neighbouring columns of its row, for A and x alike: operands of
+// two products, whose order of the columns does not matter.  Rows of other adapters are
+// computed along and dropped.  All threads; red: 16 x 128 floats, ids: 8 ints.
+__device__ __forceinline__ void lora_shrink(const LoraParams& p, float* red, int* ids)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int tiles = int((p.batch + 7) / 8), rts = (p.rank + 15) / 16;
-    const int units = tiles * 8 * rts;
-    const int k0 = int(p.d / 32) * warp / W4_WARPS, k1 = int(p.d / 32) * (warp + 1) / W4_WARPS;
-    for (int u = blockIdx.x; u < units; u += gridDim.x) {
-        // neighbouring CTAs take other rank rows and row tiles before another adapter
-        const int slot = u / (tiles * rts), rest = u - slot * (tiles * rts);
+    for (int u = blockIdx.x; u < tiles * rts * LORA_TC_PARTS; u += gridDim.x) {
+        const int part = u % LORA_TC_PARTS, rest = u / LORA_TC_PARTS;
         const int64_t b0 = int64_t(rest / rts) * 8;
-        const int r0 = rest % rts * 16;
-        if (b0 + slot >= p.batch) continue;
-        const int id = p.adapter[b0 + slot];
-        if (id < 0 || id >= p.n) {
-            if (id != -1 && threadIdx.x == 0) atomicCAS(&g_device_status, 0, kErrIndex);
-            continue;
+        const int r0 = rest % rts * 16, rounds = int(p.d / 32);
+        const int n0 = rounds * part / LORA_TC_PARTS, n = rounds * (part + 1) / LORA_TC_PARTS - n0;
+        const int k0 = n0 + n * warp / W4_WARPS, k1 = n0 + n * (warp + 1) / W4_WARPS;
+        __syncthreads();                                   // the last unit's ids have been read
+        if (threadIdx.x < 8) {
+            int id = b0 + threadIdx.x < p.batch ? p.adapter[b0 + threadIdx.x] : -1;
+            if (id < -1 || id >= p.n) {
+                atomicCAS(&g_device_status, 0, kErrIndex);
+                id = -1;
+            }
+            ids[threadIdx.x] = id;
         }
-        bool first = true;                                 // of the tile's rows with this adapter
-        for (int j = 0; j < slot; ++j) first = first && p.adapter[b0 + j] != id;
-        if (!first) continue;
-        const __half* a0 = p.a + (int64_t(id) * p.rank + min(r0 + g, p.rank - 1)) * p.d + t * 8;
-        const __half* a1 = p.a + (int64_t(id) * p.rank + min(r0 + g + 8, p.rank - 1)) * p.d + t * 8;
-        const __half* x = p.x + min(b0 + g, p.batch - 1) * p.d + t * 8;
-        float s[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int k = k0; k < k1; k += 4) {                 // four rounds of 32 columns in flight
-            uint4 av[4], bv[4], xv[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (k + i < k1) {
-                    av[i] = __ldg(reinterpret_cast<const uint4*>(a0 + (k + i) * 32));
-                    bv[i] = __ldg(reinterpret_cast<const uint4*>(a1 + (k + i) * 32));
-                    xv[i] = __ldg(reinterpret_cast<const uint4*>(x + (k + i) * 32));
-                }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (k + i < k1) {
-                    mma_16816(s, av[i].x, bv[i].x, av[i].y, bv[i].y, xv[i].x, xv[i].y);
-                    mma_16816(s, av[i].z, bv[i].z, av[i].w, bv[i].w, xv[i].z, xv[i].w);
-                }
-        }
-        __syncthreads();                                   // the last unit's sums have been read
-        *reinterpret_cast<float4*>(red + (warp * 32 + lane) * 4) = make_float4(s[0], s[1], s[2], s[3]);
         __syncthreads();
-        if (threadIdx.x < 128) {                           // element e of lane l
-            const int l = threadIdx.x >> 2, e = threadIdx.x & 3;
-            float v = 0.f;
+        const __half* x = p.x + min(b0 + g, p.batch - 1) * p.d + t * 8;
+        for (int slot = 0; slot < 8; ++slot) {
+            const int id = ids[slot];
+            bool first = id >= 0;                          // of the tile's rows with this adapter
+            for (int j = 0; j < slot; ++j) first = first && ids[j] != id;
+            if (!first) continue;
+            const __half* a0 = p.a + (int64_t(id) * p.rank + min(r0 + g, p.rank - 1)) * p.d + t * 8;
+            const __half* a1 = p.a + (int64_t(id) * p.rank + min(r0 + g + 8, p.rank - 1)) * p.d + t * 8;
+            float s[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int k = k0; k < k1; k += 3) {             // three rounds of 32 columns in flight
+                uint4 av[3], bv[3], xv[3];
 #pragma unroll
-            for (int w = 0; w < W4_WARPS; ++w) v += red[w * 128 + threadIdx.x];
-            const int r = r0 + (l >> 2) + 8 * (e >> 1);
-            const int64_t b = b0 + 2 * (l & 3) + (e & 1);
-            if (r < p.rank && b < p.batch && p.adapter[b] == id)
-                p.t[b * p.rank + r] = v * p.scaling[id];
+                for (int i = 0; i < 3; ++i)
+                    if (k + i < k1) {
+                        av[i] = __ldg(reinterpret_cast<const uint4*>(a0 + (k + i) * 32));
+                        bv[i] = __ldg(reinterpret_cast<const uint4*>(a1 + (k + i) * 32));
+                        xv[i] = __ldg(reinterpret_cast<const uint4*>(x + (k + i) * 32));
+                    }
+#pragma unroll
+                for (int i = 0; i < 3; ++i)
+                    if (k + i < k1) {
+                        mma_16816(s, av[i].x, bv[i].x, av[i].y, bv[i].y, xv[i].x, xv[i].y);
+                        mma_16816(s, av[i].z, bv[i].z, av[i].w, bv[i].w, xv[i].z, xv[i].w);
+                    }
+            }
+            __syncthreads();                               // the last adapter's sums have been read
+            *reinterpret_cast<float4*>(red + (warp * 32 + lane) * 4) =
+                make_float4(s[0], s[1], s[2], s[3]);
+            __syncthreads();
+            if (threadIdx.x < 128) {                       // element e of lane l
+                const int l = threadIdx.x >> 2, e = threadIdx.x & 3;
+                float v = 0.f;
+#pragma unroll
+                for (int w = 0; w < W4_WARPS; ++w) v += red[w * 128 + threadIdx.x];
+                const int r = r0 + (l >> 2) + 8 * (e >> 1), j = 2 * (l & 3) + (e & 1);
+                if (r < p.rank && ids[j] == id)
+                    p.t[(part * p.batch + b0 + j) * p.rank + r] = v * p.scaling[id];
+            }
         }
     }
 }
@@ -212,9 +220,10 @@ lora_product_kernel(const __grid_constant__ CUtensorMap tm, const LoraParams p)
 }
 
 // t, and the activations in the order of the product that follows, eight at a time
-__global__ void __launch_bounds__(W4_THREADS) lora_front_kernel(const LoraParams p)
+__global__ void __launch_bounds__(W4_THREADS, 2) lora_front_kernel(const LoraParams p)
 {
     __shared__ __align__(16) float red[W4_WARPS * 128];
+    __shared__ int ids[8];
     const int64_t total = p.batch * p.d;
     for (int64_t i = (int64_t(blockIdx.x) * W4_THREADS + threadIdx.x) * 8; i < total;
          i += int64_t(gridDim.x) * (W4_THREADS * 8)) {
@@ -240,7 +249,7 @@ __global__ void __launch_bounds__(W4_THREADS) lora_front_kernel(const LoraParams
         }
         *reinterpret_cast<uint4*>(p.xp + i) = *reinterpret_cast<const uint4*>(h);
     }
-    if (p.tc) lora_shrink(p, red);
+    if (p.tc) lora_shrink(p, red, ids);
     else lora_shrink_few(p);
 }
 
@@ -326,6 +335,113 @@ template <int LANES> __global__ void __launch_bounds__(LORA_JOIN_ROWS) lora_join
             if (i < rows) p.y[(b0 + i) * p.m + r] = y[i];
 }
 
+// The same for many rows of x, eight a CTA, on m16n8k16 mma.sync: the rows of B_a by t,
+// which is split into two fp16 parts (22 bits) after a power of two has taken its largest
+// element to 2^13 .. 2^14.  A run of rows with one adapter shares the loads of B_a; the
+// other rows are computed along and dropped (on FMA units, like the few rows' join: 17 us
+// against 8 for 93 rows of rank 64).
+__global__ void __launch_bounds__(LORA_JOIN_ROWS) lora_join_many_kernel(const LoraParams p)
+{
+    constexpr int J = LORA_MANY;
+    __shared__ uint4 th[J][LORA_MAX_RANK / 8 + 1], tl[J][LORA_MAX_RANK / 8 + 1];
+    __shared__ float low[J][LORA_JOIN_ROWS], back[J];
+    __shared__ int ids[J];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    const int64_t r0 = int64_t(blockIdx.x) * LORA_JOIN_ROWS, r = r0 + tid;
+    const int64_t b0 = int64_t(blockIdx.y) * J;
+    const int rows = int(min(int64_t(J), p.batch - b0)), chunks = p.rank / 8;
+    if (tid < J) {
+        const int id = tid < rows ? p.adapter[b0 + tid] : -1;
+        ids[tid] = id < p.n ? id : -1;
+    }
+    pdl_wait();
+    float y[J] = {};
+    if (r < p.m) {
+        const float* src = p.part + b0 * p.m + r;
+        const int64_t slice = p.batch * p.m;
+#pragma unroll 4
+        for (int s = 0; s < p.slices; ++s, src += slice)
+#pragma unroll
+            for (int i = 0; i < J; ++i)
+                if (i < rows) y[i] += src[i * p.m];
+    }
+    __syncthreads();
+    for (int i = warp; i < rows; i += LORA_JOIN_ROWS / 32) {   // a lane's chunk of 8 elements
+        if (ids[i] < 0) continue;
+        float v[8] = {}, top = 0.f;
+        if (lane < chunks) {
+            const float* src = p.t + (b0 + i) * p.rank + lane * 8;
+#pragma unroll
+            for (int s = 0; s < LORA_TC_PARTS; ++s, src += p.batch * p.rank) {
+                const float4 u = *reinterpret_cast<const float4*>(src);
+                const float4 w = *reinterpret_cast<const float4*>(src + 4);
+                v[0] += u.x; v[1] += u.y; v[2] += u.z; v[3] += u.w;
+                v[4] += w.x; v[5] += w.y; v[6] += w.z; v[7] += w.w;
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (isfinite(v[e])) top = fmaxf(top, fabsf(v[e]));
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const int ex = top > 0.f ? max(-126, min(126, 13 - ilogbf(top))) : 0;
+        const float scale = __int_as_float((127 + ex) << 23);
+        if (lane == 0) back[i] = __int_as_float((127 - ex) << 23);
+        alignas(16) __half hi[8], lo[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float w = v[e] * scale;
+            hi[e] = __float2half_rn(w);
+            lo[e] = __float2half_rn(isfinite(w) ? w - __half2float(hi[e]) : 0.f);
+        }
+        if (lane < chunks) {
+            th[i][lane] = *reinterpret_cast<const uint4*>(hi);
+            tl[i][lane] = *reinterpret_cast<const uint4*>(lo);
+        }
+    }
+    __syncthreads();
+    const uint4 none = make_uint4(0, 0, 0, 0);
+    for (int i0 = 0, i1; i0 < rows; i0 = i1) {             // a run of one adapter
+        const int id = ids[i0];
+        for (i1 = i0 + 1; i1 < rows && ids[i1] == id; ++i1) {}
+        if (id < 0) continue;
+        const __half* src[4];                              // rows g and g + 8 of the warp's two tiles
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            src[q] = p.b + (int64_t(id) * p.m + min(r0 + warp * 32 + q * 8 + g, p.m - 1)) * p.rank;
+        float acc[2][4] = {};
+#pragma unroll 2
+        for (int c = t; c - t < chunks; c += 4) {          // 32 columns of B_a
+            const bool in = c < chunks;
+            uint4 bv[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                bv[q] = in ? __ldg(reinterpret_cast<const uint4*>(src[q] + c * 8)) : none;
+            const uint4 h = in && g < rows ? th[g][c] : none, l = in && g < rows ? tl[g][c] : none;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                mma_16816(acc[q], bv[2 * q].x, bv[2 * q + 1].x, bv[2 * q].y, bv[2 * q + 1].y, h.x, h.y);
+                mma_16816(acc[q], bv[2 * q].z, bv[2 * q + 1].z, bv[2 * q].w, bv[2 * q + 1].w, h.z, h.w);
+                mma_16816(acc[q], bv[2 * q].x, bv[2 * q + 1].x, bv[2 * q].y, bv[2 * q + 1].y, l.x, l.y);
+                mma_16816(acc[q], bv[2 * q].z, bv[2 * q + 1].z, bv[2 * q].w, bv[2 * q + 1].w, l.z, l.w);
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = 2 * t + (e & 1);
+                if (i >= i0 && i < i1)
+                    low[i][warp * 32 + q * 16 + g + 8 * (e >> 1)] = acc[q][e] * back[i];
+            }
+    }
+    __syncthreads();
+    if (r < p.m)
+#pragma unroll
+        for (int i = 0; i < J; ++i)
+            if (i < rows) p.y[(b0 + i) * p.m + r] = ids[i] >= 0 ? y[i] + low[i][tid] : y[i];
+}
+
 struct LoraPlan {
     bool tc;                                     // the tcgen05 product
     WqPlan wq;
@@ -343,9 +459,9 @@ struct LoraPlan {
 LoraPlan lora_plan(int64_t T, int64_t m, int64_t d, int64_t g, int rank)
 {
     LoraPlan p{};
-    p.at_xp = align_up(size_t(T) * rank * 4, 256);
-    p.at_part = p.at_xp + align_up(size_t(T) * d * 2, 1024);
     p.tc = T > LORA_SWEEP && g % 64 == 0;
+    p.at_xp = align_up(size_t(T) * rank * 4 * (p.tc ? LORA_TC_PARTS : 1), 256);
+    p.at_part = p.at_xp + align_up(size_t(T) * d * 2, 1024);
     if (p.tc) {
         p.wq = wq_plan(T, m, d, g, LORA_SMS);
         p.slices = p.wq.ksplit;
@@ -463,11 +579,15 @@ extern "C" int gptq_w4a16_lora(const uint16_t* x, int64_t batch, const uint32_t*
         count_launches();
         if (launch_status() != GPTQ_OK) return GPTQ_ERR_CUDA;
     }
-    auto join = rank >= 64 ? lora_join_kernel<8> : rank >= 32 ? lora_join_kernel<4>
-              : rank >= 16 ? lora_join_kernel<2> : lora_join_kernel<1>;
+    const bool many = plan.tc;
+    auto join = many           ? lora_join_many_kernel
+                : rank >= 64   ? lora_join_kernel<8>
+                : rank >= 32   ? lora_join_kernel<4>
+                : rank >= 16   ? lora_join_kernel<2>
+                               : lora_join_kernel<1>;
     if (launch_after(join,
                      dim3((unsigned)ceil_div(d_out, LORA_JOIN_ROWS),
-                          (unsigned)ceil_div(batch, LORA_JOIN)),
+                          (unsigned)ceil_div(batch, many ? LORA_MANY : LORA_JOIN)),
                      LORA_JOIN_ROWS, 0, st, p) != cudaSuccess)
         return GPTQ_ERR_CUDA;
     count_launches();

@@ -21,7 +21,7 @@
 //    the product does not depend on the order of K;
 //  * warp 2 issues tcgen05.mma kind::f16 (M = 128 weight rows, N = the batch
 //    tile, K = 16), accumulating one scale chunk (a group, at most 512
-//    columns) per TMEM accumulator, two accumulators in turn;
+//    columns) per TMEM accumulator, four accumulators in turn;
 //  * the epilogue warps fold each chunk's accumulator into fp32 registers
 //    with the group's fp16 scale, then write y (atomically when K is split).
 // Two shapes: batch tiles up to 32 columns with four epilogue warps, and up to 128
@@ -36,6 +36,7 @@
 namespace gptq {
 
 constexpr int WQ_M = 128, WQ_K = 64, WQ_NBIG = 128;
+constexpr int WQ_ACCS = 4;                                   // TMEM accumulators in turn
 constexpr int WQ_CH = 512;                                   // max K per accumulation chunk
 constexpr int WQ_A_BYTES = WQ_M * WQ_K * 2;                  // 16 KB
 constexpr int WQ_WIN = 4;                                    // stages per copy of packed words
@@ -49,7 +50,7 @@ template <int NMAX> struct WqCfg {
     static constexpr int EPI_WARPS = NMAX <= 32 ? 4 : 8;
     static constexpr int EPI_COLS = NMAX / (EPI_WARPS / 4);    // accumulators per epilogue thread
     static constexpr int THREADS = 32 * (3 + DEQ_WARPS + EPI_WARPS);
-    static constexpr uint32_t TMEM_COLS = 2 * NMAX < 32 ? 32 : 2 * NMAX;
+    static constexpr uint32_t TMEM_COLS = WQ_ACCS * NMAX;
     static constexpr int STAGES = NMAX <= 32 ? 8 : 4;
     static constexpr int QSTAGES = 4;
     static constexpr int B_BYTES = NMAX * WQ_K * 2;            // 4 KB or 16 KB
@@ -111,15 +112,15 @@ w4a16_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     uint64_t* afull = qempty + WQ_QSTAGES;
     uint64_t* aempty = afull + WQ_STAGES;
     uint64_t* accf = aempty + WQ_STAGES;
-    uint64_t* acce = accf + 2;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acce + 2);
+    uint64_t* acce = accf + WQ_ACCS;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acce + WQ_ACCS);
     volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < WQ_QSTAGES; ++s) { mbar_init(&qfull[s], 1); mbar_init(&qempty[s], WqCfg<NMAX>::DEQ_WARPS); }
         for (int s = 0; s < WQ_STAGES; ++s) { mbar_init(&afull[s], WqCfg<NMAX>::DEQ_WARPS / 2 + 1); mbar_init(&aempty[s], 1); }
-        for (int a = 0; a < 2; ++a) { mbar_init(&accf[a], 1); mbar_init(&acce[a], WqCfg<NMAX>::EPI_WARPS); }
+        for (int a = 0; a < WQ_ACCS; ++a) { mbar_init(&accf[a], 1); mbar_init(&acce[a], WqCfg<NMAX>::EPI_WARPS); }
         *abort = 0;
         fence_mbar_init();
     }
@@ -177,8 +178,8 @@ w4a16_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             for (int q = blockIdx.x; q < p.items && ok; q += P) {
                 const WqItem it = wq_item(p, q);
                 for (int c = it.c0; c < it.c1 && ok; ++c, ++ch) {
-                    const int a = ch & 1;
-                    const uint32_t aph = (ch >> 1) & 1;
+                    const int a = ch % WQ_ACCS;
+                    const uint32_t aph = (ch / WQ_ACCS) & 1;
                     if (!mbar_wait(&acce[a], aph ^ 1, kErrWaitAccEmpty, abort)) { ok = false; break; }
                     tc_fence_after();
                     const uint32_t d_tmem = tmem + uint32_t(a * NMAX);
@@ -281,7 +282,10 @@ w4a16_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     } else {
         // epilogue: TMEM lane quarter of the warp, one weight row and EC columns per thread
         constexpr int EC = WqCfg<NMAX>::EPI_COLS;
-        const int qr = warp & 3, e0 = (warp - (3 + WqCfg<NMAX>::DEQ_WARPS)) / 4 * EC;
+        // (two warps of a quarter share its columns evenly)
+        const int qr = warp & 3, half = (warp - (3 + WqCfg<NMAX>::DEQ_WARPS)) / 4;
+        const int share = EC == NMAX ? p.ntile : (p.ntile / 16 + 1) / 2 * 16;
+        const int e0 = half * share, e1 = min(p.ntile, e0 + share);
         const int r = qr * 32 + lane;
         int ch = 0;
         bool ok = true;
@@ -295,8 +299,8 @@ w4a16_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
 #pragma unroll
             for (int u = 0; u < EC; ++u) sum[u] = 0.f;
             for (int c = it.c0; c < it.c1; ++c, ++ch, --left) {
-                const int a = ch & 1;
-                const uint32_t aph = (ch >> 1) & 1;
+                const int a = ch % WQ_ACCS;
+                const uint32_t aph = (ch / WQ_ACCS) & 1;
                 if (left == 0) { left = cpg; ++gi; }
                 // the chunk's scale is requested before the wait, which hides its latency
                 const float sc = live ? __half2float(srow[gi]) : 0.f;
@@ -306,7 +310,7 @@ w4a16_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 const uint32_t base = tmem + uint32_t(a * NMAX + e0) + (uint32_t(qr * 32) << 16);
 #pragma unroll
                 for (int cb = 0; cb < EC / 16; ++cb) {
-                    if (e0 + cb * 16 < p.ntile) {
+                    if (e0 + cb * 16 < e1) {
                         float v[16];
                         tmem_ld16(base + uint32_t(cb * 16), v);
 #pragma unroll
@@ -324,7 +328,7 @@ w4a16_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
 #pragma unroll
             for (int u = 0; u < EC; ++u) {
                 const int64_t b = b0 + e0 + u;
-                if (e0 + u < p.ntile && b < p.batch) {
+                if (e0 + u < e1 && b < p.batch) {
                     if (p.atomic) atomicAdd(y + b * p.m + row, sum[u]);
                     else y[b * p.m + row] = sum[u];
                 }
