@@ -115,15 +115,15 @@ __device__ __forceinline__ void lora_shrink(const LoraParams& p, float* red, int
     }
 }
 
-// t[b][r] = scaling (A_a[r] . x[b]): one warp per (r, b), the warps of a CTA on
-// neighbouring rows b, which find a shared adapter's row in L1 (up to LORA_SWEEP rows:
-// 8 rows of rank 16 and 4096 columns leave the whole call 9 us faster than lora_shrink,
-// which has a CTA per unit)
+// t[b][r] = scaling (A_a[r] . x[b]): one warp per (r, b), dealt out over the CTAs from the
+// last one on, for the first ones gather beside it (up to LORA_SWEEP rows: 8 rows of rank
+// 16 and 4096 columns leave the whole call 9 us faster than lora_shrink, which has a CTA
+// per unit)
 __device__ __forceinline__ void lora_shrink_few(const LoraParams& p)
 {
     const int lane = threadIdx.x & 31;
     const int64_t items = p.batch * p.rank;
-    for (int64_t it = int64_t(blockIdx.x) * W4_WARPS + (threadIdx.x >> 5); it < items;
+    for (int64_t it = int64_t(threadIdx.x >> 5) * gridDim.x + (gridDim.x - 1 - blockIdx.x); it < items;
          it += int64_t(gridDim.x) * W4_WARPS) {
         const int r = int(it / p.batch);
         const int64_t b = it - r * p.batch;
