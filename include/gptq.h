@@ -494,7 +494,9 @@ int gptq_w4a16_moe(const uint16_t* x, int64_t tokens, const float* logits, int64
  *   a, b = elements i and rot_dim / 2 + i (interleaved == 0) or 2 i and 2 i + 1
  *   (interleaved != 0); every product and sum rounded to fp32.
  * quantize: for each group of group_size elements of a head the fp16 scale s
- *   and zero point z of rtn_quantize with bits = 4, codes c = clamp(rne(x / s)
+ *   and zero point z of rtn_quantize with bits = 4, but s from range * fp32(1 / 15)
+ *   in place of range / 15 (as fp32 tensors are divided by 15 on the GPU; another
+ *   fp16 value in about 3 of 100 000 groups), codes c = clamp(rne(x / s)
  *   + z, 0, 15).  An infinite element counts as the largest finite value of
  *   its sign, a NaN as the smallest.
  *

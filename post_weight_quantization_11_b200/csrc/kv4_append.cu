@@ -5,7 +5,7 @@
 //
 //   (a, b) -> (a c - b s, b c + a s)        pairs of the first rot_dim elements
 //   mn = min(0, min x), mx = max(0, max x)  over a group of group_size elements
-//   s = fp16((mx - mn) / 15), z = clamp(rne(-mn / s)), c = clamp(rne(x / s) + z)
+//   s = fp16((mx - mn) fp32(1 / 15)), z = clamp(rne(-mn / s)), c = clamp(rne(x / s) + z)
 //
 // A row (a token's head of q, k or v) is head_dim / 8 lanes of eight consecutive
 // elements: a warp has 256 / head_dim rows at a time and a few rows of one token in
@@ -89,14 +89,17 @@ __device__ __forceinline__ void store8(__half* p, const float (&x)[8])
     *reinterpret_cast<uint4*>(p) = v;
 }
 
-// group_params for 4 bits without its divisions: the same values.  Both quotients are
-// rounded correctly by div_rn_recip where they decide anything: a range over 2^20 gives
-// the largest scale either way, one below 15 2^-25 the smallest.
+// group_params for 4 bits without its divisions.  The scale is the range times the
+// rounded 1 / 15, as a division of fp32 tensors by 15 computes it on the GPU, so that a
+// program's own fp32 quantizer gives the same bytes; it differs by one unit of the fp16
+// scale from the quotient's in about 3 of 100 000 groups.  A range over 2^20 gives the
+// largest scale either way.  The zero point's quotient is rounded correctly by
+// div_rn_recip where it decides anything.
 __device__ __forceinline__ GroupQ group_params4(float mn, float mx)
 {
     constexpr float K15 = 0x1.111112p-4f;                  // RN(1 / 15)
     if (mn == mx) { mn = -1.f; mx = 1.f; }                 // all-zero group
-    const float s_pre = div_rn_recip(fminf(__fsub_rn(mx, mn), 1048576.f), 15.f, K15);
+    const float s_pre = __fmul_rn(fminf(__fsub_rn(mx, mn), 1048576.f), K15);
     unsigned short hb = __half_as_ushort(__float2half_rn(s_pre));
     hb = hb == 0 ? (unsigned short)0x0001u : hb >= 0x7c00u ? (unsigned short)0x7bffu : hb;
     GroupQ g;

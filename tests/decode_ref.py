@@ -146,7 +146,7 @@ def quantize(x, g):
         mn, mx = np.minimum(v.min(-1), f(0)), np.maximum(v.max(-1), f(0))
         flat = mn == mx
         mn, mx = np.where(flat, f(-1), mn), np.where(flat, f(1), mx)
-        s = ((mx - mn) / f(15)).astype(np.float16)
+        s = ((mx - mn) * f(1 / 15)).astype(np.float16)
         s = np.where(s == 0, np.float16(2.0 ** -24), np.where(np.isinf(s), np.float16(65504), s))
         sf = s.astype(f)
         z = np.clip(np.rint(-mn / sf), 0, 15).astype(f)

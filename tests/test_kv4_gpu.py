@@ -93,6 +93,28 @@ def test_append_equals_the_definition(T, hq, hkv, D, rot, inter, page, g, dt):
             + 1e-6 * np.abs(x64).max(-1, keepdims=True)).all()
 
 
+def test_append_equals_the_formula_in_fp32_tensors():
+    """Scales, zero points and codes of 200000 groups are those that the formula in
+    elementary fp32 tensor operations gives on the same GPU, to the last bit."""
+    T, D, g = 12500, 128, 32
+    gen = torch.Generator(device=DEV).manual_seed(31)
+    x = torch.randn(T, 4, D, generator=gen, device=DEV) * 3.0
+    cache = G.KV4Cache.empty(T // 16 + 1, 4, 16, D, g, DEV)
+    at = torch.arange(T, device=DEV)
+    G.gptq_kv4_append(x, x, None, at, None, cache)
+    v = x.unflatten(-1, (D // g, g))
+    lo, hi = v.amin(-1).clamp(max=0), v.amax(-1).clamp(min=0)
+    s = ((hi - lo) / 15).half()
+    z = torch.round(-lo / s.float()).clamp(0, 15)
+    c = (torch.round(v / s.float()[..., None]) + z[..., None]).clamp(0, 15).flatten(-2)
+    held = cache.v_params[at // 16, :, at % 16]
+    assert torch.equal(held[..., 0], s) and torch.equal(held[..., 1].float(), z)
+    place = torch.as_tensor(R.value_nibbles(D).astype(np.int64), device=DEV)
+    words = cache.v_codes[at // 16, :, at % 16].long()
+    got = (words[..., place // 8] >> (4 * (place % 8))) & 15
+    assert torch.equal(got, c.long())
+
+
 def test_append_unusual_values():
     """Infinities, NaN, rows of one sign, fp32 values beyond fp16, subnormals."""
     k = np.zeros((6, 1, 64), np.float32)
