@@ -28,10 +28,11 @@
 //  * The rows of an operand are the keys kv_key(g) of its eight: the same keys are
 //    then two neighbouring columns of the other product's operand, and the reads of
 //    shared memory hit every bank as often (keys) or twice (values).
-// Measured (B200, 32 heads on 8 of 128): 59 us for 32 ragged sequences of up to 8000 keys
-// (178 MB: 3.0 TB/s), 92 us for two of 131000 in groups of 64 (2.7 TB/s), 6 us for one of
-// 777; bound by about 670 instructions a tile and warp (176 unpack, 48 multiply), issued in
-// half of the cycles by four warps a scheduler, and by the uneven last round of chunks.
+// Measured (B200, 32 heads on 8 of 128): 54 us for 32 ragged sequences of up to 8000 keys
+// (178 MB: 3.3 TB/s), 82 us for two of 131000 in groups of 64 (3.0 TB/s), 6 us for one of
+// 777; bound by about 740 instructions a tile and warp (176 unpack, 32 to 48 multiply),
+// issued in 62 % of the cycles by four warps a scheduler, and by the uneven last round of
+// chunks.
 #include <cmath>
 
 #include "common.cuh"
@@ -637,8 +638,8 @@ template <int D> __global__ void __launch_bounds__(256) kv4_join_kernel(const Kv
 
 // Keys per chunk: a multiple of a CTA's round of tiles, and as few chunks as give each
 // SM eight CTAs (two rounds of four) when every sequence has the bound's length; twelve
-// from 8 sequences on, whose lengths may differ (32 ragged ones: 62 us against 67 with
-// eight; two of 131000: 95 us with eight, 105 with twelve)
+// from 8 sequences on, whose lengths may differ (32 ragged ones: 54 us with twelve or
+// sixteen, 58 with eight, 56 with twenty-four; two of 131000: 82 us with eight, 85 with six)
 struct KvPlan { int chunk, splits, row_tiles; bool cluster; size_t bytes; };
 
 KvPlan kv_plan(int64_t seqs, int hq, int hkv, int D, int64_t max_q, int64_t max_len, int64_t window)

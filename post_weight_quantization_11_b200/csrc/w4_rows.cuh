@@ -34,12 +34,12 @@
 // words of a row that are 16 bytes apart, so that a product stays inside 32 columns.
 // What it reaches: a pass over 32 KB (a step of every warp) takes 0.55 us from shared
 // memory alone, 8.8 TB/s on 148 SMs; in a sweep of 14336 x 4096 rows 4.3 TB/s (0.65 of the
-// measured copy rate) with 270 instructions a step and warp (of which 128 unpack and
-// multiply), issued in half of the cycles; four warps a scheduler do not hide more.
+// measured copy rate) with 258 instructions a step and warp (of which 128 unpack and
+// multiply), issued in 59 % of the cycles; four warps a scheduler do not hide more.
 // SPLIT: x in two fp16 parts (22 bits) for fp32 activations, scaled by a power
 // of two per column: W4_TWICE: each read of the rows is multiplied with both;
 // W4_BESIDE: up to four columns, the second parts are operand columns 4 .. 7 (half
-// the products; one token of 8 experts of 14336 x 4096: 59 us against 63 in all).
+// the products; one token of 8 experts of 14336 x 4096: 58 us against 63 in all).
 #pragma once
 
 #include <atomic>

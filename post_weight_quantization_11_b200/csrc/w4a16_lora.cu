@@ -10,8 +10,8 @@
 // the tcgen05 kernel's (w4a16_tc.cu), with t computed where the activations are put
 // in its order.  Partial results go through memory, not atomics: their order is
 // fixed.
-// Measured (B200): 11 us for one row and rank 16 of 4096 x 4096 (8.9 MB; gptq_w4a16_gemm
-// without adapters 11.7), 26 us for 8 requests of 14336 x 4096 with act-order (35 MB: two
+// Measured (B200): 10.5 us for one row and rank 16 of 4096 x 4096 (8.9 MB; gptq_w4a16_gemm
+// without adapters 11.7), 25 us for 8 requests of 14336 x 4096 with act-order (35 MB: two
 // rounds of row groups where 1.5 would do, the gather 3), 53 us for 93 rows of rank 64 of
 // 4096 x 11008 (36 of them the tcgen05 product).
 #include "common.cuh"
@@ -454,8 +454,8 @@ struct LoraPlan {
 // CTAs idle.  A group costs about 190 instructions a step and warp (two operands:
 // 260, bound by the matrix pipe) and 150 to join, and the slowest CTA counts.
 // More than 16 rows: the tcgen05 product, which needs groups of a multiple of 64 (14336
-// x 4096, groups of 128: 31 us against 43 at 16 rows, 56 against 44 at 32, 180 against
-// 75 at 128).
+// x 4096, groups of 128: 31 us against 37 at 16 rows, 56 against 38 at 32, 180 against
+// 45 at 128).
 LoraPlan lora_plan(int64_t T, int64_t m, int64_t d, int64_t g, int rank)
 {
     LoraPlan p{};

@@ -10,10 +10,10 @@
 // only the experts that a token chose are read, each once per eight of its tokens.  h
 // stays fp32 between them, as two fp16 parts in the second.  Partial results go through
 // memory, not atomics: their order is fixed.
-// Measured (B200, 8 experts of 14336 x 4096, top 2, groups of 128): 59 us for one token
-// (two experts, 183 MB: 3.1 TB/s), 229 us for 24 (all eight, 732 MB: 3.2 TB/s); bound by
-// the instructions that unpack (see w4_rows.cuh) and, for one token, by the start and end
-// of three kernels.
+// Measured (B200, 8 experts of 14336 x 4096, top 2, groups of 128): 58 us for one token
+// (two experts, 183 MB: 3.1 TB/s), 227 us for 24 (all eight, 732 MB: 3.2 TB/s; the copies
+// alone, without the products, 163); bound by the instructions that unpack (see
+// w4_rows.cuh) and, for one token, by the start and end of three kernels.
 #include <cfloat>
 #include <cmath>
 
