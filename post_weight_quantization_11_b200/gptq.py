@@ -672,6 +672,8 @@ def gptq_w4a16_lora(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor
     _on(adapter, "adapter", torch.int32, dev)
     _on(lora_scaling, "lora_scaling", torch.float32, dev)
     _tensor(qweight, "qweight")
+    if x.dim() != 2 or qweight.dim() != 2 or lora_a.dim() != 3:
+        raise ValueError("x must be batch x d_in, qweight d_out x d_in / 8, lora_a adapters x rank x d_in")
     b, d = x.shape
     m = qweight.shape[0]
     n, r = lora_a.shape[0], lora_a.shape[1]
@@ -710,11 +712,12 @@ def gptq_w4a16_moe(x: torch.Tensor, logits: torch.Tensor, qweight_in: torch.Tens
     _on(x, "x", torch.float16, dev)
     _on(logits, "logits", torch.float32, dev)
     _tensor(qweight_out, "qweight_out")
+    if x.dim() != 2 or logits.dim() != 2 or logits.shape[0] != x.shape[0] or qweight_out.dim() != 3:
+        raise ValueError("x must be tokens x d_model, logits tokens x experts, qweight_out E x d_model x "
+                         "d_ff / 8")
     T, d = x.shape
     E = logits.shape[1]
-    f = qweight_out.shape[-1] * 8
-    if logits.shape != (T, E):
-        raise ValueError("logits must be tokens x experts")
+    f = qweight_out.shape[2] * 8
     _packed_layer(qweight_in, scales_in, qzeros_in, perm_in, (E,), 2 * f, d, group_size, dev, "_in")
     _packed_layer(qweight_out, scales_out, qzeros_out, perm_out, (E,), d, f, group_size, dev, "_out")
     y = _out(y, "y", (T, d), torch.float32, x)
@@ -816,6 +819,8 @@ def gptq_kv4_append(k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
     if cos_sin is not None:
         _on(cos_sin, "cos_sin", torch.float32, dev)
         _on(positions, "positions", torch.int32, dev)
+        if cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be positions x rot_dim")
         n_pos, rot = cos_sin.shape
         if positions.shape != (T,):
             raise ValueError("positions must have one entry per token")
@@ -859,9 +864,9 @@ def gptq_kv4_attention(q: torch.Tensor, cache: KV4Cache, block_table: torch.Tens
     if q.dim() != 3 or q.shape[2] != D:
         raise ValueError("q must be tokens x q_heads x head_dim")
     T, hq = q.shape[0], q.shape[1]
-    B = seq_lens.shape[0]
+    B = seq_lens.shape[0] if seq_lens.dim() == 1 else -1
     if block_table.dim() != 2 or block_table.shape[0] != B or q_start.shape != (B + 1,):
-        raise ValueError("block_table must be seqs x width, q_start seqs + 1")
+        raise ValueError("block_table must be seqs x width, seq_lens seqs, q_start seqs + 1")
     width = block_table.shape[1]
     if max_seq_len is None:
         max_seq_len = width * cache.page_size

@@ -141,3 +141,23 @@ def test_w4a16_tc_of_a_gptq_layer():
     codes, zeros = oracle.unpack_int4(qw, qz, 1024, 8)
     assert (np.abs(t(y).astype(np.float64) - ref) <= _bound(t(x), codes, zeros, sc, 1024, 128,
                                                             t(res.perm))).all()
+
+
+@pytest.mark.parametrize("m,d,g,b", [(11008, 4096, 64, 16), (14336, 4096, 64, 1), (11008, 4096, 64, 32),
+                                     (11008, 4096, 64, 93), (4096, 11008, 64, 40), (300, 32768, 128, 17),
+                                     (500, 128, 64, 20), (257, 384, 128, 128), (129, 1920, 64, 129)])
+def test_w4a16_tc_short_groups_and_many_items(m, d, g, b):
+    """Groups of one stage and CTAs that go through several items, whose packed words
+    come in copies that items share or leave half used: exact values, three layers
+    each (words of another stage in one product of many show as whole wrong rows)."""
+    gen = torch.Generator(device=DEV).manual_seed(m + d + b)
+    for _ in range(3):
+        qw = torch.randint(-2 ** 31, 2 ** 31 - 1, (m, d // 8), dtype=torch.int32, device=DEV, generator=gen)
+        qz = torch.randint(0, 256, (m, (d // g + 1) // 2), dtype=torch.uint8, device=DEV, generator=gen)
+        sc = 2.0 ** -torch.randint(4, 7, (m, d // g), device=DEV, generator=gen).half()
+        x = torch.randint(-2, 3, (b, d), device=DEV, generator=gen).half()
+        y = G.gptq_w4a16_matmul(x, qw, sc, qz, g)
+        c = torch.stack([(qw >> (4 * i)) & 15 for i in range(8)], -1).reshape(m, -1, g).double()
+        z = torch.stack([qz & 15, qz >> 4], -1).reshape(m, -1)[:, :d // g].double()
+        w = ((c - z[..., None]) * sc.double()[..., None]).reshape(m, d)
+        assert torch.equal(y.double(), x.double() @ w.T)

@@ -171,3 +171,78 @@ def test_refusals():
         _run(x, lay, a, b, sc, ids, ws=torch.empty(16, dtype=torch.uint8, device=DEV))
     with pytest.raises(ValueError):
         _run(x, lay, a, b, sc, ids, y=torch.empty(2, 65, device=DEV))
+
+
+# ---- many rows: the joining kernel on the tensor cores ---------------------
+
+@pytest.mark.parametrize("d,g,r,m", [(128, 64, 8, 1), (128, -1, 40, 129), (384, 128, 256, 300),
+                                     (640, 64, 72, 31)])
+@pytest.mark.parametrize("ids", ["none", "one", "alternating", "runs", "all different"])
+def test_adapter_ids_of_many_rows(d, g, r, m, ids):
+    T, n = 37, 40
+    ids = {"none": [-1] * T, "one": [39] * T, "alternating": [3, -1, 3, 0] * 9 + [1],
+           "runs": [5] * 11 + [-1] * 2 + [6] * 13 + [5] * 11, "all different": list(range(T))}[ids]
+    c = _case(20 + d + r, T, m, d, g, r, n, d == 384, exact=True, ids=ids)
+    assert np.array_equal(_run(*c).cpu().numpy().astype(np.float64), R.lora(*c)[0])
+
+
+def test_scalings_far_apart_in_many_rows():
+    """The parts of t are taken after a power of two of each row: scalings far outside
+    fp16's range lose nothing."""
+    c = list(_case(21, 30, 90, 512, 64, 16, 6, False, ids=list(range(6)) * 5))
+    c[4] = np.array([1e30, -3e-30, 7e4, 1e-9, 1.0, 0.0], np.float32)
+    y = _run(*c).cpu().numpy()
+    ref, bound = R.lora(*c)
+    assert (np.abs(y - ref) <= bound).all()
+
+
+def test_infinities_stay_in_their_rows_of_many():
+    """An infinite activation, and infinite elements of one adapter's A and B: the rows
+    that have nothing to do with them are as without."""
+    ids = [0, 1, 2, -1] * 6
+    c = list(_case(22, 24, 64, 512, 128, 8, 3, False, exact=True, ids=ids))
+    clean = [v.copy() if isinstance(v, np.ndarray) else v for v in c]
+    c[0][4, 5] = np.inf                                    # a row of adapter 0
+    c[2][1, 3, 7] = np.inf
+    c[3][2, 9, 2] = np.inf
+    y = _run(*c).cpu().numpy()
+    assert not np.isfinite(y[4]).all() and not np.isfinite(y[1]).any() and not np.isfinite(y[2, 9])
+    keep = [t for t in range(24) if ids[t] in (0, -1) and t != 4]
+    ref, _ = R.lora(*clean)
+    assert np.array_equal(y[keep].astype(np.float64), ref[keep])
+    two = [t for t in range(24) if ids[t] == 2]
+    rows = [i for i in range(64) if i != 9]
+    assert np.array_equal(y[np.ix_(two, rows)].astype(np.float64), ref[np.ix_(two, rows)])
+
+
+def test_bad_indices_in_many_rows_are_recorded():
+    ids = [0, 2, -2, 1] * 6
+    c = list(_case(23, 24, 64, 256, 64, 8, 2, True, exact=True, ids=ids))
+    G.gptq_device_status()
+    y = _run(*c)
+    torch.cuda.synchronize()
+    assert G.gptq_device_status() == 0x201
+    assert np.array_equal(y.cpu().numpy().astype(np.float64), R.lora(*c)[0])   # handled as -1
+
+
+def test_graph_replay_of_many_rows_from_any_workspace():
+    c = _case(24, 60, 500, 1024, 64, 24, 4, True)
+    args = [_t(c[0]), _t(c[1]["qw"]), _t(c[1]["sc"]), _t(c[1]["qz"]), _t(c[2]), _t(c[3]), _t(c[5]), _t(c[4])]
+    y = torch.full((60, 500), 7.0, device=DEV)
+    ws = torch.full((G.gptq_w4a16_lora_workspace_bytes(60, 500, 1024, 64, 24),), 255, dtype=torch.uint8,
+                    device=DEV)
+    perm = _t(c[1]["perm"])
+    call = lambda: G.gptq_w4a16_lora(*args, 64, perm, y, ws)                   # noqa: E731
+    want = call().clone()
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        call()
+        call()
+    for k in range(2):
+        ws.fill_(255 * k)
+        y.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
