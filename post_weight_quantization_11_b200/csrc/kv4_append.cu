@@ -15,16 +15,18 @@
 // cache word is a lane's: shuffles, no shared memory.  Every operation is an IEEE
 // fp32 one with its own rounding (no contraction), so the codes are a function of
 // the inputs alone.
-// Measured (B200, 32 + 2 x 8 heads of 128, fp16, groups of 32): 32 us for 4001 tokens
-// (104 MB: 3.3 TB/s, 0.50 of the measured copy rate; bound by the latency of the row
-// loads, one round ahead, and by 190 instructions a round of two rows), 2.2 us for 16.
+// Measured (B200, 32 + 2 x 8 heads of 128, fp16, groups of 32): 26 us for 4001 tokens
+// (104 MB: 4.0 TB/s, 0.61 of the measured copy rate; bound by the latency of the row
+// loads, one round ahead, and by 185 instructions a round of two rows; six CTAs an SM: 32,
+// eight: 28, ten: 26; rows two rounds ahead, with the registers that takes: 36), 2.3 us
+// for 16.
 #include "common.cuh"
 #include "quant_common.cuh"
 #include "tc_common.cuh"
 
 namespace gptq {
 
-constexpr int KVA_THREADS = 128;
+constexpr int KVA_THREADS = 128, KVA_CTAS = 9;   // a CTA's threads, CTAs an SM (56 registers)
 
 struct KvAppend {
     const void* q;
@@ -111,7 +113,7 @@ __device__ __forceinline__ GroupQ group_params4(float mn, float mx)
 }
 
 template <typename T, int D, bool INTER>
-__global__ void __launch_bounds__(KVA_THREADS) kv4_append_kernel(const KvAppend p)
+__global__ void __launch_bounds__(KVA_THREADS, KVA_CTAS) kv4_append_kernel(const KvAppend p)
 {
     constexpr int NB = D / 32, LANES = D / 8, AT_ONCE = 32 / LANES;
     constexpr uint32_t ALL = 0xffffffffu;
