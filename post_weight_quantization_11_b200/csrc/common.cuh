@@ -67,6 +67,9 @@ constexpr int64_t kMaxRows = int64_t(1) << 24;
 
 // A kernel launched by launch_after waits here for its predecessors' results
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets such a kernel's CTAs take the places that this grid's leave (they wait there for
+// all of it); in every CTA, and not in the last kernel of a call
+__device__ __forceinline__ void pdl_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // A kernel on the stream that may start before its predecessor on it has ended
 // (it waits by pdl_wait)

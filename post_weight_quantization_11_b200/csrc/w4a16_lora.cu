@@ -10,9 +10,9 @@
 // the tcgen05 kernel's (w4a16_tc.cu), with t computed where the activations are put
 // in its order.  Partial results go through memory, not atomics: their order is
 // fixed.
-// Measured (B200): 10.5 us for one row and rank 16 of 4096 x 4096 (8.9 MB; gptq_w4a16_gemm
+// Measured (B200): 10 us for one row and rank 16 of 4096 x 4096 (8.9 MB; gptq_w4a16_gemm
 // without adapters 11.7), 25 us for 8 requests of 14336 x 4096 with act-order (35 MB: two
-// rounds of row groups where 1.5 would do, the gather 3), 53 us for 93 rows of rank 64 of
+// rounds of row groups where 1.5 would do, the gather 3), 52 us for 93 rows of rank 64 of
 // 4096 x 11008 (36 of them the tcgen05 product).
 #include "common.cuh"
 #include "tc_common.cuh"
@@ -182,6 +182,7 @@ lora_product_kernel(const __grid_constant__ CUtensorMap tm, const LoraParams p)
     float* xs = reinterpret_cast<float*>(smem + w4_at_x(NT) + w4_x_bytes(p.slice, p.chunk, false));
     W4Pipe pipe = w4_pipe<NT>(smem, &abort);
     // units in the order (slice, chunk of x, row group), shared evenly
+    pdl_go();
     const int64_t units = int64_t(p.slices) * p.groups * p.chunks;
     int64_t u = units * blockIdx.x / gridDim.x;
     const int64_t u1 = units * (blockIdx.x + 1) / gridDim.x;
@@ -224,6 +225,7 @@ __global__ void __launch_bounds__(W4_THREADS, 2) lora_front_kernel(const LoraPar
 {
     __shared__ __align__(16) float red[W4_WARPS * 128];
     __shared__ int ids[8];
+    pdl_go();
     const int64_t total = p.batch * p.d;
     for (int64_t i = (int64_t(blockIdx.x) * W4_THREADS + threadIdx.x) * 8; i < total;
          i += int64_t(gridDim.x) * (W4_THREADS * 8)) {

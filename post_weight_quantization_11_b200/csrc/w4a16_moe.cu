@@ -4,14 +4,15 @@
 //
 //   p = softmax(logits), S = top_k of it,  y = sum_S w_e D_e (silu(G_e x) * U_e x)
 //
-// Three kernels, each launched while the one before it drains: routes and h, the second
-// product over slices of its columns, and the joined y.  Every CTA works out the routes
-// for itself (a warp a token), the products are sweeps of the packed rows (w4_rows.cuh):
+// Three kernels, each begun while the one before it drains: routes and h, the second
+// product over slices of its columns, and the joined y.  Every CTA of the first two works
+// out the routes for itself (a warp a token; the second while the first ends: 227 us
+// against 231 with the first's routes read behind it), the products are sweeps of the packed rows (w4_rows.cuh):
 // only the experts that a token chose are read, each once per eight of its tokens.  h
 // stays fp32 between them, as two fp16 parts in the second.  Partial results go through
 // memory, not atomics: their order is fixed.
-// Measured (B200, 8 experts of 14336 x 4096, top 2, groups of 128): 58 us for one token
-// (two experts, 183 MB: 3.1 TB/s), 227 us for 24 (all eight, 732 MB: 3.2 TB/s; the copies
+// Measured (B200, 8 experts of 14336 x 4096, top 2, groups of 128): 56 us for one token
+// (two experts, 183 MB: 3.3 TB/s), 227 us for 24 (all eight, 732 MB: 3.2 TB/s; the copies
 // alone, without the products, 163); bound by the instructions that unpack (see
 // w4_rows.cuh) and, for one token, by the start and end of three kernels.
 #include <cfloat>
@@ -99,8 +100,7 @@ __device__ __forceinline__ void moe_route(const float* logits, int E, int k, int
     }
 }
 
-// What the second kernel reads of the routes: chunks of up to p.chunk pairs of
-// one expert, in expert order
+// The routes: chunks of up to p.chunk pairs of one expert, in expert order
 struct MoeRoutes {
     int chunks;
     int16_t expert[kMoePairs];
@@ -188,8 +188,9 @@ __global__ void __launch_bounds__(W4_THREADS, 1) moe_in_kernel(const __grid_cons
     uint4* x = reinterpret_cast<uint4*>(smem + w4_at_x(1));
     float* xs = reinterpret_cast<float*>(smem + w4_at_x(1) + w4_x_bytes(steps, p.chunk, false));
     W4Pipe pipe = w4_pipe<1>(smem, &abort);
+    pdl_go();
     moe_routes(p, r, cnt, off, coff);
-    if (blockIdx.x == 0) {                                 // for the second kernel
+    if (blockIdx.x == 0) {                                 // for the joining kernel
         const int* src = reinterpret_cast<const int*>(&r);
         for (int i = threadIdx.x; i < int(sizeof(MoeRoutes) / 4); i += blockDim.x)
             reinterpret_cast<int*>(p.routes)[i] = src[i];
@@ -229,6 +230,7 @@ __global__ void __launch_bounds__(W4_THREADS, 1) moe_out_kernel(const __grid_con
     extern __shared__ uint8_t smem_raw[];
     __shared__ int abort;
     __shared__ MoeRoutes r;
+    __shared__ int cnt[kMoeExperts], off[kMoeExperts], coff[kMoeExperts];
     __shared__ float undo[8];
     __shared__ uint32_t top[8];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -237,10 +239,9 @@ __global__ void __launch_bounds__(W4_THREADS, 1) moe_out_kernel(const __grid_con
     uint4* x = reinterpret_cast<uint4*>(smem + w4_at_x(1));
     float* xs = reinterpret_cast<float*>(smem + w4_at_x(1) + w4_x_bytes(p.slice, p.chunk, true));
     W4Pipe pipe = w4_pipe<1>(smem, &abort);
-    pdl_wait();
-    for (int i = threadIdx.x; i < int(sizeof(MoeRoutes) / 4); i += blockDim.x)
-        reinterpret_cast<int*>(&r)[i] = reinterpret_cast<const int*>(p.routes)[i];
-    __syncthreads();
+    pdl_go();
+    moe_routes(p, r, cnt, off, coff);                      // again, while the first kernel ends
+    bool waited = false;
     const int64_t units = int64_t(r.chunks) * p.slices * groups;
     int64_t u = units * blockIdx.x / gridDim.x;
     const int64_t u1 = units * (blockIdx.x + 1) / gridDim.x;
@@ -254,6 +255,8 @@ __global__ void __launch_bounds__(W4_THREADS, 1) moe_out_kernel(const __grid_con
         const int64_t row0 = int64_t(e) * p.d;
         const W4Stage st{smem_u32(x), smem_u32(xs), cols, uint32_t(steps * 256 * cols)};
         auto stage = [&]() {
+            if (!waited) pdl_wait();                       // for h
+            waited = true;
             w4_stage_split<1, FOLD>(
                 x, xs, undo, top, [&](int n) { return p.h + int64_t(list[n]) * p.f; },
                 p.po ? p.po + e * p.f : nullptr, k0 * W4_STEP, steps, cols, int(p.f), cols <= 4);
@@ -273,6 +276,7 @@ __global__ void __launch_bounds__(W4_THREADS, 1) moe_out_kernel(const __grid_con
                                                            g1 - g0, k0, steps, stage, done);
         u += g1 - g0;
     }
+    if (!waited) pdl_wait();
 }
 
 // y[t] = sum over the token's experts of w (sum over the slices of part)
@@ -391,11 +395,15 @@ extern "C" int gptq_w4a16_moe(const uint16_t* x, int64_t tokens, const float* lo
     KernelTimer kt(kKMoe, st);
     const int sms = device_sm_count();
     auto ctas = [&](int64_t units) { return (unsigned)std::min<int64_t>(sms, units); };
-    // Four column shares (64 rows of h a group, half the joins) where every CTA has many
-    // groups, eight (32 rows) where few groups would leave the last round half empty
+    // Four column shares (64 rows of h a group, half the joins) or eight (32 rows, finer
+    // rounds): by the slowest CTA's share, at the costs in moe_plan (24 tokens of 8 experts
+    // of 14336: 227 us with four, 229 with eight; one token: 56.5 and 55.5)
     const int64_t pairs = tokens * top_k;
     const int64_t chunks = std::max(std::min(pairs, n_experts), ceil_div(pairs, plan.chunk));
-    const bool fine = chunks * (d_ff / kMoeInRows<4>) < 8 * sms;
+    auto cost = [&](int kw, int rows) {
+        return ceil_div(chunks * (d_ff / rows), sms) * (ceil_div(d_model / W4_STEP, kw) * 190 + 100);
+    };
+    const bool fine = cost(8, kMoeInRows<8>) < cost(4, kMoeInRows<4>);
     const int fi = w4_fold(gi), fo = w4_fold(go);
     auto in = fine ? (fi == 4 ? moe_in_kernel<8, 4> : fi == 2 ? moe_in_kernel<8, 2> : moe_in_kernel<8, 1>)
                    : (fi == 4 ? moe_in_kernel<4, 4> : fi == 2 ? moe_in_kernel<4, 2> : moe_in_kernel<4, 1>);

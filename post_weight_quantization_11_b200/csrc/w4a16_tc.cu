@@ -70,6 +70,7 @@ struct WqParams {
     int items;
     int atomic;         // ksplit > 1: y += (zeroed first)
     int64_t split_stride;   // or, not atomic: elements between the splits' own outputs
+    int go;                 // the caller joins them in a kernel launched behind this one
 };
 
 struct WqItem { int rt, nt, ks, c0, c1; }; // chunk range [c0, c1)
@@ -129,6 +130,7 @@ w4a16_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    if (p.go) pdl_go();
     const int P = gridDim.x;
     const int spc = p.chunk / WQ_K;                          // stages per chunk
     const int spg = int(p.gsz / WQ_K), cpg = spg / spc;      // stages and chunks per group
@@ -412,6 +414,7 @@ int wq_run(const WqPlan& plan, const __half* xp, int64_t batch, const uint32_t* 
     p.items = plan.n_rt * plan.n_nt * plan.ksplit;
     p.split_stride = split_stride;
     p.atomic = split_stride == 0 && p.ksplit > 1;
+    p.go = split_stride != 0;
     if (p.atomic &&
         cudaMemsetAsync(y, 0, sizeof(float) * size_t(batch) * size_t(m), st) != cudaSuccess)
         return GPTQ_ERR_CUDA;
