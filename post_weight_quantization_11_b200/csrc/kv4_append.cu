@@ -16,8 +16,8 @@
 // fp32 one with its own rounding (no contraction), so the codes are a function of
 // the inputs alone.
 // Measured (B200, 32 + 2 x 8 heads of 128, fp16, groups of 32): 26 us for 4001 tokens
-// (104 MB: 4.0 TB/s, 0.61 of the measured copy rate; bound by the latency of the row
-// loads, one round ahead, and by 185 instructions a round of two rows; six CTAs an SM: 32,
+// (104 MB: 4.0 TB/s, 0.61 of the measured copy rate; bound by 200 instructions a round
+// of two rows, issued in 75 % of the slots, with rows loaded one round ahead; six CTAs an SM: 32,
 // eight: 28, ten: 26; rows two rounds ahead, with the registers that takes: 36), 2.3 us
 // for 16.
 #include "common.cuh"

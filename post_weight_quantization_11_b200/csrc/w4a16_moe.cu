@@ -7,10 +7,10 @@
 // Three kernels, each begun while the one before it drains: routes and h, the second
 // product over slices of its columns, and the joined y.  Every CTA of the first two works
 // out the routes for itself (a warp a token; the second while the first ends: 227 us
-// against 231 with the first's routes read behind it), the products are sweeps of the packed rows (w4_rows.cuh):
-// only the experts that a token chose are read, each once per eight of its tokens.  h
-// stays fp32 between them, as two fp16 parts in the second.  Partial results go through
-// memory, not atomics: their order is fixed.
+// against 231 with the first's routes read behind it), the products are sweeps of the
+// packed rows (w4_rows.cuh): only the experts that a token chose are read, each once per
+// eight of its tokens.  h stays fp32 between them, as two fp16 parts in the second.
+// Partial results go through memory, not atomics: their order is fixed.
 // Measured (B200, 8 experts of 14336 x 4096, top 2, groups of 128): 56 us for one token
 // (two experts, 183 MB: 3.3 TB/s), 227 us for 24 (all eight, 732 MB: 3.2 TB/s; the copies
 // alone, without the products, 163); bound by the instructions that unpack (see
