@@ -139,3 +139,59 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for lay, g, i in zip(lays, got, inp):
         _check(lay, g, *i)
+
+
+def test_calls_back_to_back_equal_calls_one_by_one():
+    """Kernels begin while the ones before them end: a chain of calls, each on the last
+    one's output and all in one workspace, gives what it gives with a wait in between
+    (eagerly, in two streams at once and replayed)."""
+    rng = np.random.default_rng(41)
+    d, f, E = 1024, 512, 8
+    lay, inn, down = (R.packed_layer(rng, *s) for s in ((d, d, 64, True), (2 * f, d, 64, True, False, (E,)),
+                                                        (d, f, 64, False, False, (E,))))
+    dv = {n: [_t(v[k]) for k in ("qw", "sc", "qz", "perm")]
+          for n, v in (("lay", lay), ("inn", inn), ("down", down))}
+    a = _t((rng.standard_normal((5, 32, d)) * 0.02).astype(np.float16))
+    b = _t((rng.standard_normal((5, d, 32)) * 0.02).astype(np.float16))
+    scaling = _t(np.array([1.0, -2.0, 0.5, 1.5, 0.25], np.float32))
+    x = _t(rng.standard_normal((60, d)).astype(np.float16))
+    ids = _t(rng.integers(-1, 5, 60).astype(np.int32))
+    logits = _t(rng.standard_normal((60, E)).astype(np.float32))
+    logits[3] = float("-inf")                               # a token without experts
+    nbytes = max(G.gptq_w4a16_lora_workspace_bytes(T, d, d, 64, 32) for T in (1, 7, 16, 17, 33, 60))
+    nbytes = max(nbytes, G.gptq_w4a16_moe_workspace_bytes(60, E, 2, d, f))
+
+    def chain(ws, wait):
+        h, all_y = x, []
+        for T in (60, 7, 33, 1, 17, 60, 16):
+            q, s, z, perm = dv["lay"]
+            y = G.gptq_w4a16_lora(h[:T], q, s, z, a, b, ids[:T], scaling, 64, perm if T != 7 else None, ws=ws)
+            wait()
+            m = G.gptq_w4a16_moe(torch.tanh(y).half(), logits[:T], *dv["inn"][:3], *dv["down"][:3], 2, 64,
+                                 perm_in=dv["inn"][3], ws=ws)
+            wait()
+            all_y += [y, m]
+            h = torch.cat([torch.tanh(m).half(), x[T:]])
+        return all_y
+
+    space = [torch.full((nbytes,), 255, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    want = chain(space[0], torch.cuda.synchronize)
+    none = lambda: None                                    # noqa: E731
+    for _ in range(3):
+        assert all(torch.equal(u, v) for u, v in zip(chain(space[0], none), want))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for st, ws in zip(streams, space):
+        with torch.cuda.stream(st):
+            got.append([chain(ws, none) for _ in range(2)])
+    torch.cuda.synchronize()
+    assert all(torch.equal(u, v) for runs in got for run in runs for u, v in zip(run, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = chain(space[0], none)
+    for k in range(2):
+        space[0].fill_(255 * k)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(u, v) for u, v in zip(out, want))
