@@ -541,7 +541,7 @@ int gptq_kv4_append(const void* q, int64_t q_stride, const void* k, int64_t k_st
  * gptq_kv4_append fills.  Sequence b has seq_lens[b] keys, the new tokens'
  * among them, and n = q_start[b + 1] - q_start[b] queries, its last n tokens;
  * query i sees the keys j <= seq_lens[b] - n + i and, with window > 0, j >
- * seq_lens[b] - n + i - window:
+ * seq_lens[b] - n + i - window (a window of max_seq_len or more is none):
  *   out[t][h] = sum_j softmax_j(scale q[t][h] . K[j][h']) V[j][h'],
  *   h' = h / (q_heads / kv_heads).  A query that sees no key gets 0.
  * q, out: tokens x q_heads x head_dim fp16.  Rows of out behind q_start[seqs]

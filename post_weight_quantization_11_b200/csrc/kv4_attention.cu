@@ -727,6 +727,9 @@ extern "C" int gptq_kv4_attention(const uint16_t* q, int64_t tokens, int64_t seq
         !aligned(q_start, 4) || !aligned16(out) || !aligned16(ws))
         return GPTQ_ERR_INVALID_ARG;
     if (max_q_len > (int64_t(1) << 24)) return GPTQ_ERR_SHAPE;
+    // no query reaches back further than max_seq_len keys (and a caller's "no limit" may be
+    // the largest number there is: sums with it would wrap)
+    if (window >= max_seq_len) window = 0;
     if (ws_bytes < gptq_kv4_attention_workspace_bytes(seqs, q_heads, kv_heads, head_dim, max_q_len,
                                                       max_seq_len))
         return GPTQ_ERR_INVALID_ARG;

@@ -1,0 +1,47 @@
+"""gptq_kv4_attention at the ends of its ranges: windows longer than the cache."""
+import numpy as np
+import pytest
+
+from tests.test_kv4_gpu import _attn_case, _attn_check, _attn_ref, _attn_run
+
+pytestmark = pytest.mark.gpu
+
+# (lengths, queries, q_heads, kv_heads, head_dim, page, group): in one chunk, in chunks that a
+# cluster joins, in chunks that are joined through memory (few long ones, many of them)
+PATHS = {"one chunk": ([200, 77], [1, 2], 8, 2, 64, 16, 32),
+         "cluster": ([777], [1], 8, 2, 128, 16, 128),
+         "cluster, five rows": ([1500, 600], [5, 5], 3, 3, 128, 32, 64),
+         "joined": ([9000, 40], [1, 1], 4, 1, 64, 16, 64),
+         "joined, five rows": ([9000], [5], 2, 2, 64, 64, 64),
+         "joined, many": ([700 + 37 * i for i in range(40)], [1] * 40, 16, 8, 64, 16, 32)}
+
+
+def _case(path, seed=0):
+    return _attn_case(seed, *PATHS[path])
+
+
+def _run(c, window=0):
+    return _attn_run(c, window).cpu().numpy().astype(np.float64)
+
+
+# ---- windows --------------------------------------------------------------
+
+@pytest.mark.parametrize("window", [2 ** 63 - 1, 2 ** 62, 2 ** 31, 9000, 8999])
+@pytest.mark.parametrize("path", list(PATHS))
+def test_a_window_longer_than_the_sequences_is_none(path, window):
+    """Whatever the caller has for 'no limit' gives what no window gives."""
+    c = _case(path)
+    got = _run(c, window)
+    want, bound = _attn_ref(c, min(window, 1 << 30))
+    assert (np.abs(got - want) <= bound).all()
+    if window >= c["table"].shape[1] * c["page"]:
+        assert np.array_equal(got, _run(c))
+
+
+@pytest.mark.parametrize("window", [2 ** 63 - 1, 2 ** 62, 2 ** 31])
+def test_a_long_window_with_more_queries_than_keys(window):
+    """Rows before the first key see nothing, with any window."""
+    c = _attn_case(1, [0, 2, 40, 7], [1, 5, 0, 9], 4, 2, 64, 16, 32)
+    assert np.array_equal(_run(c, window), _attn_check(c))
+    c = _attn_case(2, [3, 900], [9, 1], 8, 2, 128, 16, 64)
+    assert np.array_equal(_run(c, window), _attn_check(c))
