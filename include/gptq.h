@@ -543,7 +543,8 @@ int gptq_kv4_append(const void* q, int64_t q_stride, const void* k, int64_t k_st
  * query i sees the keys j <= seq_lens[b] - n + i and, with window > 0, j >
  * seq_lens[b] - n + i - window (a window of max_seq_len or more is none):
  *   out[t][h] = sum_j softmax_j(scale q[t][h] . K[j][h']) V[j][h'],
- *   h' = h / (q_heads / kv_heads).  A query that sees no key gets 0.
+ *   h' = h / (q_heads / kv_heads).  A query that sees no key gets 0; one with an
+ *   infinite or NaN element that sees a key gets NaN.
  * q, out: tokens x q_heads x head_dim fp16.  Rows of out behind q_start[seqs]
  *    are left as they are.
  * block_table: seqs x table_width int32, the page of each page_size keys of a

@@ -560,7 +560,8 @@ __global__ void __launch_bounds__(KV_WARPS * 32, KvShape<D, G>::CTAS) kv4_attent
         }
         if (p.cluster) { cm[r] = top; cl[r] = sum; }
         else if (p.splits > 1) { dst[8 * D + r] = top; dst[8 * D + 8 + r] = sum; }
-        const float scale = p.splits > 1 ? 1.f : sum > 0.f ? 1.f / sum : 0.f;
+        // (sum 0: no key is seen; NaN, from a query that is not finite, goes on to the row)
+        const float scale = p.splits > 1 ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
         for (int w = 0; w < KV_WARPS; ++w) wm[w][r] = c[w] * scale;
     }
@@ -601,7 +602,7 @@ __global__ void __launch_bounds__(KV_WARPS * 32, KvShape<D, G>::CTAS) kv4_attent
                 v.x = fmaf(c, u.x, v.x); v.y = fmaf(c, u.y, v.y);
                 v.z = fmaf(c, u.z, v.z); v.w = fmaf(c, u.w, v.w);
             }
-            const float inv = sum > 0.f ? 1.f / sum : 0.f;
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
             put(r, e - r * D, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
         }
         cluster_sync();                                    // the others have read this CTA's memory
@@ -633,7 +634,7 @@ template <int D> __global__ void __launch_bounds__(256) kv4_join_kernel(const Kv
     }
     __half* dst = p.out + kv_row(p, sp.s0, hk, rt * 8 + r) * D;
 #pragma unroll
-    for (int e = 0; e < E; ++e) dst[e * 32 + lane] = __float2half_rn(sum > 0.f ? v[e] / sum : 0.f);
+    for (int e = 0; e < E; ++e) dst[e * 32 + lane] = __float2half_rn(sum == 0.f ? 0.f : v[e] / sum);
 }
 
 // Keys per chunk: a multiple of a CTA's round of tiles, and as few chunks as give each

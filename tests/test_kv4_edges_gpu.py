@@ -1,4 +1,5 @@
-"""gptq_kv4_attention at the ends of its ranges: windows longer than the cache."""
+"""gptq_kv4_attention at the ends of its ranges: windows longer than the cache,
+queries that are not finite."""
 import numpy as np
 import pytest
 
@@ -45,3 +46,27 @@ def test_a_long_window_with_more_queries_than_keys(window):
     assert np.array_equal(_run(c, window), _attn_check(c))
     c = _attn_case(2, [3, 900], [9, 1], 8, 2, 128, 16, 64)
     assert np.array_equal(_run(c, window), _attn_check(c))
+
+
+# ---- queries that are not finite -------------------------------------------
+
+@pytest.mark.parametrize("value", [np.nan, np.inf, -np.inf])
+@pytest.mark.parametrize("path", list(PATHS))
+def test_a_query_that_is_not_finite_gives_a_row_that_is_not(path, value):
+    """However the keys are split: no such row comes out as numbers, and no other row
+    changes beyond its bound."""
+    c = _case(path, 3)
+    want, bound = _attn_ref(c)
+    c["q"][0, 1, 5] = value
+    got = _run(c)
+    assert not np.isfinite(got[0, 1]).any()
+    keep = np.ones(got.shape[:2], bool)
+    keep[0, 1] = False
+    assert (np.abs(got - want) <= bound)[keep].all()
+
+
+def test_a_query_that_is_not_finite_and_sees_no_key_is_zero():
+    c = _attn_case(4, [0, 300], [2, 1], 4, 2, 64, 16, 32)
+    c["q"][:2] = np.nan
+    got = _run(c)
+    assert not got[:2].any() and np.isfinite(got[2]).all()
