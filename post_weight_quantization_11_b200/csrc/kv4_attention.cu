@@ -15,9 +15,12 @@
 //    eight bulk copies (codes and parameters of keys and values), one instruction of as
 //    many lanes, KV_RING tiles ahead on one mbarrier a tile.
 //  * Scores: S^T = K q^T on m16n8k16 mma.sync, keys as rows.  A code alone in a half
-//    word is the fp16 subnormal c 2^-24 (low nibble) or c 2^-20 (high): one AND per
-//    operand register.  A key's scale and zero point are applied to the product:
-//    s (sum c q - z sum q).
+//    word is the fp16 subnormal c 2^-24 (low nibble) or c 2^-20 (high), one AND per
+//    operand register; one packed FMA more makes it (c - z) 2^-14, exact and a normal
+//    number.  (The matrix pipe aligns subnormals by their exponent field: with the codes as
+//    they are and the zero point applied to the product, s (sum c q - z sum q), a channel
+//    in which the query is large and the keys small cost the scores up to 17 times the fp32
+//    sums' bound.  32 ragged sequences took 54 us then, two of 131000 keys 82.)
 //  * out^T = V^T p: two keys' words of the same elements, merged half by half, give
 //    operand registers of two keys again by one AND.  A value's scale goes into its
 //    probability: u = p s, in two fp16 parts (22 bits), scaled by a power of two that
@@ -28,8 +31,8 @@
 //  * The rows of an operand are the keys kv_key(g) of its eight: the same keys are
 //    then two neighbouring columns of the other product's operand, and the reads of
 //    shared memory hit every bank as often (keys) or twice (values).
-// Measured (B200, 32 heads on 8 of 128): 54 us for 32 ragged sequences of up to 8000 keys
-// (178 MB: 3.3 TB/s), 82 us for two of 131000 in groups of 64 (3.0 TB/s), 6 us for one of
+// Measured (B200, 32 heads on 8 of 128): 57 us for 32 ragged sequences of up to 8000 keys
+// (178 MB: 3.1 TB/s), 84 us for two of 131000 in groups of 64 (2.9 TB/s), 6 us for one of
 // 777; bound by about 740 instructions a tile and warp (176 unpack, 32 to 48 multiply),
 // issued in 62 % of the cycles by four warps a scheduler, and by the uneven last round of
 // chunks.
@@ -77,13 +80,29 @@ __device__ __forceinline__ float ex2(float x)
     return r;
 }
 
-// Two codes, c 2^-14 / scale each -> (c - 8) 2^-14, exact: normal numbers around 0, so
+// Two codes of values, c 2^-14 / scale each -> (c - 8) 2^-14, exact: normal numbers around 0, so
 // that neither the matrix pipe's alignment of subnormals nor the rounding of long sums of
 // codes of one sign costs bits of their difference to the zero points
 __device__ __forceinline__ uint32_t kv_center(uint32_t v, float scale)
 {
     const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&v), __float2half2_rn(scale),
                               __float2half2_rn(-8.f * 0x1p-14f));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// Minus the zero point (the high half of a parameter word), times 2^-14, twice
+__device__ __forceinline__ uint32_t kv_minus(uint32_t param)
+{
+    const uint32_t z = __byte_perm(param, param, 0x3232);
+    const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&z), __float2half2_rn(-0x1p-14f));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// Two codes of a key, c 2^-14 / scale each -> (c - z) 2^-14, exact
+__device__ __forceinline__ uint32_t kv_sub(uint32_t v, float scale, uint32_t minus)
+{
+    const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&v), __float2half2_rn(scale),
+                              *reinterpret_cast<const __half2*>(&minus));
     return *reinterpret_cast<const uint32_t*>(&r);
 }
 
@@ -191,7 +210,7 @@ __global__ void __launch_bounds__(KV_WARPS * 32, KvShape<D, G>::CTAS) kv4_attent
     constexpr int NB = Sh::NB, GB = Sh::GB;
     constexpr uint32_t LO = 0x000F000Fu, HI = 0x00F000F0u, ALL = 0xffffffffu;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ __align__(16) float qsum[G][8];             // read in pairs
+    __shared__ float poison[8];
     __shared__ float wm[KV_WARPS][8], wl[KV_WARPS][8], cm[8], cl[8];
     __shared__ __align__(8) uint64_t bars[KV_WARPS * KV_RING];
     __shared__ int abort;
@@ -263,13 +282,13 @@ __global__ void __launch_bounds__(KV_WARPS * 32, KvShape<D, G>::CTAS) kv4_attent
     for (int i = 0; i < KV_RING; ++i) issue();
 
     // the queries' operand (row g of the tile: elements 32 i + 8 t .. of block i, in the
-    // order of a word's nibbles) and the sums over each group
+    // order of a word's nibbles)
     uint32_t qf[NB][4];
     {
         const int r = HALF ? g & 3 : g;
         const bool on = r < sp.rows;
         const __half* src = p.q + kv_row(p, sp.s0, hk, rt * 8 + (on ? r : 0)) * D;
-        float qs[G] = {};
+        float sum = 0.f;                                   // finite where the elements are
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
             uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -278,19 +297,16 @@ __global__ void __launch_bounds__(KV_WARPS * 32, KvShape<D, G>::CTAS) kv4_attent
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const float2 f = __half22float2(h[e]);
-                qs[i / GB] += f.x + f.y;
+                sum += f.x + f.y;
             }
             qf[i][0] = __byte_perm(v.x, v.z, 0x5410);      // elements 0, 4
             qf[i][1] = __byte_perm(v.y, v.w, 0x5410);      // 2, 6
             qf[i][2] = __byte_perm(v.x, v.z, 0x7632);      // 1, 5
             qf[i][3] = __byte_perm(v.y, v.w, 0x7632);      // 3, 7
         }
-#pragma unroll
-        for (int k = 0; k < G; ++k) {
-            qs[k] += __shfl_xor_sync(ALL, qs[k], 1);
-            qs[k] += __shfl_xor_sync(ALL, qs[k], 2);
-            if (warp == 0 && t == 0) qsum[k][g] = qs[k] * 0x1p-24f;
-        }
+        sum += __shfl_xor_sync(ALL, sum, 1);
+        sum += __shfl_xor_sync(ALL, sum, 2);
+        if (warp == 0 && t == 0) poison[g] = sum * 0.f;
     }
     __syncthreads();
     // rows 2 t and 2 t + 1: the keys they see
@@ -310,7 +326,10 @@ __global__ void __launch_bounds__(KV_WARPS * 32, KvShape<D, G>::CTAS) kv4_attent
     float o[NB][2][4] = {};                                // [block][nibbles 0, 2 | 1, 3]
     uint32_t top_exp = 0;                                  // biased fp16 exponent of the largest value scale
     float factor = 0x1p21f;                                // 2^(21 - top_exp): u < 2^(7 + KV_LAZY)
-    const float up = p.scale * 0x1p24f;
+    const float up = p.scale * 0x1p14f;
+    // what the scores of rows 2 t, 2 t + 1 begin with: 0, or NaN for a query that is not
+    // finite (an infinity alone can make every score -inf, which is no key seen)
+    const float start[2] = {poison[2 * t], poison[2 * t + 1]};
     int slot = 0;
     uint32_t phase = 0;
     for (int tile = warp; tile < tiles; tile += KV_WARPS) {
@@ -337,34 +356,36 @@ __global__ void __launch_bounds__(KV_WARPS * 32, KvShape<D, G>::CTAS) kv4_attent
                 }
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sc[h][e] = 0.f;
+            for (int e = 0; e < 4; ++e) sc[h][e] = start[e & 1];
 #pragma unroll
             for (int k = 0; k < G; ++k) {
-                float lo[4], hi[4];
+                float sx[2];
+                uint32_t mz[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {              // scale, and minus the zero point twice
+                    const uint32_t v = *reinterpret_cast<const uint32_t*>(
+                        base + 2 * Sh::CODES + ((h * 16 + i * 8 + kv_key(g)) * G + k) * 4);
+                    sx[i] = __half2float(__ushort_as_half((unsigned short)v)) * up;
+                    mz[i] = kv_minus(v);
+                }
+                float dot[4];
 #pragma unroll
                 for (int i = 0; i < GB; ++i) {
                     const uint32_t a = kw[0][k * GB + i], c = kw[1][k * GB + i];
                     const uint32_t a8 = a >> 8, c8 = c >> 8;
                     const uint32_t (&f)[4] = qf[k * GB + i];
-                    if (i == 0) {
-                        mma_16816_first(lo, a & LO, c & LO, a8 & LO, c8 & LO, f[0], f[1]);
-                        mma_16816_first(hi, a & HI, c & HI, a8 & HI, c8 & HI, f[2], f[3]);
-                    } else {
-                        mma_16816(lo, a & LO, c & LO, a8 & LO, c8 & LO, f[0], f[1]);
-                        mma_16816(hi, a & HI, c & HI, a8 & HI, c8 & HI, f[2], f[3]);
-                    }
+                    const uint32_t l0 = kv_sub(a & LO, 1024.f, mz[0]), l1 = kv_sub(c & LO, 1024.f, mz[1]);
+                    const uint32_t l2 = kv_sub(a8 & LO, 1024.f, mz[0]), l3 = kv_sub(c8 & LO, 1024.f, mz[1]);
+                    const uint32_t h0 = kv_sub(a & HI, 64.f, mz[0]), h1 = kv_sub(c & HI, 64.f, mz[1]);
+                    const uint32_t h2 = kv_sub(a8 & HI, 64.f, mz[0]), h3 = kv_sub(c8 & HI, 64.f, mz[1]);
+                    if (i == 0) mma_16816_first(dot, l0, l1, l2, l3, f[0], f[1]);
+                    else mma_16816(dot, l0, l1, l2, l3, f[0], f[1]);
+                    mma_16816(dot, h0, h1, h2, h3, f[2], f[3]);
                 }
-                const float2 qs = *reinterpret_cast<const float2*>(&qsum[k][2 * t]);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    float2 sz = __half22float2(*reinterpret_cast<const __half2*>(
-                        base + 2 * Sh::CODES + ((h * 16 + i * 8 + kv_key(g)) * G + k) * 4));
-                    sz.x *= up;
-                    float2 v = fma2(make_float2(hi[2 * i], hi[2 * i + 1]), make_float2(0.0625f, 0.0625f),
-                                    make_float2(lo[2 * i], lo[2 * i + 1]));
-                    v = fma2(make_float2(-sz.y, -sz.y), qs, v);
-                    v = fma2(make_float2(sz.x, sz.x), v,
-                             make_float2(sc[h][2 * i], sc[h][2 * i + 1]));
+                    const float2 v = fma2(make_float2(sx[i], sx[i]), make_float2(dot[2 * i], dot[2 * i + 1]),
+                                          make_float2(sc[h][2 * i], sc[h][2 * i + 1]));
                     sc[h][2 * i] = v.x;
                     sc[h][2 * i + 1] = v.y;
                 }

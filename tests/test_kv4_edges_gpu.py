@@ -70,3 +70,12 @@ def test_a_query_that_is_not_finite_and_sees_no_key_is_zero():
     c["q"][:2] = np.nan
     got = _run(c)
     assert not got[:2].any() and np.isfinite(got[2]).all()
+
+
+def test_an_infinite_query_whose_every_score_is_minus_infinity():
+    """Rows that see one key: its score is an infinity of either sign, the row is NaN."""
+    for path in PATHS:
+        c = _case(path, 5)
+        c["q"][0, 0, 3], c["q"][0, 1, 3] = np.inf, -np.inf
+        got = _attn_run(c, 1).cpu().numpy()
+        assert np.isnan(got[0, :2]).all() and np.isfinite(got[1:]).all() and np.isfinite(got[0, 2:]).all()
