@@ -761,8 +761,10 @@ class KV4Cache:
     @classmethod
     def empty(cls, pages: int, kv_heads: int, page_size: int, head_dim: int,
               group_size: int = -1, device="cuda"):
-        """A cache of zeros."""
+        """A cache of zeros.  group_size: a divisor of head_dim, or -1 (one group a head)."""
         g = head_dim if group_size == -1 else group_size
+        if g < 1 or head_dim % g != 0:
+            raise ValueError(f"group_size must divide head_dim or be -1, got {group_size} of {head_dim}")
         codes = lambda: torch.zeros(pages, kv_heads, page_size, head_dim // 8,      # noqa: E731
                                     dtype=torch.int32, device=device)
         params = lambda: torch.zeros(pages, kv_heads, page_size, head_dim // g, 2,  # noqa: E731
