@@ -429,7 +429,8 @@ int gptq_w4a16_matmul(const uint16_t* x, int64_t batch, const uint32_t* qweight,
  *    adjacent; adjacent rows share the adapter's loads.
  * rank: a multiple of 8, 8 .. 256.  0 <= batch <= 65535 (0: no-op);
  *    0 <= n_adapters <= 65536 (0: lora_* may be NULL).
- * ws: gptq_w4a16_lora_workspace_bytes(...) bytes, not shared with a call that may run at the same time.
+ * ws: gptq_w4a16_lora_workspace_bytes(...) bytes, which serve every smaller batch too; not
+ *    shared with a call that may run at the same time.
  * All sums are fp32 (beyond 16 rows x A^T enters the product with B as two fp16
  * parts, which keep 22 bits of an element and nothing below 2^-38 of the row's
  * largest); the result does not depend on timing (no atomics on y).

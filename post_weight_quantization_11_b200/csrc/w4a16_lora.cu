@@ -448,11 +448,31 @@ struct LoraPlan {
     bool tc;                                     // the tcgen05 product
     WqPlan wq;
     int nt, chunk, chunks, slice, slices, groups;
-    size_t at_xp, at_part, bytes;
+    size_t at_xp, at_part;
 };
 
-// Rows of x that are staged together (one operand of 8, or two) and slices of the
-// columns: as few as fit beside the ring, or more where few row groups would leave
+// Rows of x that the sweep stages together (one operand of 8, or two)
+struct LoraChunk {
+    int nt, rows;
+    int slices, most;        // slices of the columns: the fewest that fit beside the ring, the most
+                             // that a plan has (steps of fewer columns than the shares gain nothing)
+};
+
+LoraChunk lora_chunk(int64_t T, int64_t d)
+{
+    LoraChunk c{};
+    c.nt = T > W4_COLS ? 2 : 1;
+    c.rows = int(std::min<int64_t>(T, W4_COLS * c.nt));
+    const int so = int(d / W4_STEP), room = (c.nt == 1 ? 72 : 56) * 1024;
+    const int steps = std::min(so, room / (256 * c.rows + 128 * c.nt));
+    c.slices = (so + steps - 1) / steps;
+    c.most = std::max(c.slices, (so + LORA_KW - 1) / LORA_KW);
+    return c;
+}
+
+bool lora_tc(int64_t T, int64_t g) { return T > LORA_SWEEP && g % 64 == 0; }
+
+// Slices of the columns: as few as fit, or more where few row groups would leave
 // CTAs idle.  A group costs about 190 instructions a step and warp (two operands:
 // 260, bound by the matrix pipe) and 150 to join, and the slowest CTA counts.
 // More than 16 rows: the tcgen05 product, which needs groups of a multiple of 64 (14336
@@ -461,31 +481,49 @@ struct LoraPlan {
 LoraPlan lora_plan(int64_t T, int64_t m, int64_t d, int64_t g, int rank)
 {
     LoraPlan p{};
-    p.tc = T > LORA_SWEEP && g % 64 == 0;
+    p.tc = lora_tc(T, g);
     p.at_xp = align_up(size_t(T) * rank * 4 * (p.tc ? LORA_TC_PARTS : 1), 256);
     p.at_part = p.at_xp + align_up(size_t(T) * d * 2, 1024);
     if (p.tc) {
         p.wq = wq_plan(T, m, d, g, LORA_SMS);
         p.slices = p.wq.ksplit;
-        p.bytes = p.at_part + (p.slices > 1 ? align_up(size_t(p.slices) * T * m * 4, 256) : 0);
         return p;
     }
-    p.nt = T > W4_COLS ? 2 : 1;
-    p.chunk = int(std::min<int64_t>(T, W4_COLS * p.nt));
+    const LoraChunk c = lora_chunk(T, d);
+    p.nt = c.nt;
+    p.chunk = c.rows;
     p.chunks = int((T + p.chunk - 1) / p.chunk);
     p.groups = int((m + LORA_ROWS - 1) / LORA_ROWS);
-    const int so = int(d / W4_STEP), room = (p.nt == 1 ? 72 : 56) * 1024;
-    const int most = std::min(so, room / (256 * p.chunk + 128 * p.nt));
+    const int so = int(d / W4_STEP);
     double best = 1e300;
-    for (int s = (so + most - 1) / most; s <= std::min(so, 64); ++s) {
+    for (int s = c.slices; s <= c.most; ++s) {
         const int steps = (so + s - 1) / s;
         const int64_t rounds = ((int64_t(p.chunks) * s * p.groups) + LORA_SMS - 1) / LORA_SMS;
         const double cost = double(rounds) * (((steps + LORA_KW - 1) / LORA_KW) * (p.nt == 1 ? 190 : 260) + 150);
         if (cost < best * 0.97) { best = cost; p.slice = steps; }
     }
     p.slices = (so + p.slice - 1) / p.slice;
-    p.bytes = p.at_part + (p.slices > 1 ? align_up(size_t(p.slices) * T * m * 4, 256) : 0);
     return p;
+}
+
+// Bytes that serve T rows and every smaller batch: each part's largest.  The tcgen05
+// product splits K into more parts where its tiles are few, a tile more per 128 rows.
+size_t lora_bytes(int64_t T, int64_t m, int64_t d, int64_t g, int rank)
+{
+    const bool tc = lora_tc(T, g);
+    const size_t front = align_up(size_t(T) * rank * 4 * (tc ? LORA_TC_PARTS : 1), 256) +
+                         align_up(size_t(T) * d * 2, 1024);
+    int64_t rows = 0;                            // of partial results: slices x rows of x
+    auto add = [&](int64_t slices, int64_t n) { if (slices > 1) rows = std::max(rows, slices * n); };
+    const int64_t sweep = tc ? LORA_SWEEP : T;
+    add(lora_chunk(sweep, d).most, sweep);
+    if (tc)
+        for (int64_t n = std::min<int64_t>(T, 128);; n = std::min(T, n + 128)) {
+            const WqPlan wq = wq_plan(n, m, d, g, LORA_SMS);
+            add(wq.ksplit, n);
+            if (n == T || int64_t(wq.n_rt) * wq.n_nt >= 2 * LORA_SMS) break;   // (no splits from here on)
+        }
+    return front + align_up(size_t(rows) * m * 4, 256);
 }
 
 }  // namespace gptq
@@ -499,7 +537,7 @@ extern "C" size_t gptq_w4a16_lora_workspace_bytes(int64_t batch, int64_t d_out, 
         d_in > kMaxDim || d_in % 128 != 0 || g < 32 || g % 32 != 0 || d_in % g != 0 || rank <= 0 ||
         rank > LORA_MAX_RANK)
         return 0;
-    return lora_plan(batch, d_out, d_in, g, rank).bytes;
+    return lora_bytes(batch, d_out, d_in, g, rank);
 }
 
 extern "C" int gptq_w4a16_lora(const uint16_t* x, int64_t batch, const uint32_t* qweight,
@@ -524,8 +562,8 @@ extern "C" int gptq_w4a16_lora(const uint16_t* x, int64_t batch, const uint32_t*
         !aligned16(y) || !aligned16(ws) || !aligned16(perm) || !aligned16(lora_a) ||
         !aligned16(lora_b) || !aligned(lora_scaling, 4) || !aligned(adapter, 4))
         return GPTQ_ERR_INVALID_ARG;
+    if (ws_bytes < lora_bytes(batch, d_out, d_in, g, rank)) return GPTQ_ERR_INVALID_ARG;
     const LoraPlan plan = lora_plan(batch, d_out, d_in, g, rank);
-    if (ws_bytes < plan.bytes) return GPTQ_ERR_INVALID_ARG;
     LoraParams p{};
     p.x = reinterpret_cast<const __half*>(x);
     p.perm = perm;

@@ -380,8 +380,8 @@ WqPlan wq_plan(int64_t batch, int64_t m, int64_t d, int64_t gsz, int sms)
     int ks = 1;
     if (tiles < 2 * sms) {
         double best = 1e300;
-        for (int k = 1; k <= nch; ++k) {
-            const int64_t cps = ceil_div(nch, k);
+        // (chunks of a split, cps: those that k = 1 .. nch splits come to)
+        for (int64_t cps = nch; cps >= 1; cps = cps > 1 ? ceil_div(nch, ceil_div(nch, cps - 1)) : 0) {
             const int64_t kk = ceil_div(nch, cps);
             const double cost =
                 double(ceil_div(tiles * kk, sms)) * double(cps * (p.chunk / WQ_K) + 8);

@@ -1,0 +1,19 @@
+"""One workspace, made for a program's largest call, behind its smaller ones."""
+import numpy as np
+import pytest
+import torch
+
+from post_weight_quantization_11_b200 import gptq as G
+from tests import decode_ref as R
+from tests.test_w4a16_lora_gpu import DEV, _case, _run
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("m,d,g,r,act", [(900, 2048, 128, 16, True), (300, 1536, 32, 8, False), (64, 8192, 64, 24, False)])
+def test_adapters_of_smaller_batches_in_the_largest_ones_workspace(m, d, g, r, act):
+    ws = torch.empty(G.gptq_w4a16_lora_workspace_bytes(256, m, d, g, r), dtype=torch.uint8, device=DEV)
+    for T in (256, 129, 128, 40, 17, 16, 9, 8, 3, 1):
+        c = _case(T + d, T, m, d, g, r, 3, act, exact=True)
+        ws.fill_(255)
+        assert np.array_equal(_run(*c, ws=ws).cpu().numpy().astype(np.float64), R.lora(*c)[0])

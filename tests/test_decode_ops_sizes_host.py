@@ -1,0 +1,31 @@
+"""Workspace sizes of the decode-step calls (no GPU): a buffer for the largest call of a
+program serves its smaller ones."""
+import pytest
+
+from post_weight_quantization_11_b200 import build
+from post_weight_quantization_11_b200 import gptq as G
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    build.build()
+    G.load_library()
+
+
+@pytest.mark.parametrize("m,d,g,r", [
+    (14336, 4096, 128, 16), (4096, 4096, 128, 16), (4096, 11008, 64, 64), (4096, 14336, -1, 8), (4096, 4096, 32, 16),
+    (6144, 4096, 64, 256), (1024, 8192, 128, 32), (64, 256, 128, 8), (1, 32768, 64, 8), (300, 32768, 32, 16),
+    (50000, 384, 96, 8), (2560, 5120, 128, 16), (19000, 128, 64, 40)])
+def test_the_adapters_workspace_grows_with_the_batch(m, d, g, r):
+    last = 0
+    for T in [*range(1, 700), *range(700, 6000, 97), 20000, 40000, 65535]:
+        now = G.gptq_w4a16_lora_workspace_bytes(T, m, d, g, r)
+        assert now >= last, (T, last, now)
+        last = now
+
+
+@pytest.mark.parametrize("m,d,g,r,most", [(14336, 4096, 128, 16, 4.2e6), (4096, 4096, 128, 16, 1.3e6),
+                                          (4096, 11008, 64, 64, 3.5e6)])
+def test_the_adapters_workspace_stays_small(m, d, g, r, most):
+    """16 rows: their partial results at the slices that a plan may have, no more."""
+    assert G.gptq_w4a16_lora_workspace_bytes(16, m, d, g, r) <= most
