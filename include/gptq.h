@@ -469,8 +469,8 @@ int gptq_w4a16_lora(const uint16_t* x, int64_t batch, const uint32_t* qweight,
  *    32768.
  * 0 <= tokens <= 64 (0: no-op), 1 <= n_experts <= 256, 1 <= top_k <=
  * min(8, n_experts).
- * ws: gptq_w4a16_moe_workspace_bytes(...) bytes, not shared with a call that
- *    may run at the same time.
+ * ws: gptq_w4a16_moe_workspace_bytes(...) bytes, which serve fewer tokens too;
+ *    not shared with a call that may run at the same time.
  * h stays in fp32 between the products; all sums are fp32 and the result does
  * not depend on timing (no atomics on y).
  */

@@ -318,7 +318,9 @@ MoePlan moe_plan(int64_t T, int64_t E, int k, int64_t d, int64_t f)
     const int most = std::min(so, MOST / (512 * m.chunk + 128));
     const int64_t chunks = std::max(std::min(T * k, E), ceil_div(T * k, m.chunk));
     double best = 1e300;
-    for (int s = (so + most - 1) / most; s <= std::min(so, 32); ++s) {
+    const int fewest = (so + most - 1) / most;             // (slices under 2 KW steps gain nothing)
+    const int top = std::max(fewest, (so + 2 * MOE_OUT_KW - 1) / (2 * MOE_OUT_KW));
+    for (int s = fewest; s <= top; ++s) {
         const int steps = (so + s - 1) / s;
         const int64_t rounds = ceil_div(chunks * s * (d / MOE_OUT_ROWS), kMoeSms);
         const double cost = double(rounds) * (((steps + 2 * MOE_OUT_KW - 1) / (2 * MOE_OUT_KW)) * 2 * 190 + 100);
@@ -330,7 +332,8 @@ MoePlan moe_plan(int64_t T, int64_t E, int k, int64_t d, int64_t f)
     const size_t pairs = size_t(T) * k;
     m.at_h = align_up(sizeof(MoeRoutes), 256);
     m.at_part = m.at_h + align_up(pairs * f * 4, 256);
-    m.bytes = m.at_part + align_up(size_t(m.slices) * pairs * d * 4, 256);
+    // the most slices that a plan may have: a workspace that serves fewer tokens too
+    m.bytes = m.at_part + align_up(size_t(top) * pairs * d * 4, 256);
     return m;
 }
 

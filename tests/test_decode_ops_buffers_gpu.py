@@ -5,6 +5,7 @@ import torch
 
 from post_weight_quantization_11_b200 import gptq as G
 from tests import decode_ref as R
+from tests import test_w4a16_moe_gpu as M
 from tests.test_w4a16_lora_gpu import DEV, _case, _run
 
 pytestmark = pytest.mark.gpu
@@ -17,3 +18,14 @@ def test_adapters_of_smaller_batches_in_the_largest_ones_workspace(m, d, g, r, a
         c = _case(T + d, T, m, d, g, r, 3, act, exact=True)
         ws.fill_(255)
         assert np.array_equal(_run(*c, ws=ws).cpu().numpy().astype(np.float64), R.lora(*c)[0])
+
+
+def test_experts_of_fewer_tokens_in_the_largest_calls_workspace():
+    E, k, d, f, g = 12, 3, 512, 1408, 64
+    ws = torch.empty(G.gptq_w4a16_moe_workspace_bytes(64, E, k, d, f), dtype=torch.uint8, device=DEV)
+    for T in (64, 33, 9, 7, 6, 5, 2, 1):
+        c = M._case(T, T, E, k, d, f, g, T == 7)
+        ws.fill_(255)
+        y = M._run(*c, ws=ws).cpu().numpy()
+        ref, bound = R.moe(*c)
+        assert (np.abs(y - ref) <= bound).all()

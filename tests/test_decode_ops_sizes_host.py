@@ -29,3 +29,10 @@ def test_the_adapters_workspace_grows_with_the_batch(m, d, g, r):
 def test_the_adapters_workspace_stays_small(m, d, g, r, most):
     """16 rows: their partial results at the slices that a plan may have, no more."""
     assert G.gptq_w4a16_lora_workspace_bytes(16, m, d, g, r) <= most
+
+
+@pytest.mark.parametrize("E,k,d,f", [(8, 2, 4096, 14336), (32, 4, 2048, 1408), (64, 8, 2048, 1408), (256, 8, 7168, 2048),
+                                     (1, 1, 128, 128), (4, 1, 20480, 32768), (16, 3, 5120, 8192), (2, 2, 640, 32768)])
+def test_the_experts_workspace_grows_with_the_tokens(E, k, d, f):
+    sizes = [G.gptq_w4a16_moe_workspace_bytes(T, E, k, d, f) for T in range(1, 65)]
+    assert sizes == sorted(sizes)
