@@ -49,6 +49,7 @@ constexpr float KV_LAZY = 7.f;
 constexpr float KV_NONE = -3e38f;          // the maximum of no scores: finite, so that no difference is NaN
 constexpr int KV_CLUSTER = 1024;           // most keys of a cluster's chunk
 constexpr int KV_ALONE = 256;              // up to so many keys: one chunk, no second kernel
+constexpr int KV_TILES = 65535;            // most key heads times row tiles of a call (grid rows)
 
 struct KvAttn {
     const __half* q;
@@ -662,12 +663,12 @@ template <int D> __global__ void __launch_bounds__(256) kv4_join_kernel(const Kv
 // SM eight CTAs (two rounds of four) when every sequence has the bound's length; twelve
 // from 8 sequences on, whose lengths may differ (32 ragged ones: 54 us with twelve or
 // sixteen, 58 with eight, 56 with twenty-four; two of 131000: 82 us with eight, 85 with six)
-struct KvPlan { int chunk, splits, row_tiles; bool cluster; size_t bytes; };
+struct KvPlan { int chunk, splits; int64_t row_tiles; bool cluster; size_t bytes; };
 
 KvPlan kv_plan(int64_t seqs, int hq, int hkv, int D, int64_t max_q, int64_t max_len, int64_t window)
 {
     KvPlan k{};
-    k.row_tiles = int((max_q * (hq / hkv) + 7) / 8);
+    k.row_tiles = std::min<int64_t>((max_q * (hq / hkv) + 7) / 8, KV_TILES / hkv + 1);
     int64_t span = max_len;
     if (window > 0) span = std::min(span, window + max_q + 2 * KV_TILE);
     span = std::max<int64_t>(span, 1);
@@ -693,10 +694,12 @@ KvPlan kv_plan(int64_t seqs, int hq, int hkv, int D, int64_t max_q, int64_t max_
     k.splits = int((span + k.chunk - 1) / k.chunk);
     k.cluster = k.cluster && k.splits > 1;
     // None where the chunks are joined in a cluster or there is one: so is every smaller
-    // call then.  Otherwise splits <= ceil(aim / units) by the choice of chunk; this bound
-    // grows with every argument, so a workspace for the bounds serves every smaller call.
+    // call then.  Otherwise units splits < units + aim by the choice of chunk, and one chunk
+    // from units = aim on; this bound grows with every argument, so a workspace for the
+    // bounds serves every smaller call.
     if (k.cluster || span <= KV_ALONE) return k;
-    const int64_t parts = std::min(units * ((max_len + ROUND - 1) / ROUND + 1), units + 148 * 12);
+    const int64_t parts = std::min(units * ((max_len + ROUND - 1) / ROUND + 1),
+                                   std::min<int64_t>(units, 148 * 12) + 148 * 12);
     k.bytes = align_up(size_t(parts) * 8 * (D + 2) * 4, 256);
     return k;
 }
@@ -758,7 +761,7 @@ extern "C" int gptq_kv4_attention(const uint16_t* q, int64_t tokens, int64_t seq
     const int64_t max_q = std::min(max_q_len, tokens);
     const KvPlan plan = kv_plan(seqs, q_heads, kv_heads, head_dim, max_q, max_seq_len, window);
     if (plan.bytes > ws_bytes || (plan.bytes && !ws)) return GPTQ_ERR_INVALID_ARG;
-    if (int64_t(kv_heads) * plan.row_tiles > 65535) return GPTQ_ERR_SHAPE;
+    if (kv_heads * plan.row_tiles > KV_TILES) return GPTQ_ERR_SHAPE;
     KvAttn p{};
     p.q = reinterpret_cast<const __half*>(q);
     p.tokens = tokens; p.seqs = seqs; p.pages = pages; p.width = table_width;
@@ -772,7 +775,7 @@ extern "C" int gptq_kv4_attention(const uint16_t* q, int64_t tokens, int64_t seq
     p.table = block_table; p.lens = seq_lens; p.start = q_start;
     p.scale = scale * 1.4426950408889634f;
     p.cluster = plan.cluster;
-    p.chunk = plan.chunk; p.splits = plan.splits; p.row_tiles = plan.row_tiles;
+    p.chunk = plan.chunk; p.splits = plan.splits; p.row_tiles = (int)plan.row_tiles;
     p.part = static_cast<float*>(ws);
     p.out = reinterpret_cast<__half*>(out);
     cudaStream_t st = as_stream(stream);

@@ -36,3 +36,19 @@ def test_the_adapters_workspace_stays_small(m, d, g, r, most):
 def test_the_experts_workspace_grows_with_the_tokens(E, k, d, f):
     sizes = [G.gptq_w4a16_moe_workspace_bytes(T, E, k, d, f) for T in range(1, 65)]
     assert sizes == sorted(sizes)
+
+
+@pytest.mark.parametrize("hq,hkv,D", [(32, 8, 128), (1024, 1, 64), (8, 8, 256), (21, 3, 64)])
+@pytest.mark.parametrize("B", [1, 7, 8, 64, 65535])
+def test_the_attentions_workspace_grows_and_stays_small(B, hq, hkv, D):
+    """In queries and keys: never past the partial results of the most chunks that a
+    launch is cut into (a prompt needs none of its own), 2 x 12 CTAs an SM of 148, eight
+    rows each."""
+    W = G.gptq_kv4_attention_workspace_bytes
+    most = 2 * 12 * 148 * 8 * (D + 2) * 4 + 256
+    for L in (1, 256, 257, 777, 9000, 131000, 1 << 30):
+        sizes = [W(B, hq, hkv, D, n, L) for n in (1, 2, 9, 64, 1000, 8192, 100000, 1 << 24)]
+        assert sizes == sorted(sizes) and sizes[-1] <= most, (L, sizes)
+    for n in (1, 64, 8192, 1 << 24):
+        sizes = [W(B, hq, hkv, D, n, L) for L in (1, 256, 257, 777, 9000, 131000, 1 << 30)]
+        assert sizes == sorted(sizes), (n, sizes)

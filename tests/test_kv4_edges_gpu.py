@@ -1,8 +1,10 @@
 """gptq_kv4_attention at the ends of its ranges: windows longer than the cache,
-queries that are not finite."""
+queries that are not finite, prompts."""
 import numpy as np
 import pytest
+import torch
 
+from post_weight_quantization_11_b200 import gptq as G
 from tests.test_kv4_gpu import _attn_case, _attn_check, _attn_ref, _attn_run
 
 pytestmark = pytest.mark.gpu
@@ -79,3 +81,18 @@ def test_an_infinite_query_whose_every_score_is_minus_infinity():
         c["q"][0, 0, 3], c["q"][0, 1, 3] = np.inf, -np.inf
         got = _attn_run(c, 1).cpu().numpy()
         assert np.isnan(got[0, :2]).all() and np.isfinite(got[1:]).all() and np.isfinite(got[0, 2:]).all()
+
+
+# ---- prompts ----------------------------------------------------------------
+
+@pytest.mark.parametrize("window", [0, 100])
+@pytest.mark.parametrize("lens,nqs,hq,hkv,D,page,g", [
+    ([700, 300, 64], [500, 300, 1], 4, 2, 64, 16, 32), ([9000], [65], 4, 1, 64, 64, 64),
+    ([400], [400], 3, 1, 128, 32, 128), ([260, 4000, 1], [9, 90, 1], 8, 2, 128, 16, 64), ([600], [200], 2, 2, 256, 16, 128)])
+def test_prompts_in_the_workspace_asked_for(lens, nqs, hq, hkv, D, page, g, window):
+    """Many row tiles a sequence, whose partial results stay inside the workspace."""
+    c = _attn_case(sum(lens) + 7, lens, nqs, hq, hkv, D, page, g)
+    n = G.gptq_kv4_attention_workspace_bytes(len(lens), hq, hkv, D, max(nqs), c["table"].shape[1] * page)
+    space = torch.full((n + 65536,), 90, dtype=torch.uint8, device="cuda:0")
+    _attn_check(c, window, ws=space[:n])
+    assert (space[n:] == 90).all()
