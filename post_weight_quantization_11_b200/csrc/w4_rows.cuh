@@ -545,6 +545,7 @@ static __device__ __noinline__ void w4_wait_long(uint32_t bar, uint32_t parity, 
 // starts at step k0 of the rows.  Group 0 begins at row0 (of tm and l; end: the rows
 // behind it are not read).  PAIR: a tile is 16 rows from row0 on and the 16 rows that
 // lie `pair` rows further on.
+// The scales of the rows from row0 on that it reads span less than 2^32 bytes.
 //   stage(): stages x (called after the first copies are issued; ends with a
 //            barrier);
 //   done(group, r, n, v): the joined result of row r of the group (PAIR: of the

@@ -40,6 +40,7 @@ struct LoraParams {
     int rank;
     W4Layer lay;
     int chunk, chunks, slice, slices, groups;
+    int run;           // most row groups of one sweep
     float* t;          // batch x rank (the tcgen05 product: LORA_TC_PARTS of them)
     __half* xp;        // batch x d: x in the order of the sweep or of the tcgen05 product, or null
     int tc;
@@ -191,7 +192,7 @@ lora_product_kernel(const __grid_constant__ CUtensorMap tm, const LoraParams p)
         // a run of row groups of one (chunk, slice)
         const int64_t cs = u / p.groups;
         const int g0 = int(u - cs * p.groups);
-        const int g1 = int(min(int64_t(p.groups), g0 + (u1 - u)));
+        const int g1 = int(min(int64_t(p.groups), g0 + min(u1 - u, int64_t(p.run))));
         const int c = int(cs % p.chunks), sl = int(cs / p.chunks);
         const int k0 = sl * p.slice, steps = min(p.slice, nsteps - k0);
         const int64_t b0 = int64_t(c) * p.chunk;
@@ -574,6 +575,8 @@ extern "C" int gptq_w4a16_lora(const uint16_t* x, int64_t batch, const uint32_t*
     p.lay = w4_layer(qweight, scales, qzeros, d_in, g);
     p.chunk = plan.chunk; p.chunks = plan.chunks; p.slice = plan.slice; p.slices = plan.slices;
     p.groups = plan.groups;
+    // (a sweep's offsets into the scales are 32 bits: 2^21 rows of 32768 columns in groups of 32)
+    p.run = int(std::min<int64_t>(int64_t(1) << 30, (int64_t(1) << 32) / (LORA_ROWS * 2 * p.lay.G)));
     p.t = static_cast<float*>(ws);
     p.tc = plan.tc;
     p.xp = plan.tc || perm ? reinterpret_cast<__half*>(static_cast<uint8_t*>(ws) + plan.at_xp) : nullptr;

@@ -29,3 +29,25 @@ def test_experts_of_fewer_tokens_in_the_largest_calls_workspace():
         y = M._run(*c, ws=ws).cpu().numpy()
         ref, bound = R.moe(*c)
         assert (np.abs(y - ref) <= bound).all()
+
+
+def test_adapters_of_scales_beyond_32_bits():
+    """A layer whose scales take more than 2^32 bytes, swept from its first row to its last
+    by one CTA: every code 1, x integers, a row's scales a power of two of the row modulo 5."""
+    m, d, g, T, r = 2 ** 21 + 192, 32768, 32, 113, 8
+    assert G.gptq_w4a16_lora_workspace_bytes(T, m, d, g, r) < 40e9
+    qw = torch.full((m, d // 8), 0x11111111, dtype=torch.int32, device=DEV)
+    s = 2.0 ** -(torch.arange(m, device=DEV) % 5).float()
+    sc = s.half()[:, None].expand(m, d // g).contiguous()
+    qz = torch.zeros(m, d // g // 2, dtype=torch.uint8, device=DEV)
+    gen = torch.Generator(device=DEV).manual_seed(5)
+    x = torch.randint(-2, 3, (T, d), generator=gen, device=DEV).half()
+    none = torch.full((T,), -1, dtype=torch.int32, device=DEV)
+    a = torch.zeros(1, r, d, dtype=torch.float16, device=DEV)
+    b = torch.zeros(1, m, r, dtype=torch.float16, device=DEV)
+    y = G.gptq_w4a16_lora(x, qw, sc, qz, a, b, none, torch.ones(1, device=DEV), g)
+    total = x.float().sum(1)
+    wrong = sum(int((y[t] != total[t] * s).sum()) for t in range(T))
+    del qw, sc, qz, b, y
+    torch.cuda.empty_cache()
+    assert wrong == 0
