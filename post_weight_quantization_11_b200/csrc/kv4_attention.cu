@@ -32,7 +32,7 @@
 //    then two neighbouring columns of the other product's operand, and the reads of
 //    shared memory hit every bank as often (keys) or twice (values).
 // Measured (B200, 32 heads on 8 of 128): 57 us for 32 ragged sequences of up to 8000 keys
-// (178 MB: 3.1 TB/s), 84 us for two of 131000 in groups of 64 (2.9 TB/s), 6 us for one of
+// (178 MB: 3.1 TB/s), 85 us for two of 131000 in groups of 64 (2.9 TB/s), 6.5 us for one of
 // 777; bound by about 740 instructions a tile and warp (176 unpack, 32 to 48 multiply),
 // issued in 62 % of the cycles by four warps a scheduler, and by the uneven last round of
 // chunks.
@@ -253,13 +253,16 @@ __global__ void __launch_bounds__(KV_WARPS * 32, KvShape<D, G>::CTAS) kv4_attent
                          half * keyb * 16;
     int ptile = warp, pslot = 0, pkey = c0 + warp * KV_TILE + half * 16;
     bool stray = false;                                    // a page out of range was met
+    uint32_t phase = 0;                                    // parity of the slot to read; from W4_GONE on:
+                                                           // a wait gave up, the results are void
     uint32_t page = 0;
     auto look = [&]() { page = pkey < c1 ? uint32_t(table[pkey >> p.page_shift]) : 0u; };
     auto issue = [&]() {
         if (ptile >= tiles) return;
         const bool bad = page >= uint32_t(p.pages);
-        if (__any_sync(ALL, bad)) {                        // page 0 in its place; its keys are masked
-            if (bad) page = 0u;
+        if (__any_sync(ALL, bad || phase >= W4_GONE)) {
+            if (__any_sync(ALL, phase >= W4_GONE)) { phase |= W4_GONE; ptile = tiles; return; }
+            if (bad) page = 0u;                            // page 0 in its place; its keys are masked
             if (lane == 0) atomicCAS(&g_device_status, 0, kErrIndex);
             stray = true;
         }
@@ -332,10 +335,16 @@ __global__ void __launch_bounds__(KV_WARPS * 32, KvShape<D, G>::CTAS) kv4_attent
     // finite (an infinity alone can make every score -inf, which is no key seen)
     const float start[2] = {poison[2 * t], poison[2 * t + 1]};
     int slot = 0;
-    uint32_t phase = 0;
     for (int tile = warp; tile < tiles; tile += KV_WARPS) {
         const int k0 = c0 + tile * KV_TILE;
-        if (!w4_try_wait(bar0 + slot * 8, phase)) w4_wait_long(bar0 + slot * 8, phase, &abort);
+        if (phase < W4_GONE && !w4_try_wait(bar0 + slot * 8, phase) &&
+            !w4_wait_long(bar0 + slot * 8, phase, &abort)) {   // its copies in flight, then no more
+            for (int i = 0; i < KV_RING && tile + i * KV_WARPS < tiles; ++i) {
+                const bool wrap = slot + i >= KV_RING;
+                w4_land(bar0 + (slot + i - (wrap ? KV_RING : 0)) * 8, phase ^ uint32_t(wrap));
+            }
+            phase |= W4_GONE;
+        }
         const uint8_t* base = smem + warp * (KV_RING * Sh::SLOT) + slot * Sh::SLOT;
         float sc[2][4];
 #pragma unroll

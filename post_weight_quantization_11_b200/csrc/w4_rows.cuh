@@ -484,11 +484,14 @@ __device__ __forceinline__ bool w4_elect()
     return ok != 0;
 }
 
+constexpr uint32_t W4_GONE = 2;
+
 // A warp's ring (shared addresses)
 struct W4Pipe {
     uint32_t ring, bar, red;
     uint32_t put, get;         // next slot to fill, to read
-    uint32_t phase;            // parity of the slot to read
+    uint32_t phase;            // parity of the slot to read; from W4_GONE on: a wait gave up, no more
+                               // waits and copies of this lane (the device status says so)
     int* abort;
 };
 
@@ -525,20 +528,30 @@ __device__ __forceinline__ bool w4_try_wait(uint32_t bar, uint32_t parity)
     return ok != 0;
 }
 
-// The rest of a wait that did not succeed at once: bounded like every wait of the
-// library; after it gave up the sweep goes on with what is there
-static __device__ __noinline__ void w4_wait_long(uint32_t bar, uint32_t parity, volatile int* abort)
+// The rest of a wait that did not succeed at once, bounded like every wait of the
+// library.  False: it gave up, or another wait of the CTA has
+static __device__ __noinline__ bool w4_wait_long(uint32_t bar, uint32_t parity, volatile int* abort)
 {
     const unsigned long long t0 = globaltimer_ns();
     for (unsigned i = 1; !w4_try_wait(bar, parity); ++i)
         if ((i & 63u) == 0) {
-            if (*abort) return;
+            if (*abort) return false;
             if (globaltimer_ns() - t0 > kWaitLimitNs) {
                 atomicCAS(&g_device_status, 0, kErrWaitFull);
                 *abort = 1;
-                return;
+                return false;
             }
         }
+    return true;
+}
+
+// For a copy in flight behind a wait that gave up: it should land before the CTA's shared
+// memory is released.  Bounded, too
+static __device__ __noinline__ void w4_land(uint32_t bar, uint32_t parity)
+{
+    const unsigned long long t0 = globaltimer_ns();
+    while (!w4_try_wait(bar, parity))
+        if (globaltimer_ns() - t0 > kWaitLimitNs) return;
 }
 
 // Sweeps the groups [0, groups) of RW row tiles over a slice of `steps` steps that
@@ -568,7 +581,7 @@ __device__ __forceinline__ void w4_sweep(W4Pipe& pipe, const CUtensorMap* tm, co
     int prow = int(row0) + rw * ROWS, pstep = first_step, pleft = n, tiles = n ? groups : 0;
     auto issue = [&]() {
         if (tiles == 0) return;
-        if (w4_elect()) {
+        if (w4_elect() && pipe.phase < W4_GONE) {          // (always the same lane)
             const uint32_t dst = pipe.ring + pipe.put * W4_SLOT, bar = pipe.bar + pipe.put * 8;
             asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar),
                          "r"(W4_SLOT)
@@ -634,8 +647,13 @@ __device__ __forceinline__ void w4_sweep(W4Pipe& pipe, const CUtensorMap* tm, co
         for (int c = 0; c < NT; ++c) x[c] = x0[c];
 #pragma unroll 1
         for (int j = 0; j < n; j += 2) {
-            if (!w4_try_wait(pipe.bar + pipe.get * 8, pipe.phase))
-                w4_wait_long(pipe.bar + pipe.get * 8, pipe.phase, pipe.abort);
+            if (pipe.phase < W4_GONE && !w4_try_wait(pipe.bar + pipe.get * 8, pipe.phase) &&
+                !w4_wait_long(pipe.bar + pipe.get * 8, pipe.phase, pipe.abort)) {
+                w4_land(pipe.bar + pipe.get * 8, pipe.phase);
+                if (grp + 1 < groups || j + 2 < n)
+                    w4_land(pipe.bar + (pipe.get ^ 1u) * 8, pipe.phase ^ pipe.get);
+                pipe.phase |= W4_GONE;                     // no copies behind this one and the next
+            }
             const uint32_t slot = from + pipe.get * W4_SLOT;
             auto next_params = [&](int jj) {
 #pragma unroll
