@@ -431,9 +431,11 @@ int gptq_w4a16_matmul(const uint16_t* x, int64_t batch, const uint32_t* qweight,
  *    0 <= n_adapters <= 65536 (0: lora_* may be NULL).
  * ws: gptq_w4a16_lora_workspace_bytes(...) bytes, which serve every smaller batch too; not
  *    shared with a call that may run at the same time.
- * All sums are fp32 (beyond 16 rows x A^T enters the product with B as two fp16
+ * All sums are fp32 (up to 16 rows codes and zero points are summed apart, sum c x -
+ * z sum x, with up to 6 bits fewer for the odd columns of a word; beyond, x A^T enters the product with B as two fp16
  * parts, which keep 22 bits of an element and nothing below 2^-38 of the row's
- * largest); the result does not depend on timing (no atomics on y).
+ * largest); the result does not depend on timing (no atomics on y), but the order
+ * of a row's sums, and so its last bits, may follow the number of rows.
  */
 size_t gptq_w4a16_lora_workspace_bytes(int64_t batch, int64_t d_out, int64_t d_in,
                                        int group_size, int rank);
@@ -471,8 +473,11 @@ int gptq_w4a16_lora(const uint16_t* x, int64_t batch, const uint32_t* qweight,
  * min(8, n_experts).
  * ws: gptq_w4a16_moe_workspace_bytes(...) bytes, which serve fewer tokens too;
  *    not shared with a call that may run at the same time.
- * h stays in fp32 between the products; all sums are fp32 and the result does
- * not depend on timing (no atomics on y).
+ * h stays in fp32 between the products and enters the second as two fp16 parts,
+ * 22 bits of its largest elements and nothing below 2^-38 of the largest.  Codes
+ * and zero points are summed apart, sum c x - z sum x: sums are fp32, of that
+ * magnitude, with up to 6 bits fewer for the odd columns of a word.  The result does not depend on timing (no atomics on y); the order
+ * of a token's sums, and so its last bits, may follow the batch it is in.
  */
 size_t gptq_w4a16_moe_workspace_bytes(int64_t tokens, int64_t n_experts, int top_k,
                                       int64_t d_model, int64_t d_ff);
