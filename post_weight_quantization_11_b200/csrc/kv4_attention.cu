@@ -33,8 +33,8 @@
 //    shared memory hit every bank as often (keys) or twice (values).
 // Measured (B200, 32 heads on 8 of 128): 57 us for 32 ragged sequences of up to 8000 keys
 // (178 MB: 3.1 TB/s), 85 us for two of 131000 in groups of 64 (2.9 TB/s), 6.5 us for one of
-// 777; bound by about 740 instructions a tile and warp (176 unpack, 32 to 48 multiply),
-// issued in 62 % of the cycles by four warps a scheduler, and by the uneven last round of
+// 777; bound by about 810 instructions a tile and warp (240 unpack, 32 to 48 multiply),
+// issued in 63 % of the cycles by four warps a scheduler, and by the uneven last round of
 // chunks.
 #include <cmath>
 
@@ -670,8 +670,10 @@ template <int D> __global__ void __launch_bounds__(256) kv4_join_kernel(const Kv
 
 // Keys per chunk: a multiple of a CTA's round of tiles, and as few chunks as give each
 // SM eight CTAs (two rounds of four) when every sequence has the bound's length; twelve
-// from 8 sequences on, whose lengths may differ (32 ragged ones: 54 us with twelve or
-// sixteen, 58 with eight, 56 with twenty-four; two of 131000: 82 us with eight, 85 with six)
+// from 8 sequences on, whose lengths may differ (us at six, eight, twelve, sixteen and
+// twenty-four: 12 ragged ones of up to 8000: 27, 29, 30, 30, 34; 16: 33, 36, 35, 35, 37;
+// 32: 59, 62, 57, 57, 59; 8 of 40000: 64, 63, 62, 63, 67; two of 131000: 88, 85, 98 with
+// sixteen, 111 with twenty-four; 6 of 40000: 54, 53, then 55 and 60)
 struct KvPlan { int chunk, splits; int64_t row_tiles; bool cluster; size_t bytes; };
 
 KvPlan kv_plan(int64_t seqs, int hq, int hkv, int D, int64_t max_q, int64_t max_len, int64_t window)
@@ -688,7 +690,8 @@ KvPlan kv_plan(int64_t seqs, int hq, int hkv, int D, int64_t max_q, int64_t max_
         return std::max<int64_t>(ROUND, (keys + ROUND - 1) / ROUND * ROUND);
     };
     // clusters of two to eight chunks where all of them fit the GPU at once (four CTAs an
-    // SM) with at most KV_CLUSTER keys each: one sequence of 777 keys in one launch
+    // SM; heads of 256, with two, may take two rounds) with at most KV_CLUSTER keys each: one
+    // sequence of 777 keys in one launch
     const int64_t most = std::min<int64_t>(8, 148 * 4 / std::max<int64_t>(units, 1));
     int64_t chunk = rounded((units * span + aim - 1) / aim);
     if (span <= KV_ALONE) {

@@ -476,9 +476,12 @@ bool lora_tc(int64_t T, int64_t g) { return T > LORA_SWEEP && g % 64 == 0; }
 // Slices of the columns: as few as fit, or more where few row groups would leave
 // CTAs idle.  A group costs about 190 instructions a step and warp (two operands:
 // 260, bound by the matrix pipe) and 150 to join, and the slowest CTA counts.
-// More than 16 rows: the tcgen05 product, which needs groups of a multiple of 64 (14336
-// x 4096, groups of 128: 31 us against 37 at 16 rows, 56 against 38 at 32, 180 against
-// 45 at 128).
+// More than 16 rows: the tcgen05 product, which needs groups of a multiple of 64.  Whole
+// calls, the sweep against that product: 14336 x 4096, rank 16: 36 us against 57 at 16
+// rows, 55 against 58 at 24, 60 against 58 at 32, 178 against 86 at 128; 4096 x 4096: 19
+// against 31, 25 against 31, 26 against 33, 62 against 38; 4096 x 11008, rank 64, groups of
+// 64: 52 against 61, 63 against 64, 65 against 65, 158 against 77.  (Every row with an
+// adapter of its own but for eight; the limit could be 24.)
 LoraPlan lora_plan(int64_t T, int64_t m, int64_t d, int64_t g, int rank)
 {
     LoraPlan p{};

@@ -6,13 +6,15 @@
 //
 // Three kernels, each begun while the one before it drains: routes and h, the second
 // product over slices of its columns, and the joined y.  Every CTA of the first two works
-// out the routes for itself (a warp a token; the second while the first ends: 227 us
-// against 231 with the first's routes read behind it), the products are sweeps of the
-// packed rows (w4_rows.cuh): only the experts that a token chose are read, each once per
-// eight of its tokens.  h stays fp32 between them, as two fp16 parts in the second.
-// Partial results go through memory, not atomics: their order is fixed.
+// out the routes for itself (a warp a token; the second while the first ends, 4 us of 24
+// tokens' time less than with the first's routes read behind it), the products are sweeps
+// of the packed rows (w4_rows.cuh): only the experts that a token chose are read, each once
+// per eight of its tokens (by the first product up to d_model 4096: rows of x are staged
+// whole, and six of 5120, four of 7168, one from 16384 on fit beside the ring).  h stays
+// fp32 between them, as two fp16 parts in the second.  Partial results go through memory,
+// not atomics: their order is fixed.
 // Measured (B200, 8 experts of 14336 x 4096, top 2, groups of 128): 56 us for one token
-// (two experts, 183 MB: 3.3 TB/s), 227 us for 24 (all eight, 732 MB: 3.2 TB/s; the copies
+// (two experts, 183 MB: 3.3 TB/s), 218 us for 24 (all eight, 732 MB: 3.4 TB/s; the copies
 // alone, without the products, 163); bound by the instructions that unpack (see
 // w4_rows.cuh) and, for one token, by the start and end of three kernels.
 #include <cfloat>
@@ -400,7 +402,7 @@ extern "C" int gptq_w4a16_moe(const uint16_t* x, int64_t tokens, const float* lo
     auto ctas = [&](int64_t units) { return (unsigned)std::min<int64_t>(sms, units); };
     // Four column shares (64 rows of h a group, half the joins) or eight (32 rows, finer
     // rounds): by the slowest CTA's share, at the costs in moe_plan (24 tokens of 8 experts
-    // of 14336: 227 us with four, 229 with eight; one token: 56.5 and 55.5)
+    // of 14336: 218 us with four, 221 with eight; one token: 56.7 and 56.1)
     const int64_t pairs = tokens * top_k;
     const int64_t chunks = std::max(std::min(pairs, n_experts), ceil_div(pairs, plan.chunk));
     auto cost = [&](int kw, int rows) {

@@ -271,9 +271,10 @@ w4a16_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&afull[as]);
                 }
-                // The words' slot is freed only here, where their values have been used: freed
-                // right behind their loads, the loads were moved past the arrival and read the
-                // slot's next words.
+                // The words' slot is freed only here, where their values have been used.  Freed
+                // right behind their loads, products came out with the words of a later stage
+                // in them (13 in 18, once the loop was shorter), and none has since; which step
+                // let the loads come after the arrival was not shown.
                 if (sub == WQ_WIN - 1 || s + 1 == s_end) {
                     if (lane == 0) mbar_arrive(&qempty[qs]);
                     if (++qs == WQ_QSTAGES) { qs = 0; qph ^= 1; }
