@@ -256,7 +256,11 @@ __global__ void __launch_bounds__(KV_WARPS * 32, KvShape<D, G>::CTAS) kv4_attent
     uint32_t phase = 0;                                    // parity of the slot to read; from W4_GONE on:
                                                            // a wait gave up, the results are void
     uint32_t page = 0;
-    auto look = [&]() { page = pkey < c1 ? uint32_t(table[pkey >> p.page_shift]) : 0u; };
+    // (pages of 16: a half tile in front of the first key that is seen takes page 0, its own
+    // may be freed)
+    auto look = [&]() {
+        page = pkey < c1 && (whole || pkey + 16 > sp.lo) ? uint32_t(table[pkey >> p.page_shift]) : 0u;
+    };
     auto issue = [&]() {
         if (ptile >= tiles) return;
         const bool bad = page >= uint32_t(p.pages);
@@ -407,7 +411,8 @@ __global__ void __launch_bounds__(KV_WARPS * 32, KvShape<D, G>::CTAS) kv4_attent
             if (stray)
                 for (int h = 0; h < 2; ++h) {
                     const int key = k0 + h * 16;
-                    if (key < c1 && uint32_t(table[key >> p.page_shift]) >= uint32_t(p.pages))
+                    if (key < c1 && (whole || key + 16 > sp.lo) &&
+                        uint32_t(table[key >> p.page_shift]) >= uint32_t(p.pages))
                         there &= ~(1u << h);
                 }
 #pragma unroll

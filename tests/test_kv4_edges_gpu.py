@@ -50,6 +50,25 @@ def test_a_long_window_with_more_queries_than_keys(window):
     assert np.array_equal(_run(c, window), _attn_check(c))
 
 
+@pytest.mark.parametrize("page", [16, 32, 64])
+@pytest.mark.parametrize("lens,nqs,window", [([100], [1], 20), ([1000, 90, 33], [1, 1, 1], 17), ([700], [5], 60),
+                                             ([9000], [1], 8000)])
+def test_pages_behind_the_window_are_not_read(lens, nqs, window, page):
+    """Their entries may hold anything (a program that frees the pages puts -1 there), also
+    where such a page ends inside the first tile of 32 keys."""
+    G.gptq_device_status()
+    for shift in range(0, 32, 5):
+        c = _attn_case(6, [L + shift for L in lens], nqs, 4, 2, 64, page, 32)
+        for b, (L, n) in enumerate(zip(c["lens"], nqs)):
+            first = max(0, int(L) - n + 1 - window) // page              # of the first key that is seen
+            c["table"][b, :first] = -1
+        got = _run(c, window)
+        assert G.gptq_device_status() == 0
+        c["table"][c["table"] < 0] = 0
+        want, bound = _attn_ref(c, window)
+        assert (np.abs(got - want) <= bound).all()
+
+
 # ---- queries that are not finite -------------------------------------------
 
 @pytest.mark.parametrize("value", [np.nan, np.inf, -np.inf])
