@@ -564,8 +564,9 @@ int gptq_kv4_append(const void* q, int64_t q_stride, const void* k, int64_t k_st
  * the device status (0x201) and its rows are left as they are; a page outside
  * 0 .. pages - 1 is recorded and its keys are not seen.
  * Keys enter the products as exact differences c - z, values as exact codes;
- * scores, softmax statistics and sums are fp32, probabilities two fp16 parts
- * (22 bits), out is rounded once.
+ * scores, softmax statistics and sums are fp32, probabilities times value
+ * scales two fp16 parts (22 bits, and nothing below 2^-31 of the largest value
+ * scale among the keys that a warp goes through), out is rounded once.
  * head_dim, group_size, page_size and the cache: as gptq_kv4_append; q_heads a
  * multiple of kv_heads.  seqs == 0 or tokens == 0: no-op.
  * ws: gptq_kv4_attention_workspace_bytes(...) bytes (0 for few keys: ws may then

@@ -24,7 +24,9 @@
 //  * out^T = V^T p: two keys' words of the same elements, merged half by half, give
 //    operand registers of two keys again by one AND.  A value's scale goes into its
 //    probability: u = p s, in two fp16 parts (22 bits), scaled by a power of two that
-//    follows the largest s; its zero point into sum u (z - 8), subtracted at the end
+//    follows the largest s of the warp's keys (n - 9 bits fewer for a key whose s is 2^-n
+//    of that one, n > 9: below the output's rounding up to n = 20); its zero point into
+//    sum u (z - 8), subtracted at the end
 //    from the sum over the codes c - 8.
 //  * The running maximum follows the scores in steps of KV_LAZY: p = 2^(score - m) may
 //    reach 2^KV_LAZY before the outputs are scaled again, which few tiles ask for.
